@@ -76,6 +76,20 @@ cudaError_t launch_amax_bf16(const void *x, int64_t count, unsigned int *amax, i
 cudaError_t launch_quantize_bf16_e4m3(const void *x, int64_t count, const float *scale, uint8_t *q, int grid,
                                       cudaStream_t s);
 
+// The norm and the epilogue's backward (rmsnorm.cuh, dact.cuh).  dt is DT_F16 or DT_BF16; every
+// launch is a programmatic dependent of the kernel before it when pdl is set.
+struct NormParams;
+struct NormBwdParams;
+struct DactParams;
+constexpr int NORM_MAX_D = 16384;
+// blocks of a backward launch = rows of its partial sums, from (m, d) alone
+int64_t norm_bwd_parts(int64_t m, int64_t d);
+cudaError_t launch_rmsnorm(int dt, int out, const NormParams &p, bool pdl, cudaStream_t s);
+cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStream_t s);
+// rows of a block's run, from (m, n) alone; the launch has ceil(m / rows) runs
+int64_t dact_rows(int64_t m, int64_t n);
+cudaError_t launch_dact(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s);
+
 // per-dtype halves of the lookups (one instantiation unit each)
 bool find_tc_f16(int cg, int epi, int axis, bool b_mn, int bn, TcLauncher *, KernelInfo *);
 bool find_tc_bf16(int cg, int epi, int axis, bool b_mn, int bn, TcLauncher *, KernelInfo *);

@@ -1,0 +1,296 @@
+// rmsnorm.cuh -- root-mean-square norm of the rows of a residual stream, with the
+// residual's addition before it and, for the FP8 plans that read its output, the
+// quantisation after it; and its backward pass.
+//
+// Forward, for each row i of length d (all arithmetic in fp32):
+//     s = x + r                          (r optional; s rounded once, to the 16-bit type, when stored)
+//     rho = 1 / sqrt(mean_j s_j^2 + eps)
+//     y_j = s_j rho g_j
+// y goes out in the 16-bit type, or in e4m3 as y / scale: with a scale the caller gives for the
+// whole tensor (max |y| reported), or with one scale a row, max_j |y_j| / 448 (1 for a row of
+// zeros).  The row maximum needs no second pass: max |y| = rho max |s g|, so the sum of squares
+// and the maximum are reduced together, and e4m3(y / scale) = e4m3(s g * 448 / max |s g|).
+// The norm is taken of the unrounded fp32 sum: the only roundings are the ones of S and Y.
+//
+// Backward, from dY, the stored sum S, the gain g and the gradient dS that reaches s past the norm:
+//     a = dy g,  c = mean_j(a_j s_j),
+//     dx_j = ds_j + rho (a_j - s_j rho^2 c)          (the gradient of x and of r alike)
+//     dg_j = sum_i dy_ij s_ij rho_i
+// rho is taken again from S in the pass that c needs anyway: no statistic is kept by the forward pass.
+//
+// Both are bound by HBM: a row is read once, held in registers as fp32 (forward) or packed
+// (backward), reduced, and written once.  A row is shared by TPR threads, each holding VPT
+// vectors of 8 elements (16-byte loads, neighbouring threads on neighbouring vectors).
+#pragma once
+#include <cstdint>
+
+#include "gemm_tc.cuh"
+
+namespace gemm_epi {
+
+enum : int { NORM_SAME = 0, NORM_E4M3 = 1, NORM_E4M3_ROWS = 2 };
+
+struct NormParams {
+    int64_t m;
+    int d;                   // a multiple of 8 (16 for an e4m3 output)
+    float eps, inv_d;
+    const void *x, *r;       // r may be NULL
+    const void *gamma;
+    void *s;                 // may be NULL
+    void *y;
+    float *scale;            // NORM_E4M3: one float, read; NORM_E4M3_ROWS: m floats, written
+    unsigned int *amax;      // NORM_E4M3, may be NULL: max |y| as float bits
+};
+
+struct NormBwdParams {
+    int64_t m;
+    int d;
+    float eps, inv_d;
+    const void *dy, *s, *gamma, *ds;    // ds may be NULL
+    void *dx;
+    float *partial;          // [grid][d] sums for dgamma, or NULL
+};
+
+// A 16-byte load that leaves no copy in L1: every element is used once.  (Not the read-only
+// path: S may be stored over X or R, and Y over X, by the thread that read those elements.)
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+    using O = OutT<DT>;
+    return make_uint4(O::pack(f[0], f[1]), O::pack(f[2], f[3]), O::pack(f[4], f[5]), O::pack(f[6], f[7]));
+}
+
+// Sum of `a` and combination of `b` (maximum, or sum) over the TPR threads of a row, the same
+// bits in each of them.  Rows of up to 32 threads use an xor butterfly (every lane of the warp
+// takes part, with whatever row it has); longer ones add their warps' results in warp order.
+template <int TPR, bool BMAX>
+__device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red) {
+    constexpr int W = TPR < 32 ? TPR : 32;
+#pragma unroll
+    for (int sh = W / 2; sh >= 1; sh >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, sh);
+        const float o = __shfl_xor_sync(0xffffffffu, b, sh);
+        b = BMAX ? fmaxf(b, o) : b + o;
+    }
+    if constexpr (TPR > 32) {
+        constexpr int NW = TPR / 32;
+        if ((threadIdx.x & 31) == 0) red[(threadIdx.x % TPR) >> 5] = make_float2(a, b);
+        __syncthreads();
+        float2 t = red[0];
+        a = t.x;
+        b = t.y;
+#pragma unroll
+        for (int w = 1; w < NW; ++w) {
+            t = red[w];
+            a += t.x;
+            b = BMAX ? fmaxf(b, t.y) : b + t.y;
+        }
+    }
+}
+
+constexpr int norm_threads(int tpr) { return tpr > 128 ? tpr : 128; }
+
+template <int DT, int OUT, int TPR, int VPT>
+__global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormParams p) {
+    constexpr int RPB = norm_threads(TPR) / TPR;      // rows of a block
+    __shared__ float2 red[RPB][TPR > 32 ? TPR / 32 : 1];
+    const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * RPB + grp;
+    const bool row_ok = row < p.m;
+    const int nvec = p.d / 8;
+    // launched as a dependent of the kernel before it: nothing in global memory is touched
+    // before that one has completed
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    uint4 xv[VPT], rv[VPT], gv[VPT];
+    const int64_t base = row * p.d;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * TPR + t;
+        xv[j] = rv[j] = gv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (row_ok && v < nvec) {
+            xv[j] = ld_stream(static_cast<const uint16_t *>(p.x) + base + 8 * v);
+            if (p.r != nullptr) rv[j] = ld_stream(static_cast<const uint16_t *>(p.r) + base + 8 * v);
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * TPR + t;
+        if (v < nvec) gv[j] = __ldg(static_cast<const uint4 *>(p.gamma) + v);
+    }
+    float s[VPT][8];
+    float ss = 0.0f, top = 0.0f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        unpack8<DT>(xv[j], s[j]);
+        if (p.r != nullptr) {
+            float r[8];
+            unpack8<DT>(rv[j], r);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[j][e] += r[e];
+            const int v = j * TPR + t;
+            if (p.s != nullptr && row_ok && v < nvec)
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.s) + base + 8 * v) = pack8<DT>(s[j]);
+        }
+        float g[8];
+        unpack8<DT>(gv[j], g);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            ss = fmaf(s[j][e], s[j][e], ss);
+            if constexpr (OUT != NORM_SAME) {
+                s[j][e] *= g[e];
+                top = fmaxf(top, fabsf(s[j][e]));
+            }
+        }
+    }
+    row_reduce<TPR, true>(ss, top, red[grp]);
+    const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+    float mul = rho;
+    if constexpr (OUT == NORM_E4M3) {
+        mul = rho / __ldg(p.scale);
+        if (p.amax != nullptr && t == 0 && row_ok) {
+            // most rows are below the maximum so far: they only read it
+            const unsigned int a = __float_as_uint(rho * top);
+            if (a > *reinterpret_cast<volatile unsigned int *>(p.amax)) atomicMax(p.amax, a);
+        }
+    } else if constexpr (OUT == NORM_E4M3_ROWS) {
+        // 448 / top overflows below 1.4e-36; such a row is one of zeros in e4m3 at any scale in use
+        const bool zero = !(top > 1e-35f);
+        mul = zero ? rho : 448.0f / top;
+        if (t == 0 && row_ok) p.scale[row] = zero ? 1.0f : rho * top * (1.0f / 448.0f);
+    }
+    if (!row_ok) return;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * TPR + t;
+        if (v >= nvec) continue;
+        if constexpr (OUT == NORM_SAME) {
+            float g[8];
+            unpack8<DT>(gv[j], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[j][e] = s[j][e] * mul * g[e];
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + base + 8 * v) = pack8<DT>(s[j]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = __nv_cvt_float2_to_fp8x2(make_float2(s[j][2 * e] * mul, s[j][2 * e + 1] * mul), __NV_SATFINITE,
+                                                __NV_E4M3);
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + base + 8 * v) =
+                make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+        }
+    }
+}
+
+// Rows are dealt to the blocks' groups round-robin; each thread keeps the gain's gradient of
+// its columns in registers over its rows, and the block writes one partial row of d floats,
+// its groups added in order.  Which rows a partial holds depends on (m, d) alone, so dgamma is
+// the same from run to run.
+template <int DT, int TPR, int VPT>
+__global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_bwd_kernel(const NormBwdParams p) {
+    constexpr int RPB = norm_threads(TPR) / TPR;
+    __shared__ float2 red[2][RPB][TPR > 32 ? TPR / 32 : 1];
+    __shared__ float col[RPB > 1 ? TPR * VPT * 8 : 1];
+    const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
+    const int nvec = p.d / 8;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+
+    uint4 gv[VPT];
+    float acc[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * TPR + t;
+        gv[j] = v < nvec ? __ldg(static_cast<const uint4 *>(p.gamma) + v) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
+    }
+    int buf = 0;
+    // (every group of a block makes the same number of turns: the reductions are block-wide)
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.m; row0 += (int64_t)gridDim.x * RPB, buf ^= 1) {
+        const int64_t row = row0 + grp;
+        const bool row_ok = row < p.m;
+        const int64_t base = row * p.d;
+        uint4 yv[VPT], sv[VPT], dv[VPT];
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * TPR + t;
+            yv[j] = sv[j] = dv[j] = make_uint4(0u, 0u, 0u, 0u);
+            if (row_ok && v < nvec) {
+                yv[j] = ld_stream(static_cast<const uint16_t *>(p.dy) + base + 8 * v);
+                sv[j] = ld_stream(static_cast<const uint16_t *>(p.s) + base + 8 * v);
+                if (p.ds != nullptr) dv[j] = ld_stream(static_cast<const uint16_t *>(p.ds) + base + 8 * v);
+            }
+        }
+        float ss = 0.0f, c = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            float y[8], s[8], g[8];
+            unpack8<DT>(yv[j], y);
+            unpack8<DT>(sv[j], s);
+            unpack8<DT>(gv[j], g);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                ss = fmaf(s[e], s[e], ss);
+                c = fmaf(y[e] * g[e], s[e], c);
+            }
+        }
+        row_reduce<TPR, false>(ss, c, red[buf][grp]);
+        const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        const float k = rho * rho * (c * p.inv_d);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * TPR + t;
+            float y[8], s[8], g[8], o[8];
+            unpack8<DT>(yv[j], y);
+            unpack8<DT>(sv[j], s);
+            unpack8<DT>(gv[j], g);
+            unpack8<DT>(dv[j], o);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                acc[j][e] = fmaf(y[e] * rho, s[e], acc[j][e]);
+                o[e] = fmaf(rho, fmaf(-s[e], k, y[e] * g[e]), o[e]);
+            }
+            if (row_ok && v < nvec)
+                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dx) + base + 8 * v) = pack8<DT>(o);
+        }
+    }
+    if (p.partial == nullptr) return;
+    float *out = p.partial + (int64_t)blockIdx.x * p.d;
+    if constexpr (RPB > 1) {
+        for (int g = 0; g < RPB; ++g) {
+            if (g == grp) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float &c = col[(j * TPR + t) * 8 + e];
+                        c = g == 0 ? acc[j][e] : c + acc[j][e];
+                    }
+            }
+            __syncthreads();
+        }
+        for (int i = threadIdx.x; i < p.d; i += norm_threads(TPR)) out[i] = col[i];
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * TPR + t;
+            if (v < nvec) {
+                float4 *o = reinterpret_cast<float4 *>(out + 8 * v);
+                o[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                o[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+            }
+        }
+    }
+}
+
+}  // namespace gemm_epi

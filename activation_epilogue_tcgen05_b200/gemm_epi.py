@@ -40,6 +40,8 @@ AXIS = {"row": BIAS_ROW, "col": BIAS_COL}
 LAYOUT = {"kn": B_KN, "nk": B_NK}
 KERNEL = {"auto": KERNEL_AUTO, "tc1": KERNEL_TC1, "tc2": KERNEL_TC2, "splitk": KERNEL_SPLITK}
 STREAM_K = {"auto": 0, "off": 1, "on": 2}
+NORM_SAME, NORM_E4M3, NORM_E4M3_ROWS = 0, 1, 2
+NORM_OUT = {"same": NORM_SAME, "e4m3": NORM_E4M3, "e4m3_rows": NORM_E4M3_ROWS}
 
 # every symbol include/gemm_epi.h declares
 EXPORTS = ("gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts", "gemm_epi_set_scales",
@@ -48,7 +50,8 @@ EXPORTS = ("gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts", "gemm_epi_
            "gemm_epi_version", "gemm_epi_run_noalloc", "gemm_epi_run_bwd", "gemm_epi_unfused_run_bwd",
            "gemm_epi_set_out_scale", "gemm_epi_mlp_plan", "gemm_epi_mlp_set_scales", "gemm_epi_mlp_run",
            "gemm_epi_mlp_check", "gemm_epi_mlp_query", "gemm_epi_mlp_free", "gemm_epi_mlp_unfused_run",
-           "gemm_epi_plan_preview")
+           "gemm_epi_plan_preview", "gemm_epi_rmsnorm", "gemm_epi_rmsnorm_workspace_bytes",
+           "gemm_epi_rmsnorm_bwd", "gemm_epi_dact_workspace_bytes", "gemm_epi_dact")
 
 
 class Options(ctypes.Structure):
@@ -118,7 +121,15 @@ def lib():
             L.gemm_epi_version.argtypes = []
             L.gemm_epi_run_noalloc.argtypes = [i64, i64, i64, i32, i32, i32, i32, vp, vp, vp, vp,
                                                vp, vp, vp, i32, vp]
-            for name in ("gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts",
+            L.gemm_epi_rmsnorm.argtypes = [i64, i64, i32, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.gemm_epi_rmsnorm_bwd.argtypes = [i64, i64, i32, ctypes.c_float, vp, vp, vp, vp, vp, vp, vp, vp]
+            L.gemm_epi_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+            L.gemm_epi_rmsnorm_workspace_bytes.restype = i64
+            L.gemm_epi_dact.argtypes = [i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
+            L.gemm_epi_dact_workspace_bytes.argtypes = [i64, i64, i32]
+            L.gemm_epi_dact_workspace_bytes.restype = i64
+            for name in ("gemm_epi_rmsnorm", "gemm_epi_rmsnorm_bwd", "gemm_epi_dact",
+                         "gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts",
                          "gemm_epi_set_scales", "gemm_epi_run", "gemm_epi_unfused_run",
                          "gemm_epi_check", "gemm_epi_plan_query", "gemm_epi_free",
                          "gemm_epi_version", "gemm_epi_run_noalloc", "gemm_epi_run_bwd",
@@ -266,6 +277,29 @@ def gemm_epi_run_noalloc(m, n, k, dtype, epilogue, bias_axis, b_layout, A, B, bi
            "gemm_epi_run_noalloc")
 
 
+def gemm_epi_rmsnorm(m, d, dtype, out_mode, eps, X, R, gamma, S, Y, d_scale, d_amax, stream) -> None:
+    _check(lib().gemm_epi_rmsnorm(m, d, dtype, out_mode, eps, X, R, gamma, S, Y, d_scale, d_amax, stream),
+           "gemm_epi_rmsnorm")
+
+
+def gemm_epi_rmsnorm_workspace_bytes(m: int, d: int) -> int:
+    return lib().gemm_epi_rmsnorm_workspace_bytes(m, d)
+
+
+def gemm_epi_rmsnorm_bwd(m, d, dtype, eps, dY, S, gamma, dS, dX, dgamma, workspace, stream) -> None:
+    _check(lib().gemm_epi_rmsnorm_bwd(m, d, dtype, eps, dY, S, gamma, dS, dX, dgamma, workspace, stream),
+           "gemm_epi_rmsnorm_bwd")
+
+
+def gemm_epi_dact_workspace_bytes(m: int, n: int, bias_axis: int) -> int:
+    return lib().gemm_epi_dact_workspace_bytes(m, n, bias_axis)
+
+
+def gemm_epi_dact(m, n, dtype, epilogue, bias_axis, dD, Z, aux, dZ, dbias, workspace, stream) -> None:
+    _check(lib().gemm_epi_dact(m, n, dtype, epilogue, bias_axis, dD, Z, aux, dZ, dbias, workspace, stream),
+           "gemm_epi_dact")
+
+
 def status_string(status: int) -> str:
     try:
         return gemm_epi_status_string(status)
@@ -406,3 +440,122 @@ class MlpPlan:
             self.close()
         except Exception:
             pass
+
+
+def _operand(t, name, dtype, count, device, optional=False):
+    """Device address of a tensor that has to be ``count`` dense values of ``dtype`` on the
+    current device (None for an optional one left out)."""
+    if t is None:
+        if optional:
+            return None
+        raise GemmEpiError(ERR_NULL, name)
+    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous() or t.get_device() != device:
+        raise GemmEpiError(ERR_ARG, f"{name}: wanted {count} contiguous {dtype} values on cuda:{device}, got "
+                                    f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
+    return t.data_ptr()
+
+
+def _device_and_stream(stream):
+    """(current device index, raw stream): the device's current stream when none is given."""
+    import torch
+    device = torch.cuda.current_device()
+    if stream is None:
+        return device, torch.cuda.current_stream(device).cuda_stream
+    return device, getattr(stream, "cuda_stream", stream)
+
+
+def _scratch(nbytes, device, stream):
+    """Scratch of one call.  Memory that is handed out to the stream that uses it may be given
+    back as soon as the call is enqueued; a stream that is not the current one is made the
+    current one for the allocation."""
+    import torch
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "value", stream) or 0), device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
+class RmsNorm:
+    """Root-mean-square norm of (m, d) rows with the residual's addition before it, and its backward
+    (gemm_epi_rmsnorm, gemm_epi_rmsnorm_bwd).  ``dtype``: "f16" or "bf16"; ``out``: "same", "e4m3" (a given
+    scale) or "e4m3_rows" (one scale a row, written).  The object holds sizes only."""
+
+    def __init__(self, m, d, dtype="bf16", out="same", eps=1e-6):
+        import torch
+        self.m, self.d, self.dtype, self.out, self.eps = int(m), int(d), dtype, out, float(eps)
+        if dtype not in ("f16", "bf16"):
+            raise GemmEpiError(ERR_ARG, f"RmsNorm: dtype {dtype!r}")
+        self._t = torch.float16 if dtype == "f16" else torch.bfloat16
+        self._dt, self._mode = DTYPE[dtype], NORM_OUT[out]
+        self._out_t = self._t if out == "same" else torch.float8_e4m3fn
+        self._f32 = torch.float32
+        self._scales = self.m if out == "e4m3_rows" else 1
+
+    def run(self, X, gamma, Y, residual=None, S=None, scale=None, amax=None, stream=None):
+        """S = X + residual (X without one), Y = S / rms(S) * gamma; ``scale`` and ``amax`` as in
+        include/gemm_epi.h.  S or Y may be X or residual."""
+        dev, s = _device_and_stream(stream)
+        n, t = self.m * self.d, self._t
+        gemm_epi_rmsnorm(self.m, self.d, self._dt, self._mode, self.eps, _operand(X, "RmsNorm.run: X", t, n, dev),
+                         _operand(residual, "RmsNorm.run: residual", t, n, dev, True),
+                         _operand(gamma, "RmsNorm.run: gamma", t, self.d, dev),
+                         _operand(S, "RmsNorm.run: S", t, n, dev, True),
+                         _operand(Y, "RmsNorm.run: Y", self._out_t, n, dev),
+                         _operand(scale, "RmsNorm.run: scale", self._f32, self._scales, dev, True),
+                         _operand(amax, "RmsNorm.run: amax", self._f32, 1, dev, True), s)
+
+    def run_bwd(self, dY, S, gamma, dX, dgamma=None, dS=None, workspace=None, stream=None):
+        """dX (of X and of the residual alike) and, if given, dgamma, from the sum S of the forward run
+        (X without a residual); dS: the skip connection's gradient.  ``workspace``: a uint8 tensor of
+        gemm_epi_rmsnorm_workspace_bytes(m, d) bytes, taken from torch's allocator when left out."""
+        dev, s = _device_and_stream(stream)
+        n, t = self.m * self.d, self._t
+        if dgamma is not None:
+            workspace = _workspace(workspace, gemm_epi_rmsnorm_workspace_bytes(self.m, self.d), "RmsNorm.run_bwd", dev, stream)
+        gemm_epi_rmsnorm_bwd(self.m, self.d, self._dt, self.eps, _operand(dY, "RmsNorm.run_bwd: dY", t, n, dev),
+                             _operand(S, "RmsNorm.run_bwd: S", t, n, dev),
+                             _operand(gamma, "RmsNorm.run_bwd: gamma", t, self.d, dev),
+                             _operand(dS, "RmsNorm.run_bwd: dS", t, n, dev, True),
+                             _operand(dX, "RmsNorm.run_bwd: dX", t, n, dev),
+                             _operand(dgamma, "RmsNorm.run_bwd: dgamma", t, self.d, dev, True),
+                             None if dgamma is None else workspace.data_ptr(), s)
+
+
+class ActBackward:
+    """Backward of a forward plan's epilogue (gemm_epi_dact): dZ = dD * act'(z) and dbias, the names as
+    for :class:`Plan`.  The object holds sizes only."""
+
+    def __init__(self, m, n, dtype="bf16", epilogue="bias", bias_axis="row"):
+        import torch
+        self.m, self.n, self.dtype, self.epilogue, self.bias_axis = int(m), int(n), dtype, epilogue, bias_axis
+        self._args = (DTYPE[dtype], EPILOGUE[epilogue], AXIS[bias_axis])
+        self._t = torch.float16 if dtype == "f16" else torch.bfloat16
+        self._i32 = torch.int32
+        self._len = self.m if bias_axis == "row" else self.n
+
+    def run(self, dD, dZ=None, z=None, aux=None, dbias=None, workspace=None, stream=None):
+        """``z``: the pre-activation (ReLU, GELU, tanh); ``aux``: the forward's packed mask as int32 words
+        (relu_aux, relu_aux_bias); dZ: left out without an activation; dbias: left out if not wanted;
+        ``workspace``: as for RmsNorm.run_bwd (gemm_epi_dact_workspace_bytes)."""
+        dev, s = _device_and_stream(stream)
+        n, t = self.m * self.n, self._t
+        if dbias is not None:
+            workspace = _workspace(workspace, gemm_epi_dact_workspace_bytes(self.m, self.n, self._args[2]), "ActBackward.run",
+                                   dev, stream)
+        gemm_epi_dact(self.m, self.n, *self._args, _operand(dD, "ActBackward.run: dD", t, n, dev),
+                      _operand(z, "ActBackward.run: z", t, n, dev, True),
+                      None if aux is None else _operand(aux, "ActBackward.run: aux", self._i32,
+                                                        self.m * aux_pitch_words(self.n), dev),
+                      _operand(dZ, "ActBackward.run: dZ", t, n, dev, True),
+                      _operand(dbias, "ActBackward.run: dbias", t, self._len, dev, True),
+                      None if dbias is None else workspace.data_ptr(), s)
+
+
+def _workspace(given, nbytes, what, device, stream):
+    if given is None:
+        return _scratch(nbytes, device, stream)
+    if given.numel() * given.element_size() < nbytes or not given.is_contiguous() or given.get_device() != device:
+        raise GemmEpiError(ERR_ARG, f"{what}: workspace of {nbytes} contiguous bytes on cuda:{device} wanted")
+    return given

@@ -381,6 +381,84 @@ int gemm_epi_mlp_query(gemm_epi_mlp_t mlp, gemm_epi_plan_info *up, gemm_epi_plan
 
 int gemm_epi_mlp_free(gemm_epi_mlp_t mlp);
 
+/* ---- the norm before the products, and the backward of their epilogue ------ */
+
+/* What gemm_epi_rmsnorm writes to Y. */
+enum gemm_epi_norm_out {
+    GEMM_EPI_NORM_SAME = 0,       /* y in the type of X                                             */
+    GEMM_EPI_NORM_E4M3 = 1,       /* e4m3(y / *d_scale): one scale the caller gives, as A's of a
+                                     plan (gemm_epi_set_scales)                                     */
+    GEMM_EPI_NORM_E4M3_ROWS = 2   /* e4m3(y / d_scale[i]), d_scale[i] = max_j |y_ij| / 448 (1 for a
+                                     row of zeros): one scale a row, which the call writes          */
+};
+
+/* Root-mean-square norm of the rows of a residual stream, the residual's addition before it:
+ *     s = x + r,   y_ij = s_ij * gamma_j / sqrt(mean_j s_ij^2 + eps)
+ *   m, d    rows (1 ... 2^31 - 1) and row length: a multiple of 8 (of 16 for an e4m3 Y;
+ *           ERR_ALIGN otherwise) up to 16384 (ERR_UNSUPPORTED beyond).
+ *   dtype   GEMM_EPI_F16 or GEMM_EPI_BF16: the type of X, R, gamma, S and a 16-bit Y.
+ *   eps     > 0 and finite.
+ *   X, R    (m, d) row-major, dense.  R may be NULL: s = x.
+ *   gamma   length d.
+ *   S       (m, d): s rounded to nearest even, the next residual.  May be NULL (not kept); must
+ *           be NULL without R.  S may be X or R (the stream updated in place).
+ *   Y       (m, d), in the 16-bit type or e4m3 (out_mode).  A 16-bit Y may be X or R, never S.
+ *   d_scale E4M3: DEVICE pointer to one float > 0, read.  E4M3_ROWS: DEVICE pointer to m floats,
+ *           written.  SAME: ignored.
+ *   d_amax  E4M3, may be NULL (else ignored): DEVICE pointer to one float, set to 0 on the stream
+ *           and max-reduced: max |y| before quantisation, as for gemm_epi_set_out_scale.
+ * All arithmetic is fp32, and the norm is taken of the unrounded sum; y and s are rounded to
+ * nearest even once, an e4m3 y saturates at +-448.  Inputs are finite, and a row's sum of squares
+ * stays below the largest fp32 number.  Every pointer is 16-byte aligned (d_scale and d_amax:
+ * 4-byte).  One launch (after a memset when d_amax is given), nothing allocated, any stream;
+ * calls may overlap as far as their buffers do.  Returns OK, ERR_ARG (a size, type, mode or eps
+ * out of range; S without R; buffers that may not coincide), ERR_ALIGN, ERR_NULL,
+ * ERR_UNSUPPORTED, ERR_NO_DEVICE or ERR_CUDA.  (The pages name LayerNorm among what surrounds
+ * the fused products, [nvmath-fusion] paragraph 6; they have no counterpart of this call.) */
+int gemm_epi_rmsnorm(int64_t m, int64_t d, int dtype, int out_mode, float eps, const void *X, const void *R,
+                     const void *gamma, void *S, void *Y, float *d_scale, float *d_amax, void *stream);
+
+/* Bytes of scratch that gemm_epi_rmsnorm_bwd needs for dgamma (0 for sizes it refuses). */
+int64_t gemm_epi_rmsnorm_workspace_bytes(int64_t m, int64_t d);
+
+/* Backward of gemm_epi_rmsnorm, from the sum S it stored (X itself without a residual):
+ *     a = dy * gamma,  rho_i = 1 / sqrt(mean_j s_ij^2 + eps),  c_i = mean_j(a_ij s_ij)
+ *     dx_ij = ds_ij + rho_i (a_ij - s_ij rho_i^2 c_i)      the gradient of X and of R alike
+ *     dgamma_j = sum_i dy_ij s_ij rho_i
+ *   dY      (m, d) in dtype: the gradient of y (of an e4m3 Y: of the values it stands for).
+ *   dS      (m, d): the gradient that reaches s past the norm (the skip connection's); NULL: none.
+ *   dX      (m, d), may be dY, S or dS.
+ *   dgamma  length d, in dtype, NULL: not wanted.  Summed in fp32 in an order fixed by (m, d),
+ *           rounded once.
+ *   workspace  16-byte aligned device memory of gemm_epi_rmsnorm_workspace_bytes(m, d) bytes,
+ *           needed with dgamma (else NULL).  It holds nothing between calls; calls that may run
+ *           at the same time (other streams, graphs that are replayed together) need one each.
+ * Rules, limits and statuses as for gemm_epi_rmsnorm; one launch, two with dgamma. */
+int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void *dY, const void *S,
+                         const void *gamma, const void *dS, void *dX, void *dgamma, void *workspace, void *stream);
+
+/* Bytes of scratch that gemm_epi_dact needs for dbias (0 for sizes or an axis it refuses). */
+int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis);
+
+/* Backward of a forward epilogue D = act(z) (+ R), z = alpha*A.B + bias, from the gradient dD:
+ *     dZ = dD * act'(z),   dbias = the sum of dZ over the axis the bias was broadcast along
+ * (the gradient of R is dD itself; those of A and B are products with dZ).
+ *   dtype, epilogue, bias_axis  of the forward plan: any epilogue from NONE to TANH, any dtype
+ *           (E4M3: dD, Z, dZ and dbias are bf16).  n is a multiple of 8.
+ *   dD      (m, n), dense.
+ *   Z       (m, n): the pre-activation z, as a NONE or BIAS plan writes it.  RELU(_BIAS),
+ *           GELU(_BIAS), TANH(_BIAS); else ignored.  ReLU's slope at z = 0 is 0.
+ *   aux     RELU_AUX(_BIAS): the packed mask that the forward run wrote (bits past column n-1
+ *           are ignored); else ignored.
+ *   dZ      (m, n), may be dD or Z.  NONE and BIAS: NULL (dZ is dD; ERR_ARG otherwise).
+ *   dbias   length m (ROW) or n (COL); NULL: not wanted (then dZ is).  Summed in fp32 from the
+ *           unrounded dZ in an order fixed by (m, n), rounded once.
+ *   workspace  as for gemm_epi_rmsnorm_bwd: gemm_epi_dact_workspace_bytes(m, n, bias_axis) bytes,
+ *           with dbias.
+ * One launch, two with dbias.  Returns OK, ERR_ARG, ERR_ALIGN, ERR_NULL, ERR_NO_DEVICE or ERR_CUDA. */
+int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, const void *dD, const void *Z,
+                  const uint32_t *aux, void *dZ, void *dbias, void *workspace, void *stream);
+
 /* Release the plan (host metadata, tensor maps, status word).  Must not
  * overlap a run still executing on the GPU that uses this plan's status word:
  * synchronise first.  ERR_ARG for an unknown or already freed handle. */
