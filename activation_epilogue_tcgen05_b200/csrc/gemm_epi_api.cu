@@ -517,8 +517,38 @@ int ensure_maps(Plan *P, const void *A, const void *B, void *D) {
     return GEMM_EPI_OK;
 }
 
+// The extended epilogue of one launch: the residual and the scales by row (either may be NULL).
+struct Ext {
+    const void *R;
+    const float *scale_rows;
+};
+
+// The plan's kernel with the extended epilogue, if the plan has one.
+int find_ext(const Plan *P, TcLauncher *tc, SkLauncher *sk) {
+    const bool b_mn = P->b_layout == GEMM_EPI_B_KN;
+    KernelInfo info;
+    if (P->a_km || P->sk_grid || P->bwd) return GEMM_EPI_ERR_UNSUPPORTED;
+    if (P->kernel == GEMM_EPI_KERNEL_SPLITK)
+        return find_sk_ext(P->dtype, P->kepi, b_mn, P->nm, P->qout, sk, &info) ? GEMM_EPI_OK : GEMM_EPI_ERR_UNSUPPORTED;
+    if (!find_tc_ext(P->kernel == GEMM_EPI_KERNEL_TC2 ? 2 : 1, P->dtype, P->kepi, b_mn, P->block_n, P->qout, tc, &info) ||
+        info.katoms != P->katoms)
+        return GEMM_EPI_ERR_UNSUPPORTED;
+    return GEMM_EPI_OK;
+}
+
+int check_ext_args(const Plan *P, const Ext &x) {
+    if (P->qout && x.R) return GEMM_EPI_ERR_UNSUPPORTED;      // a residual stream is kept in 16 bits
+    if (!aligned16(x.R) || (reinterpret_cast<uintptr_t>(x.scale_rows) & 3u)) return GEMM_EPI_ERR_ALIGN;
+    TcLauncher tc;
+    SkLauncher sk;
+    return find_ext(P, &tc, &sk);
+}
+
 int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, cudaStream_t stream,
-                float *dbias_ws = nullptr) {
+                float *dbias_ws = nullptr, const Ext *ext = nullptr) {
+    TcLauncher tc_ext = nullptr;
+    SkLauncher sk_ext = nullptr;
+    if (ext && find_ext(P, &tc_ext, &sk_ext) != GEMM_EPI_OK) return GEMM_EPI_ERR_UNSUPPORTED;
     if (!P->has_bias) bias = nullptr;
     const int bk = 128 / esize(P->dtype);
     const int num_kb = (int)((P->k + bk - 1) / bk);
@@ -572,11 +602,16 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.trace = trace_for_launch();
         L.p.pre_kb = P->sk_pre_kb;
         L.p.pre_x = P->sk_pre_x;
+        if (ext) {
+            L.p.residual = ext->R;
+            L.p.scale_rows = ext->scale_rows;
+            L.p.bias_row = P->axis == GEMM_EPI_BIAS_ROW;
+        }
         L.grid = P->grid;
         L.cluster = P->split;
         L.pdl = P->pdl;
         L.stream = stream;
-        e = (fused ? P->sk_launch : P->sk_none_launch)(L);
+        e = (ext ? sk_ext : fused ? P->sk_launch : P->sk_none_launch)(L);
     } else {
         const int cg = P->kernel == GEMM_EPI_KERNEL_TC2 ? 2 : 1;
         TcLaunch L{};
@@ -611,10 +646,15 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.l2_mode = P->l2_mode;
         L.p.prefetch = P->prefetch;
         L.p.fused = P->fused ? 1 : 0;
+        if (ext) {
+            L.p.residual = ext->R;
+            L.p.scale_rows = ext->scale_rows;
+            L.p.bias_row = P->axis == GEMM_EPI_BIAS_ROW;
+        }
         L.grid = P->grid;
         L.pdl = P->pdl;
         L.stream = stream;
-        e = (fused ? P->tc_launch : P->tc_none_launch)(L);
+        e = (ext ? tc_ext : fused ? P->tc_launch : P->tc_none_launch)(L);
     }
     if (e != cudaSuccess && getenv("GEMM_EPI_LOG")) fprintf(stderr, "gemm_epi launch: %s (%d)\n", cudaGetErrorString(e), (int)e);
     return e == cudaSuccess ? GEMM_EPI_OK : GEMM_EPI_ERR_CUDA;
@@ -785,6 +825,24 @@ bool find_tc(int cg, int dt, int epi, int axis, bool b_mn, int bn, bool qout, bo
     }
     return false;
 }
+bool find_tc_ext(int cg, int dt, int epi, bool b_mn, int bn, bool qout, TcLauncher *l, KernelInfo *i) {
+    if (qout) return dt == DT_E4M3 && find_tc_e4m3q_ext(cg, epi, b_mn, bn, l, i);
+    switch (dt) {
+    case DT_F16: return find_tc_f16_ext(cg, epi, b_mn, bn, l, i);
+    case DT_BF16: return find_tc_bf16_ext(cg, epi, b_mn, bn, l, i);
+    case DT_E4M3: return find_tc_e4m3_ext(cg, epi, b_mn, bn, l, i);
+    }
+    return false;
+}
+bool find_sk_ext(int dt, int epi, bool w_mn, int nm, bool qout, SkLauncher *l, KernelInfo *i) {
+    if (qout) return dt == DT_E4M3 && find_sk_e4m3q_ext(epi, w_mn, nm, l, i);
+    switch (dt) {
+    case DT_F16: return find_sk_f16_ext(epi, w_mn, nm, l, i);
+    case DT_BF16: return find_sk_bf16_ext(epi, w_mn, nm, l, i);
+    case DT_E4M3: return find_sk_e4m3_ext(epi, w_mn, nm, l, i);
+    }
+    return false;
+}
 bool find_sg(int dt, int epi, int axis, bool w_mn, int nm, bool qout, SgLauncher *l, KernelInfo *i) {
     KernelInfo tmp;
     if (!i) i = &tmp;
@@ -866,6 +924,21 @@ int gemm_epi_run(gemm_epi_plan_t plan, const void *A, const void *B, const void 
     // the amax word is this run's maximum: start it at 0 (the kernel max-reduces into it)
     if (P->qout && P->amax && cudaMemsetAsync(P->amax, 0, sizeof(float), s) != cudaSuccess) return GEMM_EPI_ERR_CUDA;
     return launch_main(P, true, bias, D, aux, s);
+}
+
+int gemm_epi_run_ext(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, const void *R,
+                     const float *d_scale_rows, void *D, uint32_t *aux, void *stream) {
+    if (!R && !d_scale_rows) return gemm_epi_run(plan, A, B, bias, D, aux, stream);
+    if (!live(plan)) return GEMM_EPI_ERR_ARG;
+    Plan *P = reinterpret_cast<Plan *>(plan);
+    const Ext x{R, d_scale_rows};
+    int rc = check_run_args(P, A, B, bias, D, aux);
+    if (rc == GEMM_EPI_OK) rc = check_ext_args(P, x);
+    if (rc == GEMM_EPI_OK) rc = ensure_maps(P, A, B, D);
+    if (rc != GEMM_EPI_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (P->qout && P->amax && cudaMemsetAsync(P->amax, 0, sizeof(float), s) != cudaSuccess) return GEMM_EPI_ERR_CUDA;
+    return launch_main(P, true, bias, D, aux, s, nullptr, &x);
 }
 
 int gemm_epi_unfused_run(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, void *D,
@@ -1120,6 +1193,36 @@ int gemm_epi_mlp_run(gemm_epi_mlp_t mlp, const void *X, const void *W1, const vo
     rc = launch_main(U, true, b1, H, nullptr, s);
     if (rc != GEMM_EPI_OK) return rc;
     return launch_main(Dn, true, b2, Y, nullptr, s);
+}
+
+int gemm_epi_mlp_run_prenorm(gemm_epi_mlp_t mlp, const void *X, const void *R, const void *gamma, float eps,
+                             const void *W1, const void *b1, const void *W2, const void *b2, void *S, void *N,
+                             float *d_scale_rows, void *H, void *Y, void *stream) {
+    Mlp *M = mlp_live(mlp);
+    if (!M) return GEMM_EPI_ERR_ARG;
+    Plan *U = reinterpret_cast<Plan *>(M->up), *Dn = reinterpret_cast<Plan *>(M->down);
+    const bool fp8 = U->qout;
+    if ((R && !S) || (fp8 && !d_scale_rows)) return GEMM_EPI_ERR_NULL;
+    const Ext xu{nullptr, fp8 ? d_scale_rows : nullptr}, xd{R ? S : X, nullptr};
+    // N and H are scratch of their own; Y may be the stream that it adds
+    if (N == X || N == xd.R || (R && N == R) || N == Y || H == Y || H == N || H == xd.R) return GEMM_EPI_ERR_ARG;
+    // every check of the three launches before the first is enqueued
+    int rc = check_run_args(U, N, W1, b1, H, nullptr);
+    if (rc == GEMM_EPI_OK) rc = check_run_args(Dn, H, W2, b2, Y, nullptr);
+    if (rc == GEMM_EPI_OK && fp8) rc = check_ext_args(U, xu);
+    if (rc == GEMM_EPI_OK) rc = check_ext_args(Dn, xd);
+    if (rc == GEMM_EPI_OK) rc = ensure_maps(U, N, W1, H);
+    if (rc == GEMM_EPI_OK) rc = ensure_maps(Dn, H, W2, Y);
+    if (rc != GEMM_EPI_OK) return rc;
+    const int norm_dt = fp8 ? GEMM_EPI_BF16 : U->dtype;
+    rc = gemm_epi_rmsnorm(U->m, U->k, norm_dt, fp8 ? GEMM_EPI_NORM_E4M3_ROWS : GEMM_EPI_NORM_SAME, eps, X, R, gamma,
+                          R ? S : nullptr, N, d_scale_rows, nullptr, stream);
+    if (rc != GEMM_EPI_OK) return rc;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (fp8 && U->amax && cudaMemsetAsync(U->amax, 0, sizeof(float), s) != cudaSuccess) return GEMM_EPI_ERR_CUDA;
+    rc = launch_main(U, true, b1, H, nullptr, s, nullptr, fp8 ? &xu : nullptr);
+    if (rc != GEMM_EPI_OK) return rc;
+    return launch_main(Dn, true, b2, Y, nullptr, s, nullptr, &xd);
 }
 
 int gemm_epi_mlp_unfused_run(gemm_epi_mlp_t mlp, const void *X, const void *W1, const void *b1, const void *W2,

@@ -61,10 +61,14 @@ struct SkParams {
     unsigned long long *trace;   // timeline records; used only by builds with GEMM_EPI_TRACE=2
     int pre_kb;                  // k-blocks of this CTA's weight slice asked of L2 before the dependency wait (< 0: all)
     int pre_x;                   // nonzero: also ask L2 for this CTA's activation slice before that wait
+    const void *residual;        // EXT kernels: as TcParams::residual, scale_rows, bias_row
+    const float *scale_rows;
+    int bias_row;
 };
 
-template <int DT_, int EPI_, int AXIS_, bool W_MN_, int NM_, int STAGES_, bool QOUT_ = false>
+template <int DT_, int EPI_, int AXIS_, bool W_MN_, int NM_, int STAGES_, bool QOUT_ = false, bool EXT_ = false>
 struct SkCfg {
+    static constexpr bool EXT = EXT_;               // residual and scales by row (TcCfg::EXT)
     static constexpr int DT = DT_, EPI = EPI_, AXIS = AXIS_, NM = NM_, STAGES = STAGES_;
     static constexpr bool QOUT = QOUT_;             // e4m3 output quantised in the epilogue
     static constexpr bool W_MN = W_MN_;             // weight stored (k, n): MMA operand A is MN-major
@@ -185,8 +189,25 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const bool epi = warp >= 2;
     float cbias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float alpha = 1.0f, inv_out = 1.0f;
+    // EXT: residual values and row scales of the first four blocks of rows that this warp finishes
+    // (all there are for up to 16 rows); later blocks read theirs when they come to them
+    float pre_r[4][C::EXT ? 4 : 1] = {}, pre_a[4][C::EXT ? 4 : 1] = {};
+    auto load_ext = [&](int grp, int u, float (&r)[C::EXT ? 4 : 1], float (&a)[C::EXT ? 4 : 1]) {
+        if constexpr (!C::EXT) return;
+        const int col = n0 + 32 * grp + lane;
+#pragma unroll
+        for (int c = 0; c < (C::EXT ? 4 : 0); ++c) {
+            const int i = 4 * u + c;
+            r[c] = 0.0f;
+            a[c] = alpha;
+            if (i < p.m) {
+                if (!C::QOUT && p.residual != nullptr && col < p.n) r[c] = OutT<C::DT>::load(p.residual, (int64_t)i * p.n + col);
+                if (p.scale_rows != nullptr) a[c] = __ldg(p.scale_rows + i) * (p.scale_b != nullptr ? __ldg(p.scale_b) : 1.0f);
+            }
+        }
+    };
     if (epi && groups > 0) {
-        if constexpr (C::EPI != EPI_NONE && C::AXIS == AXIS_COL) {
+        if constexpr (C::EPI != EPI_NONE && C::AXIS == AXIS_COL) if (!C::EXT || !p.bias_row) {
 #pragma unroll
             for (int gl = 0; gl < 4; ++gl) {
                 const int col = n0 + 32 * ((int)rank + gl * (int)csize) + lane;
@@ -195,6 +216,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         if (p.scale_a != nullptr) alpha = __ldg(p.scale_a) * __ldg(p.scale_b);
         if constexpr (C::QOUT) inv_out = 1.0f / __ldg(p.out_scale);
+        if constexpr (C::EXT) {
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                // the same blocks as below: four of this warp's own group, or every fourth of the owned ones
+                const int unit = warp - 2 + 4 * b;
+                if (csize == 1u) {
+                    if (b < C::NM / 4) load_ext(warp & 3, b, pre_r[b], pre_a[b]);
+                } else if (unit < groups * (C::NM / 4)) {
+                    load_ext((int)rank + unit / (C::NM / 4) * (int)csize, unit % (C::NM / 4), pre_r[b], pre_a[b]);
+                }
+            }
+        }
     }
 
     if (warp == 0) {
@@ -273,7 +306,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // The fused epilogue of rows 4u .. 4u+3 of column group `grp` (this thread's column
     // n0 + 32 grp + lane), from their fp32 sums `part`: the four rows' values first, without
     // branches, then their stores.
-    auto emit4 = [&](int grp, int u, const float (&part)[4], float cb) {
+    // (EXT: its residual values r and row scales a.)
+    auto emit4 = [&](int grp, int u, const float (&part)[4], float cb, const float (&r)[C::EXT ? 4 : 1],
+                     const float (&a)[C::EXT ? 4 : 1]) {
         const int col = n0 + 32 * grp + lane;
         const bool col_ok = col < p.n;
         // every word of the mask pitch belongs to exactly one group of one tile;
@@ -283,16 +318,19 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int i = 4 * u + c;
-            float x = part[c] * alpha;
+            float x = part[c] * (C::EXT ? a[C::EXT ? c : 0] : alpha);
             if constexpr (C::EPI != EPI_NONE) {
                 if constexpr (C::AXIS == AXIS_COL) x += cb;
-                else if (has_bias && i < p.m) x += O::load(p.bias, i);
+                if constexpr (C::EXT) {
+                    if (p.bias_row && has_bias && i < p.m) x += O::load(p.bias, i);
+                } else if constexpr (C::AXIS != AXIS_COL) if (has_bias && i < p.m) x += O::load(p.bias, i);
             }
             if constexpr (C::EPI == EPI_RELU_AUX) {
                 const uint32_t bits = __ballot_sync(0xFFFFFFFFu, col_ok && x > 0.0f);
                 if (lane == 0 && i < p.m) p.aux[(int64_t)i * p.aux_pitch_words + word] = bits;
             }
             y[c] = activate<C::EPI>(x);
+            if constexpr (C::EXT && !C::QOUT) y[c] += r[c];
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -344,7 +382,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int u = 0; u < C::NM / 4; ++u) {
                     const float part[4] = {acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]};
-                    emit4(q, u, part, cb);
+                    if constexpr (C::EXT) {
+                        if (u < 4) {
+                            emit4(q, u, part, cb, pre_r[u < 4 ? u : 0], pre_a[u < 4 ? u : 0]);
+                        } else {
+                            float r[4], a[4];
+                            load_ext(q, u, r, a);
+                            emit4(q, u, part, cb, r, a);
+                        }
+                    } else {
+                        emit4(q, u, part, cb, pre_r[0], pre_a[0]);
+                    }
                 }
             }
         } else {
@@ -391,7 +439,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     if (j == gl) cb = cbias[j];
-                emit4((int)rank + gl * (int)csize, u, part, cb);
+                const int grp = (int)rank + gl * (int)csize;
+                if constexpr (C::EXT) {
+                    const int b = (unit - ew) / 4;          // this warp's b-th block
+                    float r[4], a[4];
+                    if (b < 4) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (k == b) {
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) { r[c] = pre_r[k][c]; a[c] = pre_a[k][c]; }
+                            }
+                    } else {
+                        load_ext(grp, u, r, a);
+                    }
+                    emit4(grp, u, part, cb, r, a);
+                } else {
+                    emit4(grp, u, part, cb, pre_r[0], pre_a[0]);
+                }
                 if (warp == 2 && lane == 0) trace_stage(p.trace, 2, tr_i, 34, tile_n, unit);
             }
         }

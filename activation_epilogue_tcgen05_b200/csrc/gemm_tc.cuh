@@ -114,6 +114,10 @@ struct TcParams {
     // evict-first, so that streaming them out does not push the operands out of L2; 2 = as 1,
     // and the operands are loaded evict-last
     int l2_mode;
+    // Extended epilogue (EXT kernels): D = act(alpha_i A.B + bias) + R, alpha_i = scale_rows[i] * *scale_b
+    const void *residual;        // R, (m, n) in the output type, or NULL; may be D
+    const float *scale_rows;     // m floats that take the place of *scale_a, or NULL
+    int bias_row;                // the bias runs along the rows (length m)
 };
 
 // Timeline tracing (off unless the library is compiled with -DGEMM_EPI_TRACE=1 or 2).
@@ -273,6 +277,7 @@ struct OutT<DT_F16> {
         __half2 h = __floats2half2_rn(a, b);
         return *reinterpret_cast<uint32_t *>(&h);
     }
+    static __device__ __forceinline__ float2 unpack(uint32_t w) { return __half22float2(*reinterpret_cast<__half2 *>(&w)); }
     static __device__ __forceinline__ float load(const void *p, int64_t i) {
         return __half2float(reinterpret_cast<const __half *>(p)[i]);
     }
@@ -283,6 +288,9 @@ struct OutT<DT_BF16> {
     static __device__ __forceinline__ uint32_t pack(float a, float b) {
         __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
         return *reinterpret_cast<uint32_t *>(&h);
+    }
+    static __device__ __forceinline__ float2 unpack(uint32_t w) {
+        return __bfloat1622float2(*reinterpret_cast<__nv_bfloat162 *>(&w));
     }
     static __device__ __forceinline__ float load(const void *p, int64_t i) {
         return __bfloat162float(reinterpret_cast<const __nv_bfloat16 *>(p)[i]);
@@ -364,8 +372,12 @@ __device__ __forceinline__ float activate(float x) {
 constexpr int tc_katoms(int atom_bytes) { return atom_bytes <= 32768 ? 2 : 1; }
 
 template <int DT_, int EPI_, int AXIS_, bool B_MN_, int BN_, int CG_, int STAGES_, bool QOUT_ = false,
-          bool A_MN_ = false>
+          bool A_MN_ = false, bool EXT_ = false>
 struct TcCfg {
+    // Extended epilogue: a residual added after the activation and one scale a row of A.  Kernels of
+    // their own, so that the plain ones keep their registers; the bias axis is a run-time choice in
+    // them (AXIS is COL), and EPI_BIAS without a bias stands in for EPI_NONE.
+    static constexpr bool EXT = EXT_;
     static constexpr int DT = DT_, EPI = EPI_, AXIS = AXIS_, BN = BN_, CG = CG_, STAGES = STAGES_;
     static constexpr bool B_MN = B_MN_;             // B stored (k, n): N contiguous
     static constexpr bool A_MN = A_MN_;             // A stored (k, m): M contiguous
@@ -441,6 +453,7 @@ struct TcCfg {
     static_assert(A_BYTES % 1024 == 0 && B_BYTES % 1024 == 0, "stage alignment");
     static_assert(!BWD || (EPI_WARPS == 4 && CPG == 4), "backward epilogue: one mask uint4 per chunk group");
     static_assert(!QOUT || (DT == DT_E4M3 && !BWD && EPI != EPI_RELU_AUX), "FP8 output: e4m3 forward plans");
+    static_assert(!EXT || (FWD_BIAS && AXIS == AXIS_COL && !A_MN), "extended epilogue: forward kernels, A stored (m, k)");
     static_assert(!A_MN || BM % A_BOX_M == 0, "MN-major A tile must be whole boxes");
     static_assert(EPI_WARPS * NCH_W * 2048 <= STAGES * (A_STAGE + B_STAGE),
                   "the last tile's output staging fits in the operand ring");
@@ -880,6 +893,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if constexpr (C::FWD_BIAS && C::AXIS == AXIS_ROW) {
                 if (row_ok && has_bias) rbias = O::load(p.bias, row);
             }
+            if constexpr (C::EXT) {
+                if (row_ok && has_bias && p.bias_row) rbias = O::load(p.bias, row);
+                if (row_ok && p.scale_rows != nullptr) {
+                    alpha = __ldg(p.scale_rows + row);
+                    if (p.scale_b != nullptr) alpha *= __ldg(p.scale_b);
+                }
+            }
             // backward: this lane's mask words for columns [nw, nw + COLS_W), one uint4 per
             // 128 columns, fetched before the accumulator wait so that their latency hides
             uint4 mk0 = make_uint4(0u, 0u, 0u, 0u), mk1 = mk0;
@@ -895,7 +915,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 // this warp's copy of bias[nw .. nw+COLS_W) as fp32 (read once per tile)
                 __syncwarp();
                 // (bsm[j] holds the bias of the warp's j-th column: chunk j / 32, column j % 32)
-                if (!has_bias) {
+                if (!has_bias || (C::EXT && p.bias_row)) {
                     for (int j = lane; j < C::COLS_W; j += 32) bsm[j] = 0.0f;
                 } else {
 #pragma unroll
@@ -979,6 +999,17 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                     const int col0 = n0 + 32 * c;
+                    // this lane's 32 residual values: 64 bytes of its row
+                    uint4 res[4];
+                    if constexpr (C::EXT && !C::QOUT) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            res[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (p.residual != nullptr && row_ok && col0 + 8 * i < p.n)
+                                res[i] = __ldcs(reinterpret_cast<const uint4 *>(
+                                    static_cast<const typename O::type *>(p.residual) + (int64_t)row * p.n + col0 + 8 * i));
+                        }
+                    }
                     uint32_t packed[16];
                     uint32_t bits = 0;
                     const uint32_t mbits = cc == 0 ? mk.x : cc == 1 ? mk.y : cc == 2 ? mk.z : mk.w;
@@ -991,6 +1022,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if constexpr (C::FWD_BIAS) {
                             if constexpr (C::AXIS == AXIS_ROW) { x0 += rbias; x1 += rbias; }
                             else { x0 += bsm[32 * cl + j]; x1 += bsm[32 * cl + j + 1]; }
+                            if constexpr (C::EXT) { x0 += rbias; x1 += rbias; }
                         }
                         if constexpr (C::BWD) {
                             // ReLU backward: the gradient passes where the forward input was > 0
@@ -1008,7 +1040,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             bits |= (x0 > 0.0f ? 1u : 0u) << j;
                             bits |= (x1 > 0.0f ? 1u : 0u) << (j + 1);
                         }
-                        const float y0 = activate<C::EPI>(x0), y1 = activate<C::EPI>(x1);
+                        float y0 = activate<C::EPI>(x0), y1 = activate<C::EPI>(x1);
+                        if constexpr (C::EXT && !C::QOUT) {
+                            const float2 r = O::unpack(j % 8 == 0 ? res[j / 8].x : j % 8 == 2 ? res[j / 8].y
+                                                       : j % 8 == 4 ? res[j / 8].z : res[j / 8].w);
+                            y0 += r.x;
+                            y1 += r.y;
+                        }
                         if constexpr (C::QOUT) {
                             amax_l = fmaxf(amax_l, fmaxf(fabsf(y0), fabsf(y1)));
                             // two e4m3 codes, round to nearest even, saturating at +-448; y0 low byte

@@ -60,6 +60,9 @@ bool find_tc(int cg, int dt, int epi, int axis, bool b_mn, int bn, bool qout, bo
 bool find_sk(int dt, int epi, int axis, bool w_mn, int nm, bool qout, SkLauncher *launch, KernelInfo *info);
 bool find_sg(int dt, int epi, int axis, bool w_mn, int nm, bool qout, SgLauncher *launch, KernelInfo *info);
 bool find_bias_act(int dt, int epi, int axis, BiasActLauncher *launch);
+// The same kernels with the extended epilogue (residual, scales by row; the bias axis at run time).
+bool find_tc_ext(int cg, int dt, int epi, bool b_mn, int bn, bool qout, TcLauncher *launch, KernelInfo *info);
+bool find_sk_ext(int dt, int epi, bool w_mn, int nm, bool qout, SkLauncher *launch, KernelInfo *info);
 
 // Bias-gradient reductions (dbias.cuh); out_dt is the bias type (DT_F16 or DT_BF16).
 //   sum_parts_f32: out[i] = sum_p src[p * len + i] over fp32 partials (fused backward)
@@ -102,6 +105,14 @@ bool find_sk_f16(int epi, int axis, bool w_mn, int nm, SkLauncher *, KernelInfo 
 bool find_sk_bf16(int epi, int axis, bool w_mn, int nm, SkLauncher *, KernelInfo *);
 bool find_sk_e4m3(int epi, int axis, bool w_mn, int nm, SkLauncher *, KernelInfo *);
 bool find_sk_e4m3_q(int epi, int axis, bool w_mn, int nm, SkLauncher *, KernelInfo *);
+bool find_tc_f16_ext(int cg, int epi, bool b_mn, int bn, TcLauncher *, KernelInfo *);
+bool find_sk_f16_ext(int epi, bool w_mn, int nm, SkLauncher *, KernelInfo *);
+bool find_tc_bf16_ext(int cg, int epi, bool b_mn, int bn, TcLauncher *, KernelInfo *);
+bool find_sk_bf16_ext(int epi, bool w_mn, int nm, SkLauncher *, KernelInfo *);
+bool find_tc_e4m3_ext(int cg, int epi, bool b_mn, int bn, TcLauncher *, KernelInfo *);
+bool find_sk_e4m3_ext(int epi, bool w_mn, int nm, SkLauncher *, KernelInfo *);
+bool find_tc_e4m3q_ext(int cg, int epi, bool b_mn, int bn, TcLauncher *, KernelInfo *);
+bool find_sk_e4m3q_ext(int epi, bool w_mn, int nm, SkLauncher *, KernelInfo *);
 bool find_sg_f16(int epi, int axis, bool w_mn, int nm, SgLauncher *, KernelInfo *);
 bool find_sg_bf16(int epi, int axis, bool w_mn, int nm, SgLauncher *, KernelInfo *);
 bool find_sg_e4m3(int epi, int axis, bool w_mn, int nm, SgLauncher *, KernelInfo *);

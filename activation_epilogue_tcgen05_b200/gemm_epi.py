@@ -51,7 +51,8 @@ EXPORTS = ("gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts", "gemm_epi_
            "gemm_epi_set_out_scale", "gemm_epi_mlp_plan", "gemm_epi_mlp_set_scales", "gemm_epi_mlp_run",
            "gemm_epi_mlp_check", "gemm_epi_mlp_query", "gemm_epi_mlp_free", "gemm_epi_mlp_unfused_run",
            "gemm_epi_plan_preview", "gemm_epi_rmsnorm", "gemm_epi_rmsnorm_workspace_bytes",
-           "gemm_epi_rmsnorm_bwd", "gemm_epi_dact_workspace_bytes", "gemm_epi_dact")
+           "gemm_epi_rmsnorm_bwd", "gemm_epi_dact_workspace_bytes", "gemm_epi_dact", "gemm_epi_run_ext",
+           "gemm_epi_mlp_run_prenorm")
 
 
 class Options(ctypes.Structure):
@@ -128,7 +129,9 @@ def lib():
             L.gemm_epi_dact.argtypes = [i64, i64, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp]
             L.gemm_epi_dact_workspace_bytes.argtypes = [i64, i64, i32]
             L.gemm_epi_dact_workspace_bytes.restype = i64
-            for name in ("gemm_epi_rmsnorm", "gemm_epi_rmsnorm_bwd", "gemm_epi_dact",
+            L.gemm_epi_run_ext.argtypes = [vp] * 9
+            L.gemm_epi_mlp_run_prenorm.argtypes = [vp, vp, vp, vp, ctypes.c_float] + [vp] * 10
+            for name in ("gemm_epi_run_ext", "gemm_epi_mlp_run_prenorm", "gemm_epi_rmsnorm", "gemm_epi_rmsnorm_bwd", "gemm_epi_dact",
                          "gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts",
                          "gemm_epi_set_scales", "gemm_epi_run", "gemm_epi_unfused_run",
                          "gemm_epi_check", "gemm_epi_plan_query", "gemm_epi_free",
@@ -171,6 +174,10 @@ def gemm_epi_run(plan, A, B, bias, D, aux, stream) -> None:
     _check(lib().gemm_epi_run(plan, A, B, bias, D, aux, stream), "gemm_epi_run")
 
 
+def gemm_epi_run_ext(plan, A, B, bias, R, d_scale_rows, D, aux, stream) -> None:
+    _check(lib().gemm_epi_run_ext(plan, A, B, bias, R, d_scale_rows, D, aux, stream), "gemm_epi_run_ext")
+
+
 def gemm_epi_unfused_run(plan, A, B, bias, D, aux, stream) -> None:
     _check(lib().gemm_epi_unfused_run(plan, A, B, bias, D, aux, stream), "gemm_epi_unfused_run")
 
@@ -201,6 +208,11 @@ def gemm_epi_mlp_set_scales(mlp, d_scale_x, d_scale_w1, d_scale_h, d_amax_h, d_s
 
 def gemm_epi_mlp_run(mlp, X, W1, b1, W2, b2, H, Y, stream) -> None:
     _check(lib().gemm_epi_mlp_run(mlp, X, W1, b1, W2, b2, H, Y, stream), "gemm_epi_mlp_run")
+
+
+def gemm_epi_mlp_run_prenorm(mlp, X, R, gamma, eps, W1, b1, W2, b2, S, N, d_scale_rows, H, Y, stream) -> None:
+    _check(lib().gemm_epi_mlp_run_prenorm(mlp, X, R, gamma, eps, W1, b1, W2, b2, S, N, d_scale_rows, H, Y, stream),
+           "gemm_epi_mlp_run_prenorm")
 
 
 def gemm_epi_mlp_unfused_run(mlp, X, W1, b1, W2, b2, H, Y, H_wide, stream) -> None:
@@ -334,6 +346,7 @@ class Plan:
         layout = LAYOUT[b_layout] | (A_KM if a_layout == "km" else 0)
         self.handle = gemm_epi_plan_opts(self.m, self.n, self.k, DTYPE[dtype], EPILOGUE[epilogue],
                                          AXIS[bias_axis], layout, opts)
+        self.out_e4m3 = bool(out_e4m3)
         self._scales = None
 
     @property
@@ -354,6 +367,29 @@ class Plan:
         s = _stream_ptr(stream)
         f = gemm_epi_run if fused else gemm_epi_unfused_run
         f(self.handle, _ptr(A), _ptr(B), _ptr(bias), _ptr(D), _ptr(aux), s)
+
+    def run_ext(self, A, B, bias, D, residual=None, scale_rows=None, aux=None, stream=None):
+        """D = act(alpha_i * A.B + bias) + residual; ``scale_rows``: m fp32 values, one scale a row of A
+        (see gemm_epi_run_ext in include/gemm_epi.h).  ``residual`` may be D."""
+        dev, s = _device_and_stream(stream)
+        t_in, t_bias, t_out, f32, i32 = self._types()
+        m, n = self.m, self.n
+        bias_len = (m if self.bias_axis == "row" else n) if self.epilogue in HAS_BIAS else None
+        gemm_epi_run_ext(self.handle, _operand(A, "Plan.run_ext: A", t_in, m * self.k, dev),
+                         _operand(B, "Plan.run_ext: B", t_in, n * self.k, dev),
+                         None if bias_len is None else _operand(bias, "Plan.run_ext: bias", t_bias, bias_len, dev),
+                         _operand(residual, "Plan.run_ext: residual", t_bias, m * n, dev, True),
+                         _operand(scale_rows, "Plan.run_ext: scale_rows", f32, m, dev, True),
+                         _operand(D, "Plan.run_ext: D", t_out, m * n, dev),
+                         _operand(aux, "Plan.run_ext: aux", i32, m * aux_pitch_words(n), dev)
+                         if self.epilogue in HAS_AUX else None, s)
+
+    def _types(self):
+        """torch types of the operands, of bias and residual, and of D; of scales and mask words."""
+        import torch
+        t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[self.dtype]
+        wide = torch.bfloat16 if self.dtype == "e4m3" else t
+        return t, wide, t if self.out_e4m3 else wide, torch.float32, torch.int32
 
     def run_bwd(self, A, B, aux, D, dbias=None, stream=None, fused=True):
         """Backward plans (``drelu``/``drelu_bgrad``): D = mask ? alpha*A.B : 0 (+ dbias)."""
@@ -420,6 +456,22 @@ class MlpPlan:
         else:
             gemm_epi_mlp_unfused_run(self.handle, _ptr(X), _ptr(W1), _ptr(b1), _ptr(W2), _ptr(b2), _ptr(H),
                                      _ptr(Y), _ptr(H_wide), _stream_ptr(stream))
+
+    def run_prenorm(self, X, gamma, W1, b1, W2, b2, N, H, Y, residual=None, S=None, scale_rows=None, eps=1e-6, stream=None):
+        """S = X + residual, N = rmsnorm(S) * gamma, H = act(N.W1 + b1), Y = H.W2 + b2 + S (S is X without
+        a residual); e4m3: ``scale_rows``, m fp32 values of scratch for N's scales by row."""
+        import torch
+        dev, s = _device_and_stream(stream)
+        t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[self.dtype]
+        wide = torch.bfloat16 if self.dtype == "e4m3" else t
+        m, dm, ff, w = self.m, self.d_model, self.d_ff, "MlpPlan.run_prenorm: "
+        gemm_epi_mlp_run_prenorm(
+            self.handle, _operand(X, w + "X", wide, m * dm, dev), _operand(residual, w + "residual", wide, m * dm, dev, True),
+            _operand(gamma, w + "gamma", wide, dm, dev), float(eps), _operand(W1, w + "W1", t, dm * ff, dev),
+            _operand(b1, w + "b1", wide, ff, dev), _operand(W2, w + "W2", t, dm * ff, dev), _operand(b2, w + "b2", wide, dm, dev),
+            _operand(S, w + "S", wide, m * dm, dev, True), _operand(N, w + "N", t, m * dm, dev),
+            _operand(scale_rows, w + "scale_rows", torch.float32, m, dev, True), _operand(H, w + "H", t, m * ff, dev),
+            _operand(Y, w + "Y", wide, m * dm, dev), s)
 
     def check(self, stream=None):
         gemm_epi_mlp_check(self.handle, _stream_ptr(stream))

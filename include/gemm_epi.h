@@ -239,6 +239,22 @@ int gemm_epi_set_out_scale(gemm_epi_plan_t plan, const float *d_scale_out, float
 int gemm_epi_run(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, void *D,
                  uint32_t *aux, void *stream);
 
+/* gemm_epi_run with an extended epilogue:
+ *     D = act(alpha_i * (A . B) + bias) + R
+ *   R       (m, n) in the output type, dense, 16-byte aligned: the residual, added in fp32 after
+ *           the activation, before the one rounding of D.  NULL: none.  R may be D itself (the
+ *           residual stream updated in place) but may not overlap it otherwise.
+ *   d_scale_rows  DEVICE pointer to m floats, 4-byte aligned: one scale a row of A, as
+ *           gemm_epi_rmsnorm writes them; alpha_i = d_scale_rows[i] * s_B.  s_A of
+ *           gemm_epi_set_scales is then not read (E4M3 plans still have both set); for 16-bit
+ *           plans s_B is 1 until set.  NULL: alpha as for gemm_epi_run.
+ * The other arguments, rules and errors are gemm_epi_run's, and so is the result without R and
+ * d_scale_rows.  The mask of RELU_AUX(_BIAS) is that of the pre-activation, as ever.  Plans with
+ * A stored (k, m) return ERR_UNSUPPORTED, plans with an e4m3 output take row scales but no R
+ * (ERR_UNSUPPORTED).  The gradient of R is that of D; gemm_epi_dact gives the rest. */
+int gemm_epi_run_ext(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, const void *R,
+                     const float *d_scale_rows, void *D, uint32_t *aux, void *stream);
+
 /* The library's own UNFUSED baseline on the same plan and arguments: the bare
  * GEMM (epilogue NONE) writes alpha*A.B to D in the output type, then a
  * separate elementwise kernel reads D back, adds the bias, applies the
@@ -363,6 +379,23 @@ int gemm_epi_mlp_set_scales(gemm_epi_mlp_t mlp, const float *d_scale_x, const fl
 /* Enqueue both GEMMs on `stream` (all arguments are checked before either is enqueued). */
 int gemm_epi_mlp_run(gemm_epi_mlp_t mlp, const void *X, const void *W1, const void *b1, const void *W2,
                      const void *b2, void *H, void *Y, void *stream);
+
+/* The block with the norm before it and the residual around it, three launches:
+ *     S = X + R,  N = rmsnorm(S) * gamma,  H = act(alpha1 * N . W1 + b1),  Y = alpha2 * H . W2 + b2 + S
+ * (gemm_epi_rmsnorm, then gemm_epi_run_ext's epilogues; S is X without R).
+ *   X, R, S (m, d_model) in the 16-bit type (bf16 for e4m3 plans), eps and gamma as for
+ *           gemm_epi_rmsnorm, d_model up to 16384.  R may be NULL; S is needed with R and not
+ *           written without it.  S may be X or R; Y may be S (or X without R).
+ *   N       (m, d_model) scratch in the operand type.  e4m3: quantised with one scale a row,
+ *           written to d_scale_rows (m floats, scratch), so that no scale of X has to be known
+ *           beforehand: d_scale_x of gemm_epi_mlp_set_scales is not read by this call.
+ *           16-bit plans ignore d_scale_rows.
+ *   H, Y, W1, b1, W2, b2  as for gemm_epi_mlp_run.
+ * Returns what gemm_epi_mlp_run and gemm_epi_rmsnorm return; every argument is checked before
+ * the first launch. */
+int gemm_epi_mlp_run_prenorm(gemm_epi_mlp_t mlp, const void *X, const void *R, const void *gamma, float eps,
+                             const void *W1, const void *b1, const void *W2, const void *b2, void *S, void *N,
+                             float *d_scale_rows, void *H, void *Y, void *stream);
 
 /* The UNFUSED baseline of gemm_epi_mlp_run, same plan and arguments: bare GEMM writing the
  * up-projection in the 16-bit type, a separate bias + activation kernel, and for e4m3 an amax

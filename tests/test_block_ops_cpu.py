@@ -120,3 +120,10 @@ def test_slopes_against_differences(name):
     h = 1e-5
     diff = (ref.act(name, z + h) - ref.act(name, z - h)) / (2 * h)
     assert float((diff - ref.act_slope(name, z)).abs().max()) < 1e-8
+
+
+def test_extended_entry_points_reject_bad_handles(g):
+    for bad in (None, ctypes.c_void_p(0x1000)):
+        assert g.lib().gemm_epi_run_ext(bad, P, P, P, P, None, P, None, None) == g.ERR_ARG
+        assert g.lib().gemm_epi_run_ext(bad, P, P, P, None, None, P, None, None) == g.ERR_ARG
+        assert g.lib().gemm_epi_mlp_run_prenorm(bad, P, P, P, 1e-6, P, P, P, P, P, P, None, P, P, None) == g.ERR_ARG
