@@ -35,32 +35,69 @@ struct DactParams {
     float *partial;          // COL: [run][n]; ROW: [strip][m]; or NULL
 };
 
-// GELU'(x) = Phi(x) + x phi(x), with Phi from the same Abramowitz & Stegun 7.1.26 form as the
-// forward epilogue's GELU: one exponential serves both terms.
-__device__ __forceinline__ float gelu_slope(float x) {
-    const float ax = fabsf(x);
-    const float t = rcp_approx(fmaf(0.3275911f * 0.70710678118654752f, ax, 1.0f));
-    const float half_poly =
-        t * fmaf(t, fmaf(t, fmaf(t, fmaf(t, 0.5307027145f, -0.7265760135f), 0.7107068705f), -0.142248368f),
-                 0.127414796f);
-    const float s = ax * 0.84932180028801907f;
-    const float e = ex2_approx(-s * s);                    // exp(-x^2 / 2)
-    const float tail = half_poly * e;                      // 1 - Phi(|x|)
-    return fmaf(x * 0.39894228040143268f, e, x < 0.0f ? tail : 1.0f - tail);
+// Two fp32 values in a register pair, for Blackwell's two-wide fp32 instructions: GELU's slope
+// takes 27 instructions an element one by one and 14 in pairs, below what HBM allows time for.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(f32x2 v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
+
+// GELU'(x) = Phi(x) + x phi(x), with 1 - Phi(|x|) from the same Abramowitz & Stegun 7.1.26 form as
+// the forward epilogue's GELU (gelu_erf): one exponential serves both terms.
+//     Phi(x) = 1/2 + sign(x) (1/2 - tail),  tail = 1 - Phi(|x|)
+__device__ __forceinline__ f32x2 gelu_slope(float x0, float x1) {
+    const f32x2 x = pair(x0, x1);
+    const float2 den = split(fma2(pair(fabsf(x0), fabsf(x1)), both(0.3275911f * 0.70710678118654752f), both(1.0f)));
+    const f32x2 t = pair(rcp_approx(den.x), rcp_approx(den.y));
+    f32x2 h = fma2(t, both(0.5307027145f), both(-0.7265760135f));
+    h = fma2(t, h, both(0.7107068705f));
+    h = fma2(t, h, both(-0.142248368f));
+    h = fma2(t, h, both(0.127414796f));
+    h = mul2(t, h);
+    const f32x2 s = mul2(x, both(0.84932180028801907f));        // (c x)^2 = x^2 / 2 * log2(e)
+    const float2 q = split(mul2(s, s));
+    const f32x2 e = pair(ex2_approx(-q.x), ex2_approx(-q.y));     // exp(-x^2 / 2)
+    const float2 half = split(fma2(mul2(h, both(-1.0f)), e, both(0.5f)));
+    const f32x2 phi = pair(copysignf(half.x, x0), copysignf(half.y, x1));
+    return add2(fma2(mul2(x, both(0.39894228040143268f)), e, phi), both(0.5f));
 }
 
+// act'(z) of two neighbouring elements.
 template <int ACT>
-__device__ __forceinline__ float slope(float z) {
-    if constexpr (ACT == DACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-    else if constexpr (ACT == DACT_GELU) return gelu_slope(z);
-    else if constexpr (ACT == DACT_TANH) {
-        const float y = tanhf(z);
-        return fmaf(-y, y, 1.0f);
-    } else return 1.0f;
+__device__ __forceinline__ f32x2 slope(float z0, float z1) {
+    if constexpr (ACT == DACT_GELU) {
+        return gelu_slope(z0, z1);
+    } else {
+        const float y0 = tanhf(z0), y1 = tanhf(z1);
+        return pair(fmaf(-y0, y0, 1.0f), fmaf(-y1, y1, 1.0f));
+    }
 }
 
 template <int DT, int ACT, int AXIS>
-__global__ void __launch_bounds__(32 * DACT_WARPS) dact_kernel(const DactParams p) {
+__global__ void __launch_bounds__(32 * DACT_WARPS, 4) dact_kernel(const DactParams p) {
     __shared__ float sums[DACT_WARPS][DACT_COLS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * DACT_COLS + 8 * lane;
@@ -101,7 +138,11 @@ __global__ void __launch_bounds__(32 * DACT_WARPS) dact_kernel(const DactParams 
             } else if constexpr (ACT != DACT_NONE) {
                 unpack8<DT>(zv[u], z);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] *= slope<ACT>(z[e]);
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 f = split(mul2(pair(d[e], d[e + 1]), slope<ACT>(z[e], z[e + 1])));
+                    d[e] = f.x;
+                    d[e + 1] = f.y;
+                }
             }
             if constexpr (ACT != DACT_NONE) {
                 if (i < r1 && col_ok)

@@ -1,5 +1,6 @@
 // Launchers of the norm and its backward (rmsnorm.cuh).
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.h"
 #include "rmsnorm.cuh"
@@ -8,8 +9,9 @@ namespace gemm_epi {
 
 namespace {
 template <class Kern, class P>
-cudaError_t launch(Kern kern, int64_t grid, int threads, const P &p, bool pdl, cudaStream_t s) {
+cudaError_t launch(Kern kern, int64_t grid, int threads, const P &p, bool pdl, cudaStream_t s, int smem = 0) {
     cudaLaunchConfig_t cfg = {};
+    cfg.dynamicSmemBytes = (size_t)smem;
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.stream = s;
@@ -62,11 +64,27 @@ BwdShape bwd_shape(int64_t d) {
     if (nv <= 16) return {16, 1};
     if (nv <= 32) return {32, 1};
     if (nv <= 64) return {32, 2};
-    if (nv <= 128) return {32, 4};
+    if (nv <= 128) return {128, 1};
     if (nv <= 256) return {128, 2};
     if (nv <= 512) return {128, 4};
     if (nv <= 1024) return {256, 4};
     return {512, 4};
+}
+
+// Longer rows: the ring's depth, so that 512 threads an SM have 192 KB of it between them.
+template <int DT, int T, int VPT>
+cudaError_t bwd_rows(const NormBwdParams &p, int64_t grid, bool pdl, cudaStream_t s) {
+    constexpr int STAGES = 2, SMEM = STAGES * 3 * T * VPT * 16;
+    auto kern = rmsnorm_bwd_rows_kernel<DT, T, VPT, STAGES>;
+    static std::atomic<bool> attr_done[64];
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 0 || dev >= 64 || !attr_done[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev].store(true, std::memory_order_release);
+    }
+    return launch(kern, grid, T, p, pdl, s, SMEM);
 }
 
 template <int DT>
@@ -80,20 +98,18 @@ cudaError_t bwd(const NormBwdParams &p, bool pdl, cudaStream_t s) {
     GEMM_EPI_NORM_BWD(16, 1);
     GEMM_EPI_NORM_BWD(32, 1);
     GEMM_EPI_NORM_BWD(32, 2);
-    GEMM_EPI_NORM_BWD(32, 4);
-    GEMM_EPI_NORM_BWD(128, 2);
-    GEMM_EPI_NORM_BWD(128, 4);
-    GEMM_EPI_NORM_BWD(256, 4);
-    GEMM_EPI_NORM_BWD(512, 4);
 #undef GEMM_EPI_NORM_BWD
-    return cudaErrorInvalidValue;
+    if (b.tpr == 128 && b.vpt == 1) return bwd_rows<DT, 128, 1>(p, grid, pdl, s);
+    if (b.tpr == 128) return b.vpt == 2 ? bwd_rows<DT, 128, 2>(p, grid, pdl, s) : bwd_rows<DT, 128, 4>(p, grid, pdl, s);
+    return b.tpr == 256 ? bwd_rows<DT, 256, 4>(p, grid, pdl, s) : bwd_rows<DT, 512, 4>(p, grid, pdl, s);
 }
 }  // namespace
 
 int64_t norm_bwd_parts(int64_t m, int64_t d) {
-    const int threads = norm_threads(bwd_shape(d).tpr);
-    const int64_t rpb = threads / bwd_shape(d).tpr;
-    const int64_t resident = 148 * std::max(1, 512 / threads);     // a B200's SMs, 512 threads each
+    const BwdShape b = bwd_shape(d);
+    const int64_t rpb = norm_threads(b.tpr) / b.tpr;
+    // as many as a B200's 148 SMs hold at once
+    const int64_t resident = 148 * (b.tpr <= 32 ? 4 : norm_rows_per_sm(b.tpr, b.vpt));
     return std::min<int64_t>((m + rpb - 1) / rpb, resident);
 }
 

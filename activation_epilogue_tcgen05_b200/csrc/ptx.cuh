@@ -244,6 +244,13 @@ __device__ __forceinline__ void st_global_v4_hint(void *p, uint4 v, uint64_t pol
                  "r"(v.z), "r"(v.w), "l"(policy)
                  : "memory");
 }
+// 16-byte asynchronous copies of a thread's own (no copy in L1); committed and waited for in groups.
+__device__ __forceinline__ void cp_async_16(void *smem_dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem_dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void bulk_wait_read() {

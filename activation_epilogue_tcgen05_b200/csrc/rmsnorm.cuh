@@ -191,15 +191,16 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
     }
 }
 
-// Rows are dealt to the blocks' groups round-robin; each thread keeps the gain's gradient of
+// Backward of short rows (up to 512 elements: within a warp).  Rows are dealt to the blocks' groups
+// round-robin; each thread keeps the gain's gradient of
 // its columns in registers over its rows, and the block writes one partial row of d floats,
 // its groups added in order.  Which rows a partial holds depends on (m, d) alone, so dgamma is
 // the same from run to run.
 template <int DT, int TPR, int VPT>
-__global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_bwd_kernel(const NormBwdParams p) {
+__global__ void __launch_bounds__(norm_threads(TPR), 4) rmsnorm_bwd_kernel(const NormBwdParams p) {
+    static_assert(TPR <= 32, "rows of several warps: rmsnorm_bwd_rows_kernel");
     constexpr int RPB = norm_threads(TPR) / TPR;
-    __shared__ float2 red[2][RPB][TPR > 32 ? TPR / 32 : 1];
-    __shared__ float col[RPB > 1 ? TPR * VPT * 8 : 1];
+    __shared__ float col[TPR * VPT * 8];
     const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const int nvec = p.d / 8;
     ptx::griddep_wait();
@@ -214,9 +215,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_bwd_kernel(const No
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
     }
-    int buf = 0;
-    // (every group of a block makes the same number of turns: the reductions are block-wide)
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.m; row0 += (int64_t)gridDim.x * RPB, buf ^= 1) {
+    // (every group of a warp makes the same number of turns: the reductions are warp-wide)
+    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.m; row0 += (int64_t)gridDim.x * RPB) {
         const int64_t row = row0 + grp;
         const bool row_ok = row < p.m;
         const int64_t base = row * p.d;
@@ -244,7 +244,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_bwd_kernel(const No
                 c = fmaf(y[e] * g[e], s[e], c);
             }
         }
-        row_reduce<TPR, false>(ss, c, red[buf][grp]);
+        row_reduce<TPR, false>(ss, c, nullptr);
         const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
         const float k = rho * rho * (c * p.inv_d);
 #pragma unroll
@@ -266,29 +266,119 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_bwd_kernel(const No
     }
     if (p.partial == nullptr) return;
     float *out = p.partial + (int64_t)blockIdx.x * p.d;
-    if constexpr (RPB > 1) {
-        for (int g = 0; g < RPB; ++g) {
-            if (g == grp) {
+    for (int g = 0; g < RPB; ++g) {
+        if (g == grp) {
 #pragma unroll
-                for (int j = 0; j < VPT; ++j)
+            for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float &c = col[(j * TPR + t) * 8 + e];
-                        c = g == 0 ? acc[j][e] : c + acc[j][e];
-                    }
-            }
-            __syncthreads();
+                for (int e = 0; e < 8; ++e) {
+                    float &c = col[(j * TPR + t) * 8 + e];
+                    c = g == 0 ? acc[j][e] : c + acc[j][e];
+                }
         }
-        for (int i = threadIdx.x; i < p.d; i += norm_threads(TPR)) out[i] = col[i];
-    } else {
+        __syncthreads();
+    }
+    for (int i = threadIdx.x; i < p.d; i += norm_threads(TPR)) out[i] = col[i];
+}
+
+// Blocks of rmsnorm_bwd_rows_kernel that an SM holds at once.
+constexpr int norm_rows_per_sm(int t, int vpt) { return t > 128 ? 512 / t : vpt == 1 ? 8 : vpt == 2 ? 6 : 4; }
+
+// Backward of longer rows: a block of T threads takes one row at a time, its rows dealt round-robin.
+// Each thread copies its own vectors of the next rows into a ring of its own in shared memory
+// (cp.async, 16 bytes each) while it works on the present one, so that HBM is never waited for by
+// all of an SM's threads at once, nothing has to be held in registers across the reduction (the
+// second pass reads shared memory again), and no barrier guards the ring: nobody else reads it.
+template <int DT, int T, int VPT, int STAGES>
+__global__ void __launch_bounds__(T, norm_rows_per_sm(T, VPT)) rmsnorm_bwd_rows_kernel(const NormBwdParams p) {
+    constexpr int ARRAY = T * VPT;                    // vectors of one row of one array
+    extern __shared__ uint4 ring[];                   // [STAGES][dy, s, ds][ARRAY]
+    __shared__ float2 red[2][T / 32];
+    const int t = threadIdx.x, nvec = p.d / 8;
+    const bool skip = p.ds != nullptr;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    auto fetch = [&](int64_t row, int stage) {
+        if (row < p.m) {
+            const int64_t base = row * p.d;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                const int v = j * T + t;
+                if (v < nvec) {
+                    uint4 *dst = ring + stage * 3 * ARRAY + v;
+                    ptx::cp_async_16(dst, static_cast<const uint16_t *>(p.dy) + base + 8 * v);
+                    ptx::cp_async_16(dst + ARRAY, static_cast<const uint16_t *>(p.s) + base + 8 * v);
+                    if (skip) ptx::cp_async_16(dst + 2 * ARRAY, static_cast<const uint16_t *>(p.ds) + base + 8 * v);
+                }
+            }
+        }
+        ptx::cp_async_commit();                       // (an empty group keeps the count)
+    };
+    uint4 gv[VPT];
+    float acc[VPT][8];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * T + t;
+        gv[j] = v < nvec ? __ldg(static_cast<const uint4 *>(p.gamma) + v) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
+    }
+    int64_t row = blockIdx.x;
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) fetch(row + (int64_t)i * gridDim.x, i);
+    int stage = 0;
+    for (int buf = 0; row < p.m; row += gridDim.x, buf ^= 1) {
+        ptx::cp_async_wait<STAGES - 1>();
+        const uint4 *cur = ring + stage * 3 * ARRAY + t;
+        float ss = 0.0f, c = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = j * TPR + t;
-            if (v < nvec) {
-                float4 *o = reinterpret_cast<float4 *>(out + 8 * v);
-                o[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-                o[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+            if (j * T + t < nvec) {
+                float y[8], s[8], g[8];
+                unpack8<DT>(cur[j * T], y);
+                unpack8<DT>(cur[ARRAY + j * T], s);
+                unpack8<DT>(gv[j], g);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    ss = fmaf(s[e], s[e], ss);
+                    c = fmaf(y[e] * g[e], s[e], c);
+                }
             }
+        }
+        row_reduce<T, false>(ss, c, red[buf]);
+        const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+        const float k = rho * rho * (c * p.inv_d);
+        uint16_t *out = static_cast<uint16_t *>(p.dx) + row * p.d;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * T + t;
+            if (v < nvec) {
+                float y[8], s[8], g[8], o[8];
+                unpack8<DT>(cur[j * T], y);
+                unpack8<DT>(cur[ARRAY + j * T], s);
+                unpack8<DT>(gv[j], g);
+                unpack8<DT>(skip ? cur[2 * ARRAY + j * T] : make_uint4(0u, 0u, 0u, 0u), o);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    acc[j][e] = fmaf(y[e] * rho, s[e], acc[j][e]);
+                    o[e] = fmaf(rho, fmaf(-s[e], k, y[e] * g[e]), o[e]);
+                }
+                *reinterpret_cast<uint4 *>(out + 8 * v) = pack8<DT>(o);
+            }
+        }
+        fetch(row + (int64_t)STAGES * gridDim.x, stage);
+        if (++stage == STAGES) stage = 0;
+    }
+    ptx::cp_async_wait<0>();
+    if (p.partial == nullptr) return;
+    float *part = p.partial + (int64_t)blockIdx.x * p.d;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * T + t;
+        if (v < nvec) {
+            float4 *o = reinterpret_cast<float4 *>(part + 8 * v);
+            o[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+            o[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
         }
     }
 }

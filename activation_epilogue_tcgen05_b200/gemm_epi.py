@@ -84,6 +84,8 @@ _lock = threading.Lock()
 def lib():
     """Load libgemm_epi.so (raises RuntimeError when it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             if not os.path.exists(LIB_PATH):
@@ -511,9 +513,10 @@ def _device_and_stream(stream):
     """(current device index, raw stream): the device's current stream when none is given."""
     import torch
     device = torch.cuda.current_device()
-    if stream is None:
-        return device, torch.cuda.current_stream(device).cuda_stream
-    return device, getattr(stream, "cuda_stream", stream)
+    if stream is not None:
+        return device, getattr(stream, "cuda_stream", stream)
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # 0.1 us; a Stream object costs 1.3 us
+    return device, raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
 
 
 def _scratch(nbytes, device, stream):
