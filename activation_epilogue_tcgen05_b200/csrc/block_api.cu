@@ -90,8 +90,9 @@ int gemm_epi_rmsnorm(int64_t m, int64_t d, int dtype, int out_mode, float eps, c
     p.scale = d_scale;
     p.amax = out_mode == GEMM_EPI_NORM_E4M3 ? reinterpret_cast<unsigned int *>(d_amax) : nullptr;
     // the amax word is this call's maximum: start it at 0 (the kernel max-reduces into it)
-    if (p.amax && cudaMemsetAsync(p.amax, 0, sizeof(float), s) != cudaSuccess) return GEMM_EPI_ERR_CUDA;
-    return status(launch_rmsnorm(dtype == GEMM_EPI_F16 ? DT_F16 : DT_BF16, out_mode, p, pdl_enabled(), s));
+    const bool pdl = pdl_enabled();
+    if (p.amax && (rc = status(launch_zero_word(p.amax, pdl, s))) != GEMM_EPI_OK) return rc;
+    return status(launch_rmsnorm(dtype == GEMM_EPI_F16 ? DT_F16 : DT_BF16, out_mode, p, pdl, s));
 }
 
 int64_t gemm_epi_rmsnorm_workspace_bytes(int64_t m, int64_t d) {
@@ -125,7 +126,7 @@ int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void 
     const bool pdl = pdl_enabled();
     rc = status(launch_rmsnorm_bwd(dt, p, pdl, s));
     if (rc != GEMM_EPI_OK || !dgamma) return rc;
-    return status(launch_sum_parts_f32(dt, p.partial, norm_bwd_parts(m, d), d, dgamma, pdl, s));
+    return status(launch_add_parts(dt, p.partial, norm_bwd_parts(m, d), d, dgamma, pdl, s));
 }
 
 int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis) {
@@ -178,7 +179,9 @@ int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, 
     rc = status(launch_dact(dt, act, axis, p, pdl, s));
     if (rc != GEMM_EPI_OK || !dbias) return rc;
     const int64_t parts = axis == AXIS_COL ? (m + p.rows - 1) / p.rows : (n + DACT_COLS - 1) / DACT_COLS;
-    return status(launch_sum_parts_f32(dt, p.partial, parts, axis == AXIS_COL ? n : m, dbias, pdl, s));
+    const int64_t len = axis == AXIS_COL ? n : m;
+    return status(len % 8 == 0 ? launch_add_parts(dt, p.partial, parts, len, dbias, pdl, s)
+                               : launch_sum_parts_f32(dt, p.partial, parts, len, dbias, pdl, s));      // ROW, odd m
 }
 
 }  // extern "C"

@@ -8,8 +8,8 @@
 namespace gemm_epi {
 
 namespace {
-template <class Kern, class P>
-cudaError_t launch(Kern kern, int64_t grid, int threads, const P &p, bool pdl, cudaStream_t s, int smem = 0) {
+template <class... A, class... P>
+cudaError_t launch_as(void (*kern)(A...), int64_t grid, int threads, int smem, bool pdl, cudaStream_t s, P... p) {
     cudaLaunchConfig_t cfg = {};
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.gridDim = dim3((unsigned)grid, 1, 1);
@@ -22,24 +22,35 @@ cudaError_t launch(Kern kern, int64_t grid, int threads, const P &p, bool pdl, c
         cfg.attrs = attr;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, kern, p);
+    return cudaLaunchKernelEx(&cfg, kern, p...);
 }
 
 template <int DT, int OUT, int TPR, int VPT>
 cudaError_t fwd(const NormParams &p, bool pdl, cudaStream_t s) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR;
-    return launch(rmsnorm_kernel<DT, OUT, TPR, VPT>, (p.m + RPB - 1) / RPB, T, p, pdl, s);
+    return launch_as(rmsnorm_kernel<DT, OUT, TPR, VPT>, (p.m + RPB - 1) / RPB, T, 0, pdl, s, p);
 }
+
+// Whether the rows are few: fewer vectors of 8 than one to each thread that the GPU holds.
+bool few_rows(int64_t m, int64_t d) { return m * (d / 8) <= 148 * 2048; }
 
 template <int DT, int OUT>
 cudaError_t fwd_shape(const NormParams &p, bool pdl, cudaStream_t s) {
     const int nv = p.d / 8;
-    if (nv <= 8) return fwd<DT, OUT, 8, 1>(p, pdl, s);
-    if (nv <= 16) return fwd<DT, OUT, 16, 1>(p, pdl, s);
-    if (nv <= 32) return fwd<DT, OUT, 32, 1>(p, pdl, s);
-    if (nv <= 64) return fwd<DT, OUT, 32, 2>(p, pdl, s);
+    if (few_rows(p.m, p.d)) {
+        if (nv <= 8) return fwd<DT, OUT, 8, 1>(p, pdl, s);
+        if (nv <= 32) return fwd<DT, OUT, 32, 1>(p, pdl, s);
+        if (nv <= 128) return fwd<DT, OUT, 128, 1>(p, pdl, s);
+        if (nv <= 512) return fwd<DT, OUT, 512, 1>(p, pdl, s);
+        if (nv <= 1024) return fwd<DT, OUT, 1024, 1>(p, pdl, s);
+        return fwd<DT, OUT, 1024, 2>(p, pdl, s);
+    }
+    if (nv <= 8) return fwd<DT, OUT, 2, 4>(p, pdl, s);
+    if (nv <= 16) return fwd<DT, OUT, 4, 4>(p, pdl, s);
+    if (nv <= 32) return fwd<DT, OUT, 8, 4>(p, pdl, s);
+    if (nv <= 64) return fwd<DT, OUT, 16, 4>(p, pdl, s);
     if (nv <= 128) return fwd<DT, OUT, 32, 4>(p, pdl, s);
-    if (nv <= 256) return fwd<DT, OUT, 128, 2>(p, pdl, s);
+    if (nv <= 256) return fwd<DT, OUT, 64, 4>(p, pdl, s);
     if (nv <= 512) return fwd<DT, OUT, 128, 4>(p, pdl, s);
     if (nv <= 1024) return fwd<DT, OUT, 256, 4>(p, pdl, s);
     return fwd<DT, OUT, 512, 4>(p, pdl, s);
@@ -54,28 +65,34 @@ cudaError_t fwd_out(int out, const NormParams &p, bool pdl, cudaStream_t s) {
     }
 }
 
-// Threads a row and vectors a thread of the backward kernel for rows of d elements.
+// Threads a row and vectors a thread of the backward kernel.
 struct BwdShape {
     int tpr, vpt;
 };
-BwdShape bwd_shape(int64_t d) {
+BwdShape bwd_shape(int64_t m, int64_t d) {
     const int64_t nv = d / 8;
-    if (nv <= 8) return {8, 1};
-    if (nv <= 16) return {16, 1};
-    if (nv <= 32) return {32, 1};
-    if (nv <= 64) return {32, 2};
-    if (nv <= 128) return {128, 1};
-    if (nv <= 256) return {128, 2};
+    if (few_rows(m, d)) {
+        if (nv <= 8) return {8, 1};
+        if (nv <= 32) return {32, 1};
+        if (nv <= 128) return {128, 1};
+        if (nv <= 512) return {512, 1};
+        return {512, 4};
+    }
+    if (nv <= 8) return {2, 4};
+    if (nv <= 16) return {4, 4};
+    if (nv <= 32) return {8, 4};
+    if (nv <= 64) return {16, 4};
+    if (nv <= 128) return {32, 4};
+    if (nv <= 256) return {64, 4};
     if (nv <= 512) return {128, 4};
     if (nv <= 1024) return {256, 4};
     return {512, 4};
 }
 
-// Longer rows: the ring's depth, so that 512 threads an SM have 192 KB of it between them.
-template <int DT, int T, int VPT>
-cudaError_t bwd_rows(const NormBwdParams &p, int64_t grid, bool pdl, cudaStream_t s) {
-    constexpr int STAGES = 2, SMEM = STAGES * 3 * T * VPT * 16;
-    auto kern = rmsnorm_bwd_rows_kernel<DT, T, VPT, STAGES>;
+template <int DT, int TPR, int VPT>
+cudaError_t bwd_one(const NormBwdParams &p, int64_t grid, bool pdl, cudaStream_t s) {
+    constexpr int T = norm_bwd_threads(TPR, VPT), SMEM = norm_ring_bytes(T, VPT);
+    auto kern = rmsnorm_bwd_kernel<DT, TPR, VPT>;
     static std::atomic<bool> attr_done[64];
     int dev = 0;
     cudaGetDevice(&dev);
@@ -84,33 +101,46 @@ cudaError_t bwd_rows(const NormBwdParams &p, int64_t grid, bool pdl, cudaStream_
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_done[dev].store(true, std::memory_order_release);
     }
-    return launch(kern, grid, T, p, pdl, s, SMEM);
+    return launch_as(kern, grid, T, SMEM, pdl, s, p);
 }
 
 template <int DT>
 cudaError_t bwd(const NormBwdParams &p, bool pdl, cudaStream_t s) {
-    const BwdShape b = bwd_shape(p.d);
+    const BwdShape b = bwd_shape(p.m, p.d);
     const int64_t grid = norm_bwd_parts(p.m, p.d);
-    const int threads = norm_threads(b.tpr);
-#define GEMM_EPI_NORM_BWD(T, V) \
-    if (b.tpr == T && b.vpt == V) return launch(rmsnorm_bwd_kernel<DT, T, V>, grid, threads, p, pdl, s)
-    GEMM_EPI_NORM_BWD(8, 1);
-    GEMM_EPI_NORM_BWD(16, 1);
-    GEMM_EPI_NORM_BWD(32, 1);
-    GEMM_EPI_NORM_BWD(32, 2);
-#undef GEMM_EPI_NORM_BWD
-    if (b.tpr == 128 && b.vpt == 1) return bwd_rows<DT, 128, 1>(p, grid, pdl, s);
-    if (b.tpr == 128) return b.vpt == 2 ? bwd_rows<DT, 128, 2>(p, grid, pdl, s) : bwd_rows<DT, 128, 4>(p, grid, pdl, s);
-    return b.tpr == 256 ? bwd_rows<DT, 256, 4>(p, grid, pdl, s) : bwd_rows<DT, 512, 4>(p, grid, pdl, s);
+    if (b.vpt == 1) {
+        switch (b.tpr) {
+        case 8: return bwd_one<DT, 8, 1>(p, grid, pdl, s);
+        case 32: return bwd_one<DT, 32, 1>(p, grid, pdl, s);
+        case 128: return bwd_one<DT, 128, 1>(p, grid, pdl, s);
+        default: return bwd_one<DT, 512, 1>(p, grid, pdl, s);
+        }
+    }
+    switch (b.tpr) {
+    case 2: return bwd_one<DT, 2, 4>(p, grid, pdl, s);
+    case 4: return bwd_one<DT, 4, 4>(p, grid, pdl, s);
+    case 8: return bwd_one<DT, 8, 4>(p, grid, pdl, s);
+    case 16: return bwd_one<DT, 16, 4>(p, grid, pdl, s);
+    case 32: return bwd_one<DT, 32, 4>(p, grid, pdl, s);
+    case 64: return bwd_one<DT, 64, 4>(p, grid, pdl, s);
+    case 128: return bwd_one<DT, 128, 4>(p, grid, pdl, s);
+    case 256: return bwd_one<DT, 256, 4>(p, grid, pdl, s);
+    default: return bwd_one<DT, 512, 4>(p, grid, pdl, s);
+    }
+}
+// Sets the word that a launch max-reduces into to 0: a launch of the library's own, since a memset
+// between two launches keeps the second from being set up during the first (4 us a call).
+__global__ void zero_word_kernel(unsigned int *w) {
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    if (threadIdx.x == 0) *w = 0u;
 }
 }  // namespace
 
 int64_t norm_bwd_parts(int64_t m, int64_t d) {
-    const BwdShape b = bwd_shape(d);
-    const int64_t rpb = norm_threads(b.tpr) / b.tpr;
-    // as many as a B200's 148 SMs hold at once
-    const int64_t resident = 148 * (b.tpr <= 32 ? 4 : norm_rows_per_sm(b.tpr, b.vpt));
-    return std::min<int64_t>((m + rpb - 1) / rpb, resident);
+    const BwdShape b = bwd_shape(m, d);
+    const int rpb = norm_bwd_threads(b.tpr, b.vpt) / b.tpr;
+    return std::min<int64_t>((m + rpb - 1) / rpb, NORM_BWD_BLOCKS);
 }
 
 cudaError_t launch_rmsnorm(int dt, int out, const NormParams &p, bool pdl, cudaStream_t s) {
@@ -119,6 +149,22 @@ cudaError_t launch_rmsnorm(int dt, int out, const NormParams &p, bool pdl, cudaS
 
 cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStream_t s) {
     return dt == DT_F16 ? bwd<DT_F16>(p, pdl, s) : bwd<DT_BF16>(p, pdl, s);
+}
+
+namespace {
+template <int DT>
+cudaError_t add_parts(const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s) {
+    if (parts <= 320) return launch_as(add_parts_kernel<DT, 32>, (len + 31) / 32, 256, 0, pdl, s, src, parts, len, out);
+    return launch_as(add_parts_kernel<DT, 64>, (len + 31) / 32, 512, 0, pdl, s, src, parts, len, out);
+}
+}  // namespace
+
+cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s) {
+    return dt == DT_F16 ? add_parts<DT_F16>(src, parts, len, out, pdl, s) : add_parts<DT_BF16>(src, parts, len, out, pdl, s);
+}
+
+cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s) {
+    return launch_as(zero_word_kernel, 1, 32, 0, pdl, s, w);
 }
 
 }  // namespace gemm_epi

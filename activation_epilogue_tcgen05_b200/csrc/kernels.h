@@ -89,6 +89,9 @@ constexpr int NORM_MAX_D = 16384;
 int64_t norm_bwd_parts(int64_t m, int64_t d);
 cudaError_t launch_rmsnorm(int dt, int out, const NormParams &p, bool pdl, cudaStream_t s);
 cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStream_t s);
+// out[i] = sum_p src[p * len + i], fp32 partials, len a multiple of 8, out in dt
+cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s);
+cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s);
 // rows of a block's run, from (m, n) alone; the launch has ceil(m / rows) runs
 int64_t dact_rows(int64_t m, int64_t n);
 cudaError_t launch_dact(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s);

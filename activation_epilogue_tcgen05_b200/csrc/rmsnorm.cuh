@@ -20,7 +20,9 @@
 //
 // Both are bound by HBM: a row is read once, held in registers as fp32 (forward) or packed
 // (backward), reduced, and written once.  A row is shared by TPR threads, each holding VPT
-// vectors of 8 elements (16-byte loads, neighbouring threads on neighbouring vectors).
+// vectors of 8 elements (16-byte loads, neighbouring threads on neighbouring vectors): four
+// vectors a thread where there are rows enough to fill the GPU, so that a thread has many loads in
+// flight and a block enough work; one where there are few, so that a row is done soonest.
 #pragma once
 #include <cstdint>
 
@@ -70,9 +72,10 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 
 // Sum of `a` and combination of `b` (maximum, or sum) over the TPR threads of a row, the same
 // bits in each of them.  Rows of up to 32 threads use an xor butterfly (every lane of the warp
-// takes part, with whatever row it has); longer ones add their warps' results in warp order.
-template <int TPR, bool BMAX>
-__device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red) {
+// takes part, with whatever row it has); longer ones add their warps' results in warp order, and wait
+// for their own TPR threads only (barrier 1 + grp) where a block of T threads has several rows.
+template <int TPR, int T, bool BMAX>
+__device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red, int grp) {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
     for (int sh = W / 2; sh >= 1; sh >>= 1) {
@@ -83,7 +86,8 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red) {
     if constexpr (TPR > 32) {
         constexpr int NW = TPR / 32;
         if ((threadIdx.x & 31) == 0) red[(threadIdx.x % TPR) >> 5] = make_float2(a, b);
-        __syncthreads();
+        if constexpr (TPR == T) __syncthreads();
+        else ptx::named_bar_sync(1 + grp, TPR);
         float2 t = red[0];
         a = t.x;
         b = t.y;
@@ -96,6 +100,7 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red) {
     }
 }
 
+// Threads of a block: one row, or as many short ones as make 128 threads.
 constexpr int norm_threads(int tpr) { return tpr > 128 ? tpr : 128; }
 
 template <int DT, int OUT, int TPR, int VPT>
@@ -152,15 +157,16 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
             }
         }
     }
-    row_reduce<TPR, true>(ss, top, red[grp]);
+    row_reduce<TPR, norm_threads(TPR), true>(ss, top, red[grp], grp);
     const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
     float mul = rho;
     if constexpr (OUT == NORM_E4M3) {
         mul = rho / __ldg(p.scale);
-        if (p.amax != nullptr && t == 0 && row_ok) {
-            // most rows are below the maximum so far: they only read it
-            const unsigned int a = __float_as_uint(rho * top);
-            if (a > *reinterpret_cast<volatile unsigned int *>(p.amax)) atomicMax(p.amax, a);
+        if (p.amax != nullptr && (TPR <= 32 || t < 32)) {
+            // one word a warp (rows past the last hold zeros); most are below the maximum so far and
+            // only read it
+            const unsigned int a = __reduce_max_sync(0xffffffffu, __float_as_uint(rho * top));
+            if ((threadIdx.x & 31) == 0 && a > *reinterpret_cast<volatile unsigned int *>(p.amax)) atomicMax(p.amax, a);
         }
     } else if constexpr (OUT == NORM_E4M3_ROWS) {
         // 448 / top overflows below 1.4e-36; such a row is one of zeros in e4m3 at any scale in use
@@ -191,110 +197,31 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
     }
 }
 
-// Backward of short rows (up to 512 elements: within a warp).  Rows are dealt to the blocks' groups
-// round-robin; each thread keeps the gain's gradient of
-// its columns in registers over its rows, and the block writes one partial row of d floats,
-// its groups added in order.  Which rows a partial holds depends on (m, d) alone, so dgamma is
-// the same from run to run.
-template <int DT, int TPR, int VPT>
-__global__ void __launch_bounds__(norm_threads(TPR), 4) rmsnorm_bwd_kernel(const NormBwdParams p) {
-    static_assert(TPR <= 32, "rows of several warps: rmsnorm_bwd_rows_kernel");
-    constexpr int RPB = norm_threads(TPR) / TPR;
-    __shared__ float col[TPR * VPT * 8];
-    const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
-    const int nvec = p.d / 8;
-    ptx::griddep_wait();
-    ptx::griddep_launch_dependents();
-
-    uint4 gv[VPT];
-    float acc[VPT][8];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int v = j * TPR + t;
-        gv[j] = v < nvec ? __ldg(static_cast<const uint4 *>(p.gamma) + v) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
-    }
-    // (every group of a warp makes the same number of turns: the reductions are warp-wide)
-    for (int64_t row0 = (int64_t)blockIdx.x * RPB; row0 < p.m; row0 += (int64_t)gridDim.x * RPB) {
-        const int64_t row = row0 + grp;
-        const bool row_ok = row < p.m;
-        const int64_t base = row * p.d;
-        uint4 yv[VPT], sv[VPT], dv[VPT];
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = j * TPR + t;
-            yv[j] = sv[j] = dv[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (row_ok && v < nvec) {
-                yv[j] = ld_stream(static_cast<const uint16_t *>(p.dy) + base + 8 * v);
-                sv[j] = ld_stream(static_cast<const uint16_t *>(p.s) + base + 8 * v);
-                if (p.ds != nullptr) dv[j] = ld_stream(static_cast<const uint16_t *>(p.ds) + base + 8 * v);
-            }
-        }
-        float ss = 0.0f, c = 0.0f;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            float y[8], s[8], g[8];
-            unpack8<DT>(yv[j], y);
-            unpack8<DT>(sv[j], s);
-            unpack8<DT>(gv[j], g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ss = fmaf(s[e], s[e], ss);
-                c = fmaf(y[e] * g[e], s[e], c);
-            }
-        }
-        row_reduce<TPR, false>(ss, c, nullptr);
-        const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-        const float k = rho * rho * (c * p.inv_d);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int v = j * TPR + t;
-            float y[8], s[8], g[8], o[8];
-            unpack8<DT>(yv[j], y);
-            unpack8<DT>(sv[j], s);
-            unpack8<DT>(gv[j], g);
-            unpack8<DT>(dv[j], o);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc[j][e] = fmaf(y[e] * rho, s[e], acc[j][e]);
-                o[e] = fmaf(rho, fmaf(-s[e], k, y[e] * g[e]), o[e]);
-            }
-            if (row_ok && v < nvec)
-                *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dx) + base + 8 * v) = pack8<DT>(o);
-        }
-    }
-    if (p.partial == nullptr) return;
-    float *out = p.partial + (int64_t)blockIdx.x * p.d;
-    for (int g = 0; g < RPB; ++g) {
-        if (g == grp) {
-#pragma unroll
-            for (int j = 0; j < VPT; ++j)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    float &c = col[(j * TPR + t) * 8 + e];
-                    c = g == 0 ? acc[j][e] : c + acc[j][e];
-                }
-        }
-        __syncthreads();
-    }
-    for (int i = threadIdx.x; i < p.d; i += norm_threads(TPR)) out[i] = col[i];
-}
-
-// Blocks of rmsnorm_bwd_rows_kernel that an SM holds at once.
-constexpr int norm_rows_per_sm(int t, int vpt) { return t > 128 ? 512 / t : vpt == 1 ? 8 : vpt == 2 ? 6 : 4; }
-
-// Backward of longer rows: a block of T threads takes one row at a time, its rows dealt round-robin.
+// Backward.  Rows are dealt to the blocks' groups of TPR threads round-robin; each thread keeps the
+// gain's gradient of its columns in registers over its rows, and the block writes one partial row of
+// d floats, its groups added in order.  Which rows a partial holds depends on (m, d) alone, so dgamma
+// is the same from run to run.
+//
 // Each thread copies its own vectors of the next rows into a ring of its own in shared memory
 // (cp.async, 16 bytes each) while it works on the present one, so that HBM is never waited for by
 // all of an SM's threads at once, nothing has to be held in registers across the reduction (the
 // second pass reads shared memory again), and no barrier guards the ring: nobody else reads it.
-template <int DT, int T, int VPT, int STAGES>
-__global__ void __launch_bounds__(T, norm_rows_per_sm(T, VPT)) rmsnorm_bwd_rows_kernel(const NormBwdParams p) {
-    constexpr int ARRAY = T * VPT;                    // vectors of one row of one array
-    extern __shared__ uint4 ring[];                   // [STAGES][dy, s, ds][ARRAY]
-    __shared__ float2 red[2][T / 32];
-    const int t = threadIdx.x, nvec = p.d / 8;
+constexpr int NORM_RING = 2;                          // rows of a group in the ring
+constexpr int norm_ring_bytes(int threads, int vpt) { return NORM_RING * 3 * threads * vpt * 16; }
+// Four vectors a thread: one block of 512 threads an SM, so that there are few partial rows to add up
+// (148; with blocks of 128 threads, 592 of them made the second launch 3 us longer at d = 4096).
+// One vector a thread (few rows): blocks of one row or 128 threads, again one an SM.
+constexpr int norm_bwd_threads(int tpr, int vpt) { return vpt == 1 ? norm_threads(tpr) : 512; }
+constexpr int NORM_BWD_BLOCKS = 148;                  // a B200's SMs
+
+template <int DT, int TPR, int VPT>
+__global__ void __launch_bounds__(norm_bwd_threads(TPR, VPT), 1)
+    rmsnorm_bwd_kernel(const NormBwdParams p) {
+    constexpr int T = norm_bwd_threads(TPR, VPT), RPB = T / TPR;
+    constexpr int ARRAY = T * VPT;                    // vectors of one array in a stage of the ring
+    extern __shared__ uint4 ring[];                   // [NORM_RING][dy, s, ds][vector][thread]
+    __shared__ float2 red[2][RPB][TPR > 32 ? TPR / 32 : 1];
+    const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR, nvec = p.d / 8;
     const bool skip = p.ds != nullptr;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
@@ -303,9 +230,9 @@ __global__ void __launch_bounds__(T, norm_rows_per_sm(T, VPT)) rmsnorm_bwd_rows_
             const int64_t base = row * p.d;
 #pragma unroll
             for (int j = 0; j < VPT; ++j) {
-                const int v = j * T + t;
+                const int v = j * TPR + t;
                 if (v < nvec) {
-                    uint4 *dst = ring + stage * 3 * ARRAY + v;
+                    uint4 *dst = ring + stage * 3 * ARRAY + j * T + threadIdx.x;
                     ptx::cp_async_16(dst, static_cast<const uint16_t *>(p.dy) + base + 8 * v);
                     ptx::cp_async_16(dst + ARRAY, static_cast<const uint16_t *>(p.s) + base + 8 * v);
                     if (skip) ptx::cp_async_16(dst + 2 * ARRAY, static_cast<const uint16_t *>(p.ds) + base + 8 * v);
@@ -318,22 +245,26 @@ __global__ void __launch_bounds__(T, norm_rows_per_sm(T, VPT)) rmsnorm_bwd_rows_
     float acc[VPT][8];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        const int v = j * T + t;
+        const int v = j * TPR + t;
         gv[j] = v < nvec ? __ldg(static_cast<const uint4 *>(p.gamma) + v) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[j][e] = 0.0f;
     }
-    int64_t row = blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * RPB;
+    int64_t row0 = (int64_t)blockIdx.x * RPB;
 #pragma unroll
-    for (int i = 0; i < STAGES; ++i) fetch(row + (int64_t)i * gridDim.x, i);
+    for (int i = 0; i < NORM_RING; ++i) fetch(row0 + grp + i * step, i);
     int stage = 0;
-    for (int buf = 0; row < p.m; row += gridDim.x, buf ^= 1) {
-        ptx::cp_async_wait<STAGES - 1>();
-        const uint4 *cur = ring + stage * 3 * ARRAY + t;
+    // (every group of a block makes the same number of turns: short rows share a warp's shuffles)
+    for (int buf = 0; row0 < p.m; row0 += step, buf ^= 1) {
+        const int64_t row = row0 + grp;
+        const bool row_ok = row < p.m;
+        ptx::cp_async_wait<NORM_RING - 1>();
+        const uint4 *cur = ring + stage * 3 * ARRAY + threadIdx.x;
         float ss = 0.0f, c = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (j * T + t < nvec) {
+            if (row_ok && j * TPR + t < nvec) {
                 float y[8], s[8], g[8];
                 unpack8<DT>(cur[j * T], y);
                 unpack8<DT>(cur[ARRAY + j * T], s);
@@ -345,14 +276,14 @@ __global__ void __launch_bounds__(T, norm_rows_per_sm(T, VPT)) rmsnorm_bwd_rows_
                 }
             }
         }
-        row_reduce<T, false>(ss, c, red[buf]);
+        row_reduce<TPR, T, false>(ss, c, red[buf][grp], grp);
         const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
         const float k = rho * rho * (c * p.inv_d);
         uint16_t *out = static_cast<uint16_t *>(p.dx) + row * p.d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int v = j * T + t;
-            if (v < nvec) {
+            const int v = j * TPR + t;
+            if (row_ok && v < nvec) {
                 float y[8], s[8], g[8], o[8];
                 unpack8<DT>(cur[j * T], y);
                 unpack8<DT>(cur[ARRAY + j * T], s);
@@ -366,20 +297,116 @@ __global__ void __launch_bounds__(T, norm_rows_per_sm(T, VPT)) rmsnorm_bwd_rows_
                 *reinterpret_cast<uint4 *>(out + 8 * v) = pack8<DT>(o);
             }
         }
-        fetch(row + (int64_t)STAGES * gridDim.x, stage);
-        if (++stage == STAGES) stage = 0;
+        fetch(row + NORM_RING * step, stage);
+        if (++stage == NORM_RING) stage = 0;
     }
     ptx::cp_async_wait<0>();
     if (p.partial == nullptr) return;
     float *part = p.partial + (int64_t)blockIdx.x * p.d;
+    if constexpr (RPB > 1) {
+        // a warp's groups by butterflies, then the block's through the ring, in order:
+        // [group][half of a vector][vector], so that neighbouring threads are on neighbouring words
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int v = j * T + t;
-        if (v < nvec) {
-            float4 *o = reinterpret_cast<float4 *>(part + 8 * v);
-            o[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
-            o[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+        for (int sh = TPR; sh < 32; sh <<= 1)
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) acc[j][e] += __shfl_xor_sync(0xffffffffu, acc[j][e], sh);
+        constexpr int W = TPR < 32 ? 32 : TPR, G = T / W, V = VPT * TPR;
+        float4 *sums = reinterpret_cast<float4 *>(ring);
+        static_assert(2 * V * G <= NORM_RING * 3 * ARRAY, "the ring holds every group's sums");
+        __syncthreads();
+        if (threadIdx.x % W < TPR) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    sums[(threadIdx.x / W * 2 + h) * V + j * TPR + t] =
+                        make_float4(acc[j][4 * h], acc[j][4 * h + 1], acc[j][4 * h + 2], acc[j][4 * h + 3]);
         }
+        __syncthreads();
+        for (int i = threadIdx.x; i < 2 * nvec; i += T) {
+            const float4 *src = sums + (i & 1) * V + (i >> 1);
+            float4 a = src[0];
+#pragma unroll
+            for (int g = 1; g < G; ++g) {
+                const float4 b = src[2 * V * g];
+                a.x += b.x;
+                a.y += b.y;
+                a.z += b.z;
+                a.w += b.w;
+            }
+            reinterpret_cast<float4 *>(part)[i] = a;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * TPR + t;
+            if (v < nvec) {
+                float4 *o = reinterpret_cast<float4 *>(part + 8 * v);
+                o[0] = make_float4(acc[j][0], acc[j][1], acc[j][2], acc[j][3]);
+                o[1] = make_float4(acc[j][4], acc[j][5], acc[j][6], acc[j][7]);
+            }
+        }
+    }
+}
+
+// out[i] = sum_p src[p * len + i] over fp32 partials, len a multiple of 8.  A block takes 32 outputs:
+// thread (x, y) adds parts y, y + Y, ... of four neighbouring outputs, ten loads in flight (it is
+// latency that counts here: all of a thread's loads should go out at once), then the Y sums are added in
+// a fixed tree; the order depends on (parts, len) alone.
+template <int DT, int Y>
+__global__ void __launch_bounds__(8 * Y) add_parts_kernel(const float *__restrict__ src, int64_t parts, int64_t len,
+                                                          void *out) {
+    constexpr int U = 10;
+    __shared__ float4 red[Y][8];
+    const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
+    const int64_t i = (int64_t)blockIdx.x * 32 + 4 * x;
+    ptx::griddep_wait();
+    ptx::griddep_launch_dependents();
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (i < len) {
+        const float4 *s4 = reinterpret_cast<const float4 *>(src + i);
+        const int64_t pitch = len / 4;
+        for (int64_t p0 = y; p0 < parts; p0 += U * Y) {
+            float4 v[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                v[u] = p0 + Y * u < parts ? __ldcg(s4 + (p0 + Y * u) * pitch) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                a.x += v[u].x;
+                a.y += v[u].y;
+                a.z += v[u].z;
+                a.w += v[u].w;
+            }
+        }
+    }
+    red[y][x] = a;
+    __syncthreads();
+    // a warp an output quad: Y / 32 of its sums a lane, then a butterfly over the lanes
+    const int q = threadIdx.x >> 5, l = threadIdx.x & 31;
+    if (q < 8) {
+        float4 s = red[l][q];
+#pragma unroll
+        for (int k = 1; k < Y / 32; ++k) {
+            const float4 b = red[l + 32 * k][q];
+            s.x += b.x;
+            s.y += b.y;
+            s.z += b.z;
+            s.w += b.w;
+        }
+#pragma unroll
+        for (int sh = 16; sh >= 1; sh >>= 1) {
+            s.x += __shfl_xor_sync(0xffffffffu, s.x, sh);
+            s.y += __shfl_xor_sync(0xffffffffu, s.y, sh);
+            s.z += __shfl_xor_sync(0xffffffffu, s.z, sh);
+            s.w += __shfl_xor_sync(0xffffffffu, s.w, sh);
+        }
+        const int64_t o = (int64_t)blockIdx.x * 32 + 4 * q;
+        if (l == 0 && o < len)
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + o) =
+                make_uint2(OutT<DT>::pack(s.x, s.y), OutT<DT>::pack(s.z, s.w));
     }
 }
 

@@ -443,7 +443,7 @@ enum gemm_epi_norm_out {
  * All arithmetic is fp32, and the norm is taken of the unrounded sum; y and s are rounded to
  * nearest even once, an e4m3 y saturates at +-448.  Inputs are finite, and a row's sum of squares
  * stays below the largest fp32 number.  Every pointer is 16-byte aligned (d_scale and d_amax:
- * 4-byte).  One launch (after a memset when d_amax is given), nothing allocated, any stream;
+ * 4-byte).  One launch (two with d_amax), nothing allocated, any stream;
  * calls may overlap as far as their buffers do.  Returns OK, ERR_ARG (a size, type, mode or eps
  * out of range; S without R; buffers that may not coincide), ERR_ALIGN, ERR_NULL,
  * ERR_UNSUPPORTED, ERR_NO_DEVICE or ERR_CUDA.  (The pages name LayerNorm among what surrounds
