@@ -31,21 +31,14 @@ cudaError_t fwd(const NormParams &p, bool pdl, cudaStream_t s) {
     return launch_as(rmsnorm_kernel<DT, OUT, TPR, VPT>, (p.m + RPB - 1) / RPB, T, 0, pdl, s, p);
 }
 
-// Whether the rows are few: fewer vectors of 8 than one to each thread that the GPU holds.
-bool few_rows(int64_t m, int64_t d) { return m * (d / 8) <= 148 * 2048; }
-
+// Four vectors a thread at every size: with one vector and more threads few rows were not done
+// sooner (1 x 4096 1.4 us either way, 300 x 4096 2.3 against 3.1 us) and many were slower (65536 x
+// 256 without a residual 12.4 against 17.4 us).  Rows of up to 64 take two, so that a row's threads still
+// read 64 bytes at a time (262144 x 64 with a residual 21.2 us, with four 25.9).
 template <int DT, int OUT>
 cudaError_t fwd_shape(const NormParams &p, bool pdl, cudaStream_t s) {
     const int nv = p.d / 8;
-    if (few_rows(p.m, p.d)) {
-        if (nv <= 8) return fwd<DT, OUT, 8, 1>(p, pdl, s);
-        if (nv <= 32) return fwd<DT, OUT, 32, 1>(p, pdl, s);
-        if (nv <= 128) return fwd<DT, OUT, 128, 1>(p, pdl, s);
-        if (nv <= 512) return fwd<DT, OUT, 512, 1>(p, pdl, s);
-        if (nv <= 1024) return fwd<DT, OUT, 1024, 1>(p, pdl, s);
-        return fwd<DT, OUT, 1024, 2>(p, pdl, s);
-    }
-    if (nv <= 8) return fwd<DT, OUT, 2, 4>(p, pdl, s);
+    if (nv <= 8) return fwd<DT, OUT, 4, 2>(p, pdl, s);
     if (nv <= 16) return fwd<DT, OUT, 4, 4>(p, pdl, s);
     if (nv <= 32) return fwd<DT, OUT, 8, 4>(p, pdl, s);
     if (nv <= 64) return fwd<DT, OUT, 16, 4>(p, pdl, s);
@@ -65,6 +58,11 @@ cudaError_t fwd_out(int out, const NormParams &p, bool pdl, cudaStream_t s) {
     }
 }
 
+// Whether a backward call has few rows: up to one vector of 8 to each of 1024 threads an SM.  Then a
+// thread takes one vector, so that a row is done soonest (37 x 1000: 3.2 us, with four vectors 6.2;
+// 64 x 4096 4.7 against 6.0); above, four (300 x 4096 the same, 1200 x 1024 6.3 against 6.7).
+bool few_rows(int64_t m, int64_t d) { return m * (d / 8) <= 148 * 1024; }
+
 // Threads a row and vectors a thread of the backward kernel.
 struct BwdShape {
     int tpr, vpt;
@@ -78,7 +76,7 @@ BwdShape bwd_shape(int64_t m, int64_t d) {
         if (nv <= 512) return {512, 1};
         return {512, 4};
     }
-    if (nv <= 8) return {2, 4};
+    if (nv <= 8) return {4, 2};
     if (nv <= 16) return {4, 4};
     if (nv <= 32) return {8, 4};
     if (nv <= 64) return {16, 4};
@@ -117,8 +115,7 @@ cudaError_t bwd(const NormBwdParams &p, bool pdl, cudaStream_t s) {
         }
     }
     switch (b.tpr) {
-    case 2: return bwd_one<DT, 2, 4>(p, grid, pdl, s);
-    case 4: return bwd_one<DT, 4, 4>(p, grid, pdl, s);
+    case 4: return b.vpt == 2 ? bwd_one<DT, 4, 2>(p, grid, pdl, s) : bwd_one<DT, 4, 4>(p, grid, pdl, s);
     case 8: return bwd_one<DT, 8, 4>(p, grid, pdl, s);
     case 16: return bwd_one<DT, 16, 4>(p, grid, pdl, s);
     case 32: return bwd_one<DT, 32, 4>(p, grid, pdl, s);

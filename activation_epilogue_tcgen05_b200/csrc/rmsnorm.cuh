@@ -101,7 +101,7 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red, int 
 }
 
 // Threads of a block: one row, or as many short ones as make 128 threads.
-constexpr int norm_threads(int tpr) { return tpr > 128 ? tpr : 128; }
+constexpr int norm_threads(int tpr) { return tpr > 32 ? tpr : 128; }
 
 template <int DT, int OUT, int TPR, int VPT>
 __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormParams p) {
