@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, 4) dact_kernel(const DactPara
             dv[u] = zv[u] = make_uint4(0u, 0u, 0u, 0u);
             mv[u] = 0u;
             if (i < r1 && col_ok) {
-                dv[u] = ld_stream(static_cast<const uint16_t *>(p.dd) + i * p.n + col);
+                dv[u] = ptx::ld_stream(static_cast<const uint16_t *>(p.dd) + i * p.n + col);
                 if constexpr (ACT == DACT_RELU_MASK) mv[u] = __ldg(p.aux + i * p.aux_pitch + col / 8);
-                else if constexpr (ACT != DACT_NONE) zv[u] = ld_stream(static_cast<const uint16_t *>(p.z) + i * p.n + col);
+                else if constexpr (ACT != DACT_NONE) zv[u] = ptx::ld_stream(static_cast<const uint16_t *>(p.z) + i * p.n + col);
             }
         }
 #pragma unroll

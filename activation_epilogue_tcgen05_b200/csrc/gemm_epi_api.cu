@@ -80,6 +80,9 @@ struct Plan {
     const void *cA = nullptr, *cB = nullptr;
     void *cD = nullptr;
     CUtensorMap tmA, tmB, tmD;
+    // the residual's map (extended epilogue), keyed on its pointer
+    const void *cR = nullptr;
+    CUtensorMap tmR;
 };
 
 std::mutex g_mu;
@@ -544,6 +547,16 @@ int check_ext_args(const Plan *P, const Ext &x) {
     return find_ext(P, &tc, &sk);
 }
 
+// The residual's tensor map: boxes and swizzle as D's.
+int ensure_res_map(Plan *P, const Ext &x) {
+    if (!x.R || P->kernel == GEMM_EPI_KERNEL_SPLITK || P->cR == x.R) return GEMM_EPI_OK;
+    const int out_dt = P->dtype == GEMM_EPI_E4M3 ? GEMM_EPI_BF16 : P->dtype;
+    P->cR = nullptr;
+    if (!make_map(&P->tmR, out_dt, x.R, P->n, P->m, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return GEMM_EPI_ERR_CUDA;
+    P->cR = x.R;
+    return GEMM_EPI_OK;
+}
+
 int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, cudaStream_t stream,
                 float *dbias_ws = nullptr, const Ext *ext = nullptr) {
     TcLauncher tc_ext = nullptr;
@@ -647,6 +660,7 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.prefetch = P->prefetch;
         L.p.fused = P->fused ? 1 : 0;
         if (ext) {
+            L.tmR = ext->R ? P->tmR : P->tmD;
             L.p.residual = ext->R;
             L.p.scale_rows = ext->scale_rows;
             L.p.bias_row = P->axis == GEMM_EPI_BIAS_ROW;
@@ -935,6 +949,7 @@ int gemm_epi_run_ext(gemm_epi_plan_t plan, const void *A, const void *B, const v
     int rc = check_run_args(P, A, B, bias, D, aux);
     if (rc == GEMM_EPI_OK) rc = check_ext_args(P, x);
     if (rc == GEMM_EPI_OK) rc = ensure_maps(P, A, B, D);
+    if (rc == GEMM_EPI_OK) rc = ensure_res_map(P, x);
     if (rc != GEMM_EPI_OK) return rc;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (P->qout && P->amax && cudaMemsetAsync(P->amax, 0, sizeof(float), s) != cudaSuccess) return GEMM_EPI_ERR_CUDA;
@@ -1213,6 +1228,7 @@ int gemm_epi_mlp_run_prenorm(gemm_epi_mlp_t mlp, const void *X, const void *R, c
     if (rc == GEMM_EPI_OK) rc = check_ext_args(Dn, xd);
     if (rc == GEMM_EPI_OK) rc = ensure_maps(U, N, W1, H);
     if (rc == GEMM_EPI_OK) rc = ensure_maps(Dn, H, W2, Y);
+    if (rc == GEMM_EPI_OK) rc = ensure_res_map(Dn, xd);
     if (rc != GEMM_EPI_OK) return rc;
     const int norm_dt = fp8 ? GEMM_EPI_BF16 : U->dtype;
     rc = gemm_epi_rmsnorm(U->m, U->k, norm_dt, fp8 ? GEMM_EPI_NORM_E4M3_ROWS : GEMM_EPI_NORM_SAME, eps, X, R, gamma,

@@ -190,19 +190,24 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     float cbias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float alpha = 1.0f, inv_out = 1.0f;
     // EXT: residual values and row scales of the first four blocks of rows that this warp finishes
-    // (all there are for up to 16 rows); later blocks read theirs when they come to them
-    float pre_r[4][C::EXT ? 4 : 1] = {}, pre_a[4][C::EXT ? 4 : 1] = {};
-    auto load_ext = [&](int grp, int u, float (&r)[C::EXT ? 4 : 1], float (&a)[C::EXT ? 4 : 1]) {
-        if constexpr (!C::EXT) return;
-        const int col = n0 + 32 * grp + lane;
+    // (all there are for up to 16 rows, or 64 with a cluster of four); later blocks read theirs when they
+    // come to them.  Addresses past the last row or column are drawn back to it and the values not
+    // used: without branches every load goes out before the first is waited for (64 x 4096 x 4096:
+    // FIG us, FIG with a branch around each).  The residual stays in its 16 bits until it is added.
+    using R16 = typename OutT<C::DT>::type;
+    R16 pre_r[4][C::EXT ? 4 : 1];
+    float pre_a[4][C::EXT ? 4 : 1];
+    auto load_ext = [&](int grp, int u, R16(&r)[C::EXT ? 4 : 1], float (&a)[C::EXT ? 4 : 1]) {
+        if constexpr (C::EXT) {
+            const int col = min(n0 + 32 * grp + lane, p.n - 1);
+            if (!C::QOUT && p.residual != nullptr) {
 #pragma unroll
-        for (int c = 0; c < (C::EXT ? 4 : 0); ++c) {
-            const int i = 4 * u + c;
-            r[c] = 0.0f;
-            a[c] = alpha;
-            if (i < p.m) {
-                if (!C::QOUT && p.residual != nullptr && col < p.n) r[c] = OutT<C::DT>::load(p.residual, (int64_t)i * p.n + col);
-                if (p.scale_rows != nullptr) a[c] = __ldg(p.scale_rows + i) * (p.scale_b != nullptr ? __ldg(p.scale_b) : 1.0f);
+                for (int c = 0; c < 4; ++c)
+                    r[c] = reinterpret_cast<const R16 *>(p.residual)[(int64_t)min(4 * u + c, p.m - 1) * p.n + col];
+            }
+            if (p.scale_rows != nullptr) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) a[c] = __ldg(p.scale_rows + min(4 * u + c, p.m - 1));
             }
         }
     };
@@ -214,7 +219,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (gl < groups && col < p.n && p.bias != nullptr) cbias[gl] = OutT<C::DT>::load(p.bias, col);
             }
         }
-        if (p.scale_a != nullptr) alpha = __ldg(p.scale_a) * __ldg(p.scale_b);
+        if (C::EXT && p.scale_rows != nullptr) alpha = p.scale_b != nullptr ? __ldg(p.scale_b) : 1.0f;
+        else if (p.scale_a != nullptr) alpha = __ldg(p.scale_a) * __ldg(p.scale_b);
         if constexpr (C::QOUT) inv_out = 1.0f / __ldg(p.out_scale);
         if constexpr (C::EXT) {
 #pragma unroll
@@ -307,7 +313,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // n0 + 32 grp + lane), from their fp32 sums `part`: the four rows' values first, without
     // branches, then their stores.
     // (EXT: its residual values r and row scales a.)
-    auto emit4 = [&](int grp, int u, const float (&part)[4], float cb, const float (&r)[C::EXT ? 4 : 1],
+    auto emit4 = [&](int grp, int u, const float (&part)[4], float cb, const R16(&r)[C::EXT ? 4 : 1],
                      const float (&a)[C::EXT ? 4 : 1]) {
         const int col = n0 + 32 * grp + lane;
         const bool col_ok = col < p.n;
@@ -318,7 +324,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             const int i = 4 * u + c;
-            float x = part[c] * (C::EXT ? a[C::EXT ? c : 0] : alpha);
+            float al = alpha;
+            if constexpr (C::EXT) if (p.scale_rows != nullptr) al = a[c] * alpha;
+            float x = part[c] * al;
             if constexpr (C::EPI != EPI_NONE) {
                 if constexpr (C::AXIS == AXIS_COL) x += cb;
                 if constexpr (C::EXT) {
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (lane == 0 && i < p.m) p.aux[(int64_t)i * p.aux_pitch_words + word] = bits;
             }
             y[c] = activate<C::EPI>(x);
-            if constexpr (C::EXT && !C::QOUT) y[c] += r[c];
+            if constexpr (C::EXT && !C::QOUT) if (p.residual != nullptr) y[c] += O::load(&r[c], 0);
         }
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -386,7 +394,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         if (u < 4) {
                             emit4(q, u, part, cb, pre_r[u < 4 ? u : 0], pre_a[u < 4 ? u : 0]);
                         } else {
-                            float r[4], a[4];
+                            R16 r[4];
+                            float a[4];
                             load_ext(q, u, r, a);
                             emit4(q, u, part, cb, r, a);
                         }
@@ -442,7 +451,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 const int grp = (int)rank + gl * (int)csize;
                 if constexpr (C::EXT) {
                     const int b = (unit - ew) / 4;          // this warp's b-th block
-                    float r[4], a[4];
+                    R16 r[4];
+                    float a[4];
                     if (b < 4) {
 #pragma unroll
                         for (int k = 0; k < 4; ++k)

@@ -53,6 +53,7 @@
 #include <cuda_fp8.h>
 
 #include <cstdint>
+#include <type_traits>
 
 #include "ptx.cuh"
 
@@ -118,6 +119,10 @@ struct TcParams {
     const void *residual;        // R, (m, n) in the output type, or NULL; may be D
     const float *scale_rows;     // m floats that take the place of *scale_a, or NULL
     int bias_row;                // the bias runs along the rows (length m)
+};
+// Parameters of the kernels that add a residual: R's tensor map (boxes as D's) beside the rest.
+struct TcResParams : TcParams {
+    CUtensorMap tmR;
 };
 
 // Timeline tracing (off unless the library is compiled with -DGEMM_EPI_TRACE=1 or 2).
@@ -423,6 +428,8 @@ struct TcCfg {
     // e4m3 output quantised with a per-tensor scale (the MLP block's intermediate): written
     // with direct 16-byte stores from registers, no staging
     static constexpr bool QOUT = QOUT_;
+    static constexpr bool RES = EXT && !QOUT;                // adds a residual (kept in 16 bits)
+    using Params = std::conditional_t<RES, TcResParams, TcParams>;
     static constexpr int EPI_WARPS = HEAVY_EPI ? 8 : 4;
     static constexpr int THREADS = 64 + 32 * EPI_WARPS;
     static constexpr int COLS_W = BN * 4 / EPI_WARPS;       // columns of a tile one epilogue warp handles
@@ -431,17 +438,21 @@ struct TcCfg {
     static_assert(NCH_W % CPG == 0 && (CPG == 2 || CPG == 4), "chunk grouping");
     static constexpr int TMEM_COLS = (NUM_ACC * BN <= 32) ? 32 : (NUM_ACC * BN <= 64) ? 64 : (NUM_ACC * BN <= 128) ? 128
                                    : (NUM_ACC * BN <= 256) ? 256 : 512;
-    static constexpr int STG_BYTES = QOUT ? 0 : 32 * 64;   // per epilogue warp: 32 rows x 32 16-bit outputs
+    // per epilogue warp: 32 rows x 32 16-bit outputs, twice where the residual's chunks land there
+    static constexpr int STG_BYTES = QOUT ? 0 : (RES ? 2 : 1) * 32 * 64;
     // shared-memory layout (offsets from a 1024-byte aligned base)
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_STAGE;
     static constexpr int OFF_STG = OFF_B + STAGES * B_STAGE;
     static constexpr int OFF_BIAS = OFF_STG + EPI_WARPS * STG_BYTES;
-    static constexpr int BIAS_FLOATS = (FWD_BIAS && AXIS == AXIS_COL) ? COLS_W : 0;
+    // (the residual's second buffer takes the room of the bias copies: RES kernels read the bias through L1)
+    static constexpr int BIAS_FLOATS = (FWD_BIAS && AXIS == AXIS_COL && !RES) ? COLS_W : 0;
     static constexpr int OFF_BAR = OFF_BIAS + EPI_WARPS * BIAS_FLOATS * 4;
     // a full barrier per (stage, k-atom): the MMA starts on a stage's first atom while the
     // second is still landing; an empty barrier per stage; two accumulator pairs; done
-    static constexpr int NUM_BARS = (KATOMS + 1) * STAGES + 4 + 1;
+    // (RES: two more for every epilogue warp, one a buffer)
+    static constexpr int RES_BARS = RES ? 2 * EPI_WARPS : 0;
+    static constexpr int NUM_BARS = (KATOMS + 1) * STAGES + 4 + 1 + RES_BARS;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;   // + alignment slack
     static_assert(BN == 128 || BN == 256 || (BN == 512 && CG == 2), "BN is 128 or 256 (512 for CTA pairs)");
@@ -501,7 +512,7 @@ __device__ __forceinline__ void tile_coords(const TcParams &p, int t, int &tm, i
 template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     tc_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                   const __grid_constant__ CUtensorMap tmD, const TcParams p) {
+                   const __grid_constant__ CUtensorMap tmD, const __grid_constant__ typename C::Params p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -537,6 +548,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             ptx::mbar_init(tempty_bar(a), C::EPI_WARPS * C::CG);
         }
         ptx::mbar_init(done_bar, 1);
+        for (int i = 0; i < C::RES_BARS; ++i) ptx::mbar_init(done_bar + 8u * (1 + i), 1);
         *abort_flag = 0;
         ptx::fence_mbarrier_init();
     }
@@ -870,6 +882,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if constexpr (C::QOUT) inv_out = 1.0f / __ldg(p.out_scale);
         uint32_t acc = 0, acc_phase = 0, tr_i = 0;
         bool ok = true;
+        // RES: chunks of the residual consumed and asked for by this warp, its barriers, one load
+        uint32_t res_n = 0, res_issued = 0;
+        auto res_bar = [&](uint32_t i) { return done_bar + 8u * (1 + 2 * ew + i); };
+        auto load_res = [&](uint32_t b, int col, int r0) {
+            if constexpr (C::RES) {
+                ptx::mbar_arrive_expect_tx(res_bar(b), 2048);
+                ptx::tma_load_2d(stg + b * 2048, &p.tmR, res_bar(b), col, r0, ptx::policy_evict_first());
+            }
+        };
+        // element pair j of 32 that sit in four vectors
+        auto word = [](const uint4(&v)[C::RES ? 4 : 1], int j) {
+            const uint4 &u = v[C::RES ? j / 8 : 0];
+            return j % 8 == 0 ? u.x : j % 8 == 2 ? u.y : j % 8 == 4 ? u.z : u.w;
+        };
+        (void)res_n; (void)res_issued; (void)word;
         WorkIter it(p, unit, units);
         WorkItem w;
         while (ok && it.next(p, units, w)) {
@@ -936,6 +963,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 __syncwarp();
             }
+            // The residual comes in 32 x 32 boxes like D's, each into the buffer that its output leaves
+            // from: a thread reads the 64 bytes of its row there and writes the result over them.  A warp
+            // has two such buffers, used in turn (chunk number res_n in buffer res_n & 1), and loads a chunk
+            // while it works on the one before.  The first chunk is loaded, and the others asked of L2,
+            // before the accumulator is waited for.
+            const bool res = C::RES && p.residual != nullptr && !partial_out;
+            if constexpr (C::RES) if (res && lane == 0) {
+                ptx::bulk_wait_read<0>();     // earlier stores have read the buffers
+                load_res(res_n & 1u, n0 + 32 * chunk_of<C>(ew, 0), m0 + 32 * q);
+                for (int cl = 1; cl < C::NCH_W; ++cl) {
+                    const int col = n0 + 32 * chunk_of<C>(ew, cl);
+                    if (col < p.n && m0 + 32 * q < p.m) ptx::tma_prefetch_l2_2d(&p.tmR, col, m0 + 32 * q);
+                }
+            }
+            if constexpr (C::RES) if (res) ++res_issued;
             if (lane == 0) trace_event(p.trace, warp, 5, w.tile, w.kb0);
             if (!wait_bounded<false>(tfull_bar(acc), acc_phase, abort_flag, p.status, ST_TIMEOUT_EPILOGUE)) {
                 ok = false;
@@ -965,6 +1007,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     uint32_t(&v)[32] = vb[cc & 1];
                     ptx::tmem_wait_ld(v);                      // the only load in flight: this chunk's
                     if (cl + 1 < C::NCH_W) ptx::tmem_ld_32x32b_x32(tbase + chunk_of<C>(ew, cl + 1) * 32, vb[(cc + 1) & 1]);
+                    if constexpr (C::RES) if (res && cl + 1 < C::NCH_W) {
+                        if (lane == 0) {
+                            ptx::bulk_wait_read<0>();
+                            load_res((res_n + 1u) & 1u, n0 + 32 * chunk_of<C>(ew, cl + 1), m0 + 32 * q);
+                        }
+                        ++res_issued;
+                    }
                     // accumulator (or, SPLIT_HALVES, one half of it) fully read by this warp: hand
                     // it back to the MMA issuer
                     const bool last_chunk = cc == C::CPG - 1 && g == C::NCH_W / C::CPG - 1;
@@ -999,15 +1048,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                     const int col0 = n0 + 32 * c;
-                    // this lane's 32 residual values: 64 bytes of its row
-                    uint4 res[4];
-                    if constexpr (C::EXT && !C::QOUT) {
+                    // RES: this chunk's bias (column bias; one address for the whole warp) and residual
+                    uint4 cb[C::RES ? 4 : 1], rv[C::RES ? 4 : 1];
+                    uint8_t *res_row = nullptr;
+                    if constexpr (C::RES) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            res[i] = make_uint4(0u, 0u, 0u, 0u);
-                            if (p.residual != nullptr && row_ok && col0 + 8 * i < p.n)
-                                res[i] = __ldcs(reinterpret_cast<const uint4 *>(
-                                    static_cast<const typename O::type *>(p.residual) + (int64_t)row * p.n + col0 + 8 * i));
+                            cb[i] = rv[i] = make_uint4(0u, 0u, 0u, 0u);
+                            if (has_bias && !p.bias_row && col0 + 8 * i < p.n)
+                                cb[i] = __ldg(reinterpret_cast<const uint4 *>(
+                                    reinterpret_cast<const typename O::type *>(p.bias) + col0 + 8 * i));
+                        }
+                        res_row = smem + C::OFF_STG + ew * C::STG_BYTES + (res_n & 1u) * 2048 + lane * 64;
+                        if (res) {
+                            if (!wait_bounded<false>(res_bar(res_n & 1u), (res_n >> 1) & 1u, abort_flag, p.status,
+                                                     ST_TIMEOUT_EPILOGUE)) {
+                                ok = false;
+                                break;
+                            }
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                rv[i] = *reinterpret_cast<const uint4 *>(res_row + (i ^ ((lane >> 1) & 3)) * 16);
                         }
                     }
                     uint32_t packed[16];
@@ -1021,7 +1082,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         x1 *= alpha;
                         if constexpr (C::FWD_BIAS) {
                             if constexpr (C::AXIS == AXIS_ROW) { x0 += rbias; x1 += rbias; }
-                            else { x0 += bsm[32 * cl + j]; x1 += bsm[32 * cl + j + 1]; }
+                            else if constexpr (C::RES) {
+                                const float2 b = O::unpack(word(cb, j));
+                                x0 += b.x;
+                                x1 += b.y;
+                            } else { x0 += bsm[32 * cl + j]; x1 += bsm[32 * cl + j + 1]; }
                             if constexpr (C::EXT) { x0 += rbias; x1 += rbias; }
                         }
                         if constexpr (C::BWD) {
@@ -1041,9 +1106,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             bits |= (x1 > 0.0f ? 1u : 0u) << (j + 1);
                         }
                         float y0 = activate<C::EPI>(x0), y1 = activate<C::EPI>(x1);
-                        if constexpr (C::EXT && !C::QOUT) {
-                            const float2 r = O::unpack(j % 8 == 0 ? res[j / 8].x : j % 8 == 2 ? res[j / 8].y
-                                                       : j % 8 == 4 ? res[j / 8].z : res[j / 8].w);
+                        if constexpr (C::RES) {
+                            const float2 r = O::unpack(word(rv, j));
                             y0 += r.x;
                             y1 += r.y;
                         }
@@ -1082,7 +1146,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         // otherwise the warp's single staging buffer is reused.
                         uint32_t stg_c = stg;
                         uint8_t *stg_row = smem + C::OFF_STG + ew * C::STG_BYTES + lane * 64;
-                        if (last_item) {
+                        if (C::RES && res) {
+                            stg_c = stg + (res_n & 1u) * 2048;      // the residual's buffer, free to this thread's row
+                            stg_row = res_row;
+                        } else if (last_item) {
                             const int slot = ew * C::NCH_W + cl;
                             stg_c = sA + slot * 2048;
                             stg_row = smem + C::OFF_A + slot * 2048 + lane * 64;
@@ -1103,6 +1170,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             ptx::tma_store_2d_hint(&tmD, stg_c, col0, m0 + 32 * q, pol_d);
                             ptx::bulk_commit();
                         }
+                        if constexpr (C::RES) if (res) ++res_n;
                     }
                     if constexpr (C::BWD && C::AXIS == AXIS_COL) if (bgrad) {
                         // column sums over this warp's 32 rows: a butterfly that halves the
@@ -1125,6 +1193,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             p.dbias_ws[(size_t)((m0 + 32 * q) >> 5) * p.n + col0 + lane] = f[0];
                     }
                 }
+                if constexpr (C::RES) if (!ok) break;
                 if (partial_out) continue;
                 if constexpr (C::EPI == EPI_RELU_AUX) {
                     const int wcol = n0 + 32 * chunk_of<C>(ew, C::CPG * g);
@@ -1152,6 +1221,11 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (lane == 0) trace_event(p.trace, warp, 9, w.tile, 0);
             if (lane == 0 && ew == 0) trace_stage(p.trace, 2, tr_i, 27, w.tile, w.kb1);
             if (++acc == (uint32_t)C::NUM_ACC) { acc = 0; acc_phase ^= 1u; }
+        }
+        if constexpr (C::RES) {
+            // after an abort: the loads still in flight have landed before shared memory is given up
+            if (!ok)
+                for (uint32_t i = res_n; i < res_issued; ++i) wait_drain(res_bar(i & 1u), (i >> 1) & 1u, p.status);
         }
         if (lane == 0) ptx::bulk_wait<0>();
         __syncwarp();

@@ -16,6 +16,7 @@ namespace gemm_epi {
 struct TcLaunch {
     CUtensorMap tmA, tmB, tmD;
     TcParams p;
+    CUtensorMap tmR;     // kernels that add a residual: its map (any valid one without a residual)
     int grid;
     bool pdl;            // launch with programmatic stream serialisation
     cudaStream_t stream;
@@ -160,7 +161,14 @@ cudaError_t launch_tc(const TcLaunch &L) {
     }
     cfg.attrs = na ? attr : nullptr;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, kern, L.tmA, L.tmB, L.tmD, L.p);
+    if constexpr (C::RES) {
+        TcResParams p;
+        static_cast<TcParams &>(p) = L.p;
+        p.tmR = L.tmR;
+        return cudaLaunchKernelEx(&cfg, kern, L.tmA, L.tmB, L.tmD, p);
+    } else {
+        return cudaLaunchKernelEx(&cfg, kern, L.tmA, L.tmB, L.tmD, L.p);
+    }
 }
 
 template <class C>

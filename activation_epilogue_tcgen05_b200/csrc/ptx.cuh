@@ -244,6 +244,17 @@ __device__ __forceinline__ void st_global_v4_hint(void *p, uint4 v, uint64_t pol
                  "r"(v.z), "r"(v.w), "l"(policy)
                  : "memory");
 }
+// A 16-byte load that leaves no copy in L1, for data that is read once.  (Not the read-only path: the
+// output may be stored over such an input, by the thread that read it.)
+__device__ __forceinline__ uint4 ld_stream(const void *p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p)
+                 : "memory");
+    return v;
+}
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // 16-byte asynchronous copies of a thread's own (no copy in L1); committed and waited for in groups.
 __device__ __forceinline__ void cp_async_16(void *smem_dst, const void *src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(smem_dst)), "l"(src) : "memory");

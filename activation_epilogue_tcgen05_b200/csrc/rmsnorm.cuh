@@ -53,17 +53,6 @@ struct NormBwdParams {
     float *partial;          // [grid][d] sums for dgamma, or NULL
 };
 
-// A 16-byte load that leaves no copy in L1: every element is used once.  (Not the read-only
-// path: S may be stored over X or R, and Y over X, by the thread that read those elements.)
-__device__ __forceinline__ uint4 ld_stream(const void *p) {
-    uint4 v;
-    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p)
-                 : "memory");
-    return v;
-}
-
 template <int DT>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     using O = OutT<DT>;
@@ -123,8 +112,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
         const int v = j * TPR + t;
         xv[j] = rv[j] = gv[j] = make_uint4(0u, 0u, 0u, 0u);
         if (row_ok && v < nvec) {
-            xv[j] = ld_stream(static_cast<const uint16_t *>(p.x) + base + 8 * v);
-            if (p.r != nullptr) rv[j] = ld_stream(static_cast<const uint16_t *>(p.r) + base + 8 * v);
+            xv[j] = ptx::ld_stream(static_cast<const uint16_t *>(p.x) + base + 8 * v);
+            if (p.r != nullptr) rv[j] = ptx::ld_stream(static_cast<const uint16_t *>(p.r) + base + 8 * v);
         }
     }
 #pragma unroll
