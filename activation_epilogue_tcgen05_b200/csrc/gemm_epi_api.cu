@@ -526,16 +526,25 @@ struct Ext {
     const float *scale_rows;
 };
 
-// The plan's kernel with the extended epilogue, if the plan has one.
-int find_ext(const Plan *P, TcLauncher *tc, SkLauncher *sk) {
+// Tile width of a TC plan's launches with the extended epilogue: 256 where the plan chose 512 by
+// itself.  A 512-wide tile has one accumulator, and the residual lengthens the epilogue that the next
+// tile's mainloop cannot pass (8192 x 8192 x 1024 bf16 FIG us against FIG, 8192 x 8192 x 4096 FIG
+// against FIG).  (Stage-wide copies have their maps made for the plan's own stages.)
+int ext_block_n(const Plan *P) {
+    return P->block_n == 512 && P->opts.block_n == 0 && !P->fused ? 256 : P->block_n;
+}
+
+// The plan's kernel with the extended epilogue, if the plan has one, and the k-atoms of its stages.
+int find_ext(const Plan *P, TcLauncher *tc, SkLauncher *sk, int *katoms) {
     const bool b_mn = P->b_layout == GEMM_EPI_B_KN;
     KernelInfo info;
     if (P->a_km || P->sk_grid || P->bwd) return GEMM_EPI_ERR_UNSUPPORTED;
+
     if (P->kernel == GEMM_EPI_KERNEL_SPLITK)
         return find_sk_ext(P->dtype, P->kepi, b_mn, P->nm, P->qout, sk, &info) ? GEMM_EPI_OK : GEMM_EPI_ERR_UNSUPPORTED;
-    if (!find_tc_ext(P->kernel == GEMM_EPI_KERNEL_TC2 ? 2 : 1, P->dtype, P->kepi, b_mn, P->block_n, P->qout, tc, &info) ||
-        info.katoms != P->katoms)
+    if (!find_tc_ext(P->kernel == GEMM_EPI_KERNEL_TC2 ? 2 : 1, P->dtype, P->kepi, b_mn, ext_block_n(P), P->qout, tc, &info))
         return GEMM_EPI_ERR_UNSUPPORTED;
+    *katoms = info.katoms;
     return GEMM_EPI_OK;
 }
 
@@ -544,7 +553,8 @@ int check_ext_args(const Plan *P, const Ext &x) {
     if (!aligned16(x.R) || (reinterpret_cast<uintptr_t>(x.scale_rows) & 3u)) return GEMM_EPI_ERR_ALIGN;
     TcLauncher tc;
     SkLauncher sk;
-    return find_ext(P, &tc, &sk);
+    int katoms;
+    return find_ext(P, &tc, &sk, &katoms);
 }
 
 // The residual's tensor map: boxes and swizzle as D's.
@@ -561,7 +571,8 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
                 float *dbias_ws = nullptr, const Ext *ext = nullptr) {
     TcLauncher tc_ext = nullptr;
     SkLauncher sk_ext = nullptr;
-    if (ext && find_ext(P, &tc_ext, &sk_ext) != GEMM_EPI_OK) return GEMM_EPI_ERR_UNSUPPORTED;
+    int katoms = P->katoms;
+    if (ext && find_ext(P, &tc_ext, &sk_ext, &katoms) != GEMM_EPI_OK) return GEMM_EPI_ERR_UNSUPPORTED;
     if (!P->has_bias) bias = nullptr;
     const int bk = 128 / esize(P->dtype);
     const int num_kb = (int)((P->k + bk - 1) / bk);
@@ -635,11 +646,12 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.n = (int)P->n;
         L.p.k = (int)P->k;
         L.p.tiles_m = (int)((P->m + 128 * cg - 1) / (128 * cg));
-        L.p.tiles_n = (int)((P->n + P->block_n - 1) / P->block_n);
+        const int bn = ext ? ext_block_n(P) : P->block_n;
+        L.p.tiles_n = (int)((P->n + bn - 1) / bn);
         L.p.num_tiles = L.p.tiles_m * L.p.tiles_n;
-        L.p.num_kb = (int)((P->k + (int64_t)bk * P->katoms - 1) / ((int64_t)bk * P->katoms));   // ring stages
+        L.p.num_kb = (int)((P->k + (int64_t)bk * katoms - 1) / ((int64_t)bk * katoms));   // ring stages
         L.p.group_m = P->group_m;
-        L.p.group_n = P->group_n;
+        L.p.group_n = P->group_n > 0 ? L.p.tiles_n : 0;     // (a group of tile-columns is all of them)
         L.p.bias = bias;
         L.p.aux = aux;
         L.p.aux_pitch_words = pitch_words;
@@ -647,8 +659,9 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.scale_b = P->scale_b;
         L.p.status = P->status;
         L.p.inject_stall = P->opts.inject_stall;
-        L.p.sk_tiles = P->sk_tiles;
-        L.p.sk_split = P->sk_split;
+        // (no split tail for the narrower tiles of a plan with 512-wide ones: many waves)
+        L.p.sk_tiles = bn == P->block_n ? P->sk_tiles : 0;
+        L.p.sk_split = bn == P->block_n ? P->sk_split : 0;
         L.p.workspace = P->workspace;
         L.p.flags = P->flags;
         L.p.trace = trace_for_launch();

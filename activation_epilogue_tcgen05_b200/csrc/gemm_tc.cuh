@@ -438,20 +438,20 @@ struct TcCfg {
     static_assert(NCH_W % CPG == 0 && (CPG == 2 || CPG == 4), "chunk grouping");
     static constexpr int TMEM_COLS = (NUM_ACC * BN <= 32) ? 32 : (NUM_ACC * BN <= 64) ? 64 : (NUM_ACC * BN <= 128) ? 128
                                    : (NUM_ACC * BN <= 256) ? 256 : 512;
-    // per epilogue warp: 32 rows x 32 16-bit outputs, twice where the residual's chunks land there
-    static constexpr int STG_BYTES = QOUT ? 0 : (RES ? 2 : 1) * 32 * 64;
+    static constexpr int STG_BYTES = QOUT ? 0 : 32 * 64;   // per epilogue warp: 32 rows x 32 16-bit outputs
     // shared-memory layout (offsets from a 1024-byte aligned base)
     static constexpr int OFF_A = 0;
     static constexpr int OFF_B = OFF_A + STAGES * A_STAGE;
     static constexpr int OFF_STG = OFF_B + STAGES * B_STAGE;
-    static constexpr int OFF_BIAS = OFF_STG + EPI_WARPS * STG_BYTES;
-    // (the residual's second buffer takes the room of the bias copies: RES kernels read the bias through L1)
+    static constexpr int OFF_RES = OFF_STG + EPI_WARPS * STG_BYTES;     // a chunk of the residual a warp
+    static constexpr int OFF_BIAS = OFF_RES + (RES ? EPI_WARPS * 2048 : 0);
+    // (the residual's buffers take the room of the bias copies: RES kernels read the bias through L1)
     static constexpr int BIAS_FLOATS = (FWD_BIAS && AXIS == AXIS_COL && !RES) ? COLS_W : 0;
     static constexpr int OFF_BAR = OFF_BIAS + EPI_WARPS * BIAS_FLOATS * 4;
     // a full barrier per (stage, k-atom): the MMA starts on a stage's first atom while the
     // second is still landing; an empty barrier per stage; two accumulator pairs; done
-    // (RES: two more for every epilogue warp, one a buffer)
-    static constexpr int RES_BARS = RES ? 2 * EPI_WARPS : 0;
+    // (RES: one more for every epilogue warp)
+    static constexpr int RES_BARS = RES ? EPI_WARPS : 0;
     static constexpr int NUM_BARS = (KATOMS + 1) * STAGES + 4 + 1 + RES_BARS;
     static constexpr int OFF_MISC = OFF_BAR + NUM_BARS * 8;
     static constexpr int SMEM_BYTES = OFF_MISC + 16 + 1024;   // + alignment slack
@@ -882,13 +882,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if constexpr (C::QOUT) inv_out = 1.0f / __ldg(p.out_scale);
         uint32_t acc = 0, acc_phase = 0, tr_i = 0;
         bool ok = true;
-        // RES: chunks of the residual consumed and asked for by this warp, its barriers, one load
+        // RES: chunks of the residual that this warp has taken and has asked for, its barrier, one load
         uint32_t res_n = 0, res_issued = 0;
-        auto res_bar = [&](uint32_t i) { return done_bar + 8u * (1 + 2 * ew + i); };
-        auto load_res = [&](uint32_t b, int col, int r0) {
+        const uint32_t res_bar = done_bar + 8u * (1 + ew);
+        auto load_res = [&](int col, int r0) {
             if constexpr (C::RES) {
-                ptx::mbar_arrive_expect_tx(res_bar(b), 2048);
-                ptx::tma_load_2d(stg + b * 2048, &p.tmR, res_bar(b), col, r0, ptx::policy_evict_first());
+                ptx::mbar_arrive_expect_tx(res_bar, 2048);
+                ptx::tma_load_2d(sb + C::OFF_RES + ew * 2048, &p.tmR, res_bar, col, r0, ptx::policy_evict_first());
             }
         };
         // element pair j of 32 that sit in four vectors
@@ -963,21 +963,31 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 __syncwarp();
             }
-            // The residual comes in 32 x 32 boxes like D's, each into the buffer that its output leaves
-            // from: a thread reads the 64 bytes of its row there and writes the result over them.  A warp
-            // has two such buffers, used in turn (chunk number res_n in buffer res_n & 1), and loads a chunk
-            // while it works on the one before.  The first chunk is loaded, and the others asked of L2,
-            // before the accumulator is waited for.
+            // The residual comes in 32 x 32 boxes like D's, into a buffer of the warp's own: a chunk is taken
+            // from there into registers, and the next one asked for, before its arithmetic.  The first is
+            // asked for here, and the others are asked of L2, before the accumulator is waited for.
             const bool res = C::RES && p.residual != nullptr && !partial_out;
-            if constexpr (C::RES) if (res && lane == 0) {
-                ptx::bulk_wait_read<0>();     // earlier stores have read the buffers
-                load_res(res_n & 1u, n0 + 32 * chunk_of<C>(ew, 0), m0 + 32 * q);
-                for (int cl = 1; cl < C::NCH_W; ++cl) {
-                    const int col = n0 + 32 * chunk_of<C>(ew, cl);
-                    if (col < p.n && m0 + 32 * q < p.m) ptx::tma_prefetch_l2_2d(&p.tmR, col, m0 + 32 * q);
+            if constexpr (C::RES) if (res) {
+                if (lane == 0) {
+                    load_res(n0 + 32 * chunk_of<C>(ew, 0), m0 + 32 * q);
+                    for (int cl = 1; cl < C::NCH_W; ++cl) {
+                        const int col = n0 + 32 * chunk_of<C>(ew, cl);
+                        if (col < p.n && m0 + 32 * q < p.m) ptx::tma_prefetch_l2_2d(&p.tmR, col, m0 + 32 * q);
+                    }
                 }
+                ++res_issued;
             }
-            if constexpr (C::RES) if (res) ++res_issued;
+            // RES: a chunk's column bias (one address for the whole warp), loaded as soon as the chunk
+            // before has used its own: there is no room in shared memory for copies of it
+            uint4 cb[C::RES ? 4 : 1] = {};
+            auto load_bias = [&](int c) {
+#pragma unroll
+                for (int i = 0; i < (C::RES ? 4 : 0); ++i)
+                    if (has_bias && !p.bias_row && n0 + 32 * c + 8 * i < p.n)
+                        cb[i] = __ldg(reinterpret_cast<const uint4 *>(
+                            reinterpret_cast<const typename O::type *>(p.bias) + n0 + 32 * c + 8 * i));
+            };
+            if (!partial_out) load_bias(chunk_of<C>(ew, 0));
             if (lane == 0) trace_event(p.trace, warp, 5, w.tile, w.kb0);
             if (!wait_bounded<false>(tfull_bar(acc), acc_phase, abort_flag, p.status, ST_TIMEOUT_EPILOGUE)) {
                 ok = false;
@@ -1005,15 +1015,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const int cl = C::CPG * g + cc;            // chunk index within this warp
                     const int c = chunk_of<C>(ew, cl);         // chunk index within the tile
                     uint32_t(&v)[32] = vb[cc & 1];
+                    uint4 rv[C::RES ? 4 : 1] = {};             // RES: this chunk's residual
                     ptx::tmem_wait_ld(v);                      // the only load in flight: this chunk's
                     if (cl + 1 < C::NCH_W) ptx::tmem_ld_32x32b_x32(tbase + chunk_of<C>(ew, cl + 1) * 32, vb[(cc + 1) & 1]);
-                    if constexpr (C::RES) if (res && cl + 1 < C::NCH_W) {
-                        if (lane == 0) {
-                            ptx::bulk_wait_read<0>();
-                            load_res((res_n + 1u) & 1u, n0 + 32 * chunk_of<C>(ew, cl + 1), m0 + 32 * q);
-                        }
-                        ++res_issued;
-                    }
                     // accumulator (or, SPLIT_HALVES, one half of it) fully read by this warp: hand
                     // it back to the MMA issuer
                     const bool last_chunk = cc == C::CPG - 1 && g == C::NCH_W / C::CPG - 1;
@@ -1048,27 +1052,20 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                     const int col0 = n0 + 32 * c;
-                    // RES: this chunk's bias (column bias; one address for the whole warp) and residual
-                    uint4 cb[C::RES ? 4 : 1], rv[C::RES ? 4 : 1];
-                    uint8_t *res_row = nullptr;
-                    if constexpr (C::RES) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            cb[i] = rv[i] = make_uint4(0u, 0u, 0u, 0u);
-                            if (has_bias && !p.bias_row && col0 + 8 * i < p.n)
-                                cb[i] = __ldg(reinterpret_cast<const uint4 *>(
-                                    reinterpret_cast<const typename O::type *>(p.bias) + col0 + 8 * i));
+                    if constexpr (C::RES) if (res) {
+                        if (!wait_bounded<false>(res_bar, res_n & 1u, abort_flag, p.status, ST_TIMEOUT_EPILOGUE)) {
+                            ok = false;
+                            break;
                         }
-                        res_row = smem + C::OFF_STG + ew * C::STG_BYTES + (res_n & 1u) * 2048 + lane * 64;
-                        if (res) {
-                            if (!wait_bounded<false>(res_bar(res_n & 1u), (res_n >> 1) & 1u, abort_flag, p.status,
-                                                     ST_TIMEOUT_EPILOGUE)) {
-                                ok = false;
-                                break;
-                            }
+                        ++res_n;
+                        const uint8_t *row_in = smem + C::OFF_RES + ew * 2048 + lane * 64;     // swizzled as D's staging
 #pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                rv[i] = *reinterpret_cast<const uint4 *>(res_row + (i ^ ((lane >> 1) & 3)) * 16);
+                        for (int i = 0; i < 4; ++i)
+                            rv[i] = *reinterpret_cast<const uint4 *>(row_in + (i ^ ((lane >> 1) & 3)) * 16);
+                        __syncwarp();                     // every row is in registers: the buffer is free
+                        if (cl + 1 < C::NCH_W) {
+                            if (lane == 0) load_res(n0 + 32 * chunk_of<C>(ew, cl + 1), m0 + 32 * q);
+                            ++res_issued;
                         }
                     }
                     uint32_t packed[16];
@@ -1120,6 +1117,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             packed[j / 2] = O::pack(y0, y1);
                         }
                     }
+                    if (cl + 1 < C::NCH_W) load_bias(chunk_of<C>(ew, cl + 1));
                     if constexpr (C::EPI == EPI_RELU_AUX) {
                         const int valid = p.n - col0;
                         const uint32_t keep = valid >= 32 ? 0xFFFFFFFFu : (valid <= 0 ? 0u : ((1u << valid) - 1u));
@@ -1146,10 +1144,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         // otherwise the warp's single staging buffer is reused.
                         uint32_t stg_c = stg;
                         uint8_t *stg_row = smem + C::OFF_STG + ew * C::STG_BYTES + lane * 64;
-                        if (C::RES && res) {
-                            stg_c = stg + (res_n & 1u) * 2048;      // the residual's buffer, free to this thread's row
-                            stg_row = res_row;
-                        } else if (last_item) {
+                        if (last_item) {
                             const int slot = ew * C::NCH_W + cl;
                             stg_c = sA + slot * 2048;
                             stg_row = smem + C::OFF_A + slot * 2048 + lane * 64;
@@ -1170,7 +1165,6 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             ptx::tma_store_2d_hint(&tmD, stg_c, col0, m0 + 32 * q, pol_d);
                             ptx::bulk_commit();
                         }
-                        if constexpr (C::RES) if (res) ++res_n;
                     }
                     if constexpr (C::BWD && C::AXIS == AXIS_COL) if (bgrad) {
                         // column sums over this warp's 32 rows: a butterfly that halves the
@@ -1223,9 +1217,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             if (++acc == (uint32_t)C::NUM_ACC) { acc = 0; acc_phase ^= 1u; }
         }
         if constexpr (C::RES) {
-            // after an abort: the loads still in flight have landed before shared memory is given up
-            if (!ok)
-                for (uint32_t i = res_n; i < res_issued; ++i) wait_drain(res_bar(i & 1u), (i >> 1) & 1u, p.status);
+            // after an abort: a load still in flight has landed before shared memory is given up
+            if (!ok && res_n != res_issued) wait_drain(res_bar, res_n & 1u, p.status);
         }
         if (lane == 0) ptx::bulk_wait<0>();
         __syncwarp();
