@@ -35,36 +35,8 @@ struct DactParams {
     float *partial;          // COL: [run][n]; ROW: [strip][m]; or NULL
 };
 
-// Two fp32 values in a register pair, for Blackwell's two-wide fp32 instructions: GELU's slope
-// takes 27 instructions an element one by one and 14 in pairs, below what HBM allows time for.
-using f32x2 = unsigned long long;
-__device__ __forceinline__ f32x2 pair(float a, float b) {
-    f32x2 r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ float2 split(f32x2 v) {
-    float2 f;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
-    return f;
-}
-__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
-    f32x2 r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
-    f32x2 r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
-
+// GELU's slope takes 27 instructions an element one by one and 14 in pairs, below what HBM allows
+// time for.
 // GELU'(x) = Phi(x) + x phi(x), with 1 - Phi(|x|) from the same Abramowitz & Stegun 7.1.26 form as
 // the forward epilogue's GELU (gelu_erf): one exponential serves both terms.
 //     Phi(x) = 1/2 + sign(x) (1/2 - tail),  tail = 1 - Phi(|x|)

@@ -356,6 +356,51 @@ __device__ __forceinline__ float gelu_erf(float x) {
     return fmaf(-ax, half_poly * ex2_approx(-s * s), fmaxf(x, 0.0f));
 }
 
+// Two fp32 values in a register pair, for Blackwell's two-wide fp32 instructions.
+using f32x2 = unsigned long long;
+__device__ __forceinline__ f32x2 pair(float a, float b) {
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float2 split(f32x2 v) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(v));
+    return f;
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c) {
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 mul2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b) {
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f32x2 both(float a) { return pair(a, a); }
+
+// gelu_erf of two values at once: the same operations, 9 instructions an element for its 13.
+__device__ __forceinline__ float2 gelu_erf2(float x0, float x1) {
+    const f32x2 ax = pair(fabsf(x0), fabsf(x1));
+    const float2 den = split(fma2(ax, both(0.3275911f * 0.70710678118654752f), both(1.0f)));
+    const f32x2 t = pair(rcp_approx(den.x), rcp_approx(den.y));
+    f32x2 h = fma2(t, both(0.5307027145f), both(-0.7265760135f));
+    h = fma2(t, h, both(0.7107068705f));
+    h = fma2(t, h, both(-0.142248368f));
+    h = fma2(t, h, both(0.127414796f));
+    h = mul2(t, h);
+    const f32x2 s = mul2(ax, both(0.84932180028801907f));
+    const float2 q = split(mul2(s, s));
+    const f32x2 e = pair(ex2_approx(-q.x), ex2_approx(-q.y));
+    return split(fma2(pair(-fabsf(x0), -fabsf(x1)), mul2(h, e), pair(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f))));
+}
+
 template <int EPI>
 __device__ __forceinline__ float activate(float x) {
     if constexpr (EPI == EPI_RELU || EPI == EPI_RELU_AUX) {
@@ -921,7 +966,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 if (row_ok && has_bias) rbias = O::load(p.bias, row);
             }
             if constexpr (C::EXT) {
-                if (row_ok && has_bias && p.bias_row) rbias = O::load(p.bias, row);
+                if (!C::RES && row_ok && has_bias && p.bias_row) rbias = O::load(p.bias, row);
                 if (row_ok && p.scale_rows != nullptr) {
                     alpha = __ldg(p.scale_rows + row);
                     if (p.scale_b != nullptr) alpha *= __ldg(p.scale_b);
@@ -977,9 +1022,15 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                 }
                 ++res_issued;
             }
-            // RES: a chunk's column bias (one address for the whole warp), loaded as soon as the chunk
-            // before has used its own: there is no room in shared memory for copies of it
+            // RES: a chunk's bias in the output type.  Column bias: one address for the whole warp, loaded
+            // as soon as the chunk before has used its own (there is no room in shared memory for copies
+            // of it).  Row bias: this lane's row's, in every place.
             uint4 cb[C::RES ? 4 : 1] = {};
+            if constexpr (C::RES) if (has_bias && p.bias_row && row_ok) {
+                const uint32_t b = reinterpret_cast<const uint16_t *>(p.bias)[row] * 0x10001u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) cb[i] = make_uint4(b, b, b, b);
+            }
             auto load_bias = [&](int c) {
 #pragma unroll
                 for (int i = 0; i < (C::RES ? 4 : 0); ++i)
@@ -1075,15 +1126,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
                         float x0 = __uint_as_float(v[j]), x1 = __uint_as_float(v[j + 1]);
-                        x0 *= alpha;
-                        x1 *= alpha;
-                        if constexpr (C::FWD_BIAS) {
+                        if constexpr (C::RES) {
+                            const float2 b = O::unpack(word(cb, j));
+                            const float2 x = split(fma2(pair(x0, x1), both(alpha), pair(b.x, b.y)));
+                            x0 = x.x;
+                            x1 = x.y;
+                        } else {
+                            x0 *= alpha;
+                            x1 *= alpha;
+                        }
+                        if constexpr (C::FWD_BIAS && !C::RES) {
                             if constexpr (C::AXIS == AXIS_ROW) { x0 += rbias; x1 += rbias; }
-                            else if constexpr (C::RES) {
-                                const float2 b = O::unpack(word(cb, j));
-                                x0 += b.x;
-                                x1 += b.y;
-                            } else { x0 += bsm[32 * cl + j]; x1 += bsm[32 * cl + j + 1]; }
+                            else { x0 += bsm[32 * cl + j]; x1 += bsm[32 * cl + j + 1]; }
                             if constexpr (C::EXT) { x0 += rbias; x1 += rbias; }
                         }
                         if constexpr (C::BWD) {
@@ -1102,11 +1156,18 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             bits |= (x0 > 0.0f ? 1u : 0u) << j;
                             bits |= (x1 > 0.0f ? 1u : 0u) << (j + 1);
                         }
-                        float y0 = activate<C::EPI>(x0), y1 = activate<C::EPI>(x1);
+                        float y0, y1;
                         if constexpr (C::RES) {
+                            float2 y = make_float2(x0, x1);
+                            if constexpr (C::EPI == EPI_GELU) y = gelu_erf2(x0, x1);
+                            else y = make_float2(activate<C::EPI>(x0), activate<C::EPI>(x1));
                             const float2 r = O::unpack(word(rv, j));
-                            y0 += r.x;
-                            y1 += r.y;
+                            y = split(add2(pair(y.x, y.y), pair(r.x, r.y)));
+                            y0 = y.x;
+                            y1 = y.y;
+                        } else {
+                            y0 = activate<C::EPI>(x0);
+                            y1 = activate<C::EPI>(x1);
                         }
                         if constexpr (C::QOUT) {
                             amax_l = fmaxf(amax_l, fmaxf(fabsf(y0), fabsf(y1)));
