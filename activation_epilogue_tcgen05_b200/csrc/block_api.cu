@@ -3,6 +3,7 @@
 // before the device is looked at; nothing is allocated here.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <atomic>
 #include <cmath>
 #include <cstdio>
@@ -133,7 +134,7 @@ int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis) {
     if (m <= 0 || n <= 0 || m > 0x7fffffffll || n > 0x7fffffffll) return 0;
     if (bias_axis == GEMM_EPI_BIAS_ROW) return (n + DACT_COLS - 1) / DACT_COLS * m * (int64_t)sizeof(float);
     if (bias_axis != GEMM_EPI_BIAS_COL) return 0;
-    const int64_t rows = dact_rows(m, n);
+    const int64_t rows = std::min(dact_rows(m, n, true), dact_rows(m, n, false));      // whatever the epilogue
     return (m + rows - 1) / rows * n * (int64_t)sizeof(float);
 }
 
@@ -168,7 +169,7 @@ int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, 
     DactParams p{};
     p.m = m;
     p.n = (int)n;
-    p.rows = dact_rows(m, n);
+    p.rows = dact_rows(m, n, dact_reads_z(act));
     p.dd = dD;
     p.z = Z;
     p.aux = reinterpret_cast<const uint8_t *>(aux);

@@ -9,9 +9,10 @@
 //
 // Bound by HBM (dD and z read once, dZ written once).  A warp covers 256 columns of a row, a
 // lane 8 of them (one 16-byte load); a block of 8 warps covers a strip of 256 columns and a
-// run of rows, dealt to its warps in turn.  Column sums stay in a lane's registers over the
-// rows; row sums are one butterfly a row.  Either way the block writes fp32 partials, one a
-// strip or a run of rows, that a second small kernel adds in order.
+// run of rows, dealt to its warps in turn.  (Warps side by side, 4 KB of a row together, were
+// no faster.)  Column sums stay in a lane's registers over the rows; row sums are one butterfly
+// a row.  Either way the block writes fp32 partials, one a run of rows or a strip, that a second
+// small kernel adds in order.
 #pragma once
 #include <cstdint>
 
@@ -68,47 +69,86 @@ __device__ __forceinline__ f32x2 slope(float z0, float z1) {
     }
 }
 
+// With z to read, rows go through a ring of batches in shared memory, each thread copying its own vectors
+// (cp.async, as the norm's backward does): the next batch is on its way while the slopes of one are
+// worked out (8192 x 14336 GELU 114 us, loaded where it is used 134).  Without z there is little to work
+// out, and a batch is loaded into registers by four blocks an SM instead of three (bias alone 38.6 us,
+// through a ring 40.6; 1023 x 4104 from the mask 5.4 us against 7.0).
+constexpr int DACT_U = 4;                             // rows of a warp in a batch
+constexpr bool dact_reads_z(int act) { return act != DACT_NONE && act != DACT_RELU_MASK; }
+constexpr int DACT_RING = 2;
+constexpr int DACT_SMEM = DACT_RING * 2 * DACT_U * 32 * DACT_WARPS * 16;
+
 template <int DT, int ACT, int AXIS>
-__global__ void __launch_bounds__(32 * DACT_WARPS, 4) dact_kernel(const DactParams p) {
-    __shared__ float sums[DACT_WARPS][DACT_COLS];
+__global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_kernel(const DactParams p) {
+    constexpr int T = 32 * DACT_WARPS, U = DACT_U;
+    constexpr bool Z = dact_reads_z(ACT);
+    extern __shared__ uint4 ring[];                   // Z: [DACT_RING][U][dd, z][T]
+    __shared__ float4 sums[AXIS == AXIS_COL ? 64 * DACT_WARPS : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * DACT_COLS + 8 * lane;
     const bool col_ok = col < p.n;                    // n is a multiple of 8
     const int64_t r0 = (int64_t)blockIdx.y * p.rows, r1 = min(p.m, r0 + p.rows);
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    float acc[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-    constexpr int U = 4;                              // rows of a warp in flight
-    for (int64_t row = r0 + warp; row < r1; row += U * DACT_WARPS) {
-        uint4 dv[U], zv[U];
-        uint32_t mv[U];
+    auto fetch = [&](int64_t row, int stage) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t i = row + u * DACT_WARPS;
-            dv[u] = zv[u] = make_uint4(0u, 0u, 0u, 0u);
-            mv[u] = 0u;
             if (i < r1 && col_ok) {
-                dv[u] = ptx::ld_stream(static_cast<const uint16_t *>(p.dd) + i * p.n + col);
-                if constexpr (ACT == DACT_RELU_MASK) mv[u] = __ldg(p.aux + i * p.aux_pitch + col / 8);
-                else if constexpr (ACT != DACT_NONE) zv[u] = ptx::ld_stream(static_cast<const uint16_t *>(p.z) + i * p.n + col);
+                uint4 *dst = ring + (stage * U + u) * 2 * T + threadIdx.x;
+                ptx::cp_async_16(dst, static_cast<const uint16_t *>(p.dd) + i * p.n + col);
+                ptx::cp_async_16(dst + T, static_cast<const uint16_t *>(p.z) + i * p.n + col);
+            }
+        }
+        ptx::cp_async_commit();                       // (an empty group keeps the count)
+    };
+    float acc[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
+    int64_t row = r0 + warp;
+    constexpr int64_t step = U * DACT_WARPS;
+    if constexpr (Z) {
+#pragma unroll
+        for (int i = 0; i < DACT_RING; ++i) fetch(row + i * step, i);
+    }
+    int stage = 0;
+    for (; row < r1; row += step) {
+        uint4 dv[U];
+        uint32_t bits[U];
+        if constexpr (Z) {
+            ptx::cp_async_wait<DACT_RING - 1>();
+        } else {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const int64_t i = row + u * DACT_WARPS;
+                dv[u] = make_uint4(0u, 0u, 0u, 0u);
+                bits[u] = 0u;
+                if (i < r1 && col_ok) {
+                    dv[u] = ptx::ld_stream(static_cast<const uint16_t *>(p.dd) + i * p.n + col);
+                    if constexpr (ACT == DACT_RELU_MASK) bits[u] = __ldg(p.aux + i * p.aux_pitch + col / 8);
+                }
             }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t i = row + u * DACT_WARPS;
+            const bool ok = i < r1 && col_ok;
+            const uint4 *src = ring + (stage * U + u) * 2 * T + threadIdx.x;
             float d[8], z[8];
-            unpack8<DT>(dv[u], d);
+            if constexpr (Z) {
+                unpack8<DT>(ok ? src[0] : make_uint4(0u, 0u, 0u, 0u), d);
+                unpack8<DT>(ok ? src[T] : make_uint4(0u, 0u, 0u, 0u), z);
+            } else {
+                unpack8<DT>(dv[u], d);
+            }
             if constexpr (ACT == DACT_RELU_MASK) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) d[e] = ((mv[u] >> e) & 1u) ? d[e] : 0.0f;
+                for (int e = 0; e < 8; ++e) d[e] = ((bits[u] >> e) & 1u) ? d[e] : 0.0f;
             } else if constexpr (ACT == DACT_RELU) {
-                unpack8<DT>(zv[u], z);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = z[e] > 0.0f ? d[e] : 0.0f;
             } else if constexpr (ACT != DACT_NONE) {
-                unpack8<DT>(zv[u], z);
 #pragma unroll
                 for (int e = 0; e < 8; e += 2) {
                     const float2 f = split(mul2(pair(d[e], d[e + 1]), slope<ACT>(z[e], z[e + 1])));
@@ -117,12 +157,15 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, 4) dact_kernel(const DactPara
                 }
             }
             if constexpr (ACT != DACT_NONE) {
-                if (i < r1 && col_ok)
-                    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + i * p.n + col) = pack8<DT>(d);
+                if (ok) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + i * p.n + col) = pack8<DT>(d);
             }
             if constexpr (AXIS == AXIS_COL) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) acc[e] += d[e];
+                for (int e = 0; e < 8; e += 2) {
+                    const float2 f = split(add2(pair(acc[e], acc[e + 1]), pair(d[e], d[e + 1])));
+                    acc[e] = f.x;
+                    acc[e + 1] = f.y;
+                }
             } else if (p.partial != nullptr) {
                 float s = ((d[0] + d[1]) + (d[2] + d[3])) + ((d[4] + d[5]) + (d[6] + d[7]));
 #pragma unroll
@@ -130,17 +173,30 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, 4) dact_kernel(const DactPara
                 if (lane == 0 && i < r1) p.partial[(int64_t)blockIdx.x * p.m + i] = s;
             }
         }
+        if constexpr (Z) {
+            fetch(row + DACT_RING * step, stage);
+            if (++stage == DACT_RING) stage = 0;
+        }
     }
+    if constexpr (Z) ptx::cp_async_wait<0>();
     if constexpr (AXIS == AXIS_COL) {
         if (p.partial == nullptr) return;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sums[warp][8 * lane + e] = acc[e];
+        // the warps' sums, in order: [warp][half of a lane's 8][lane]
+        sums[(2 * warp) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        sums[(2 * warp + 1) * 32 + lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         __syncthreads();
-        const int c = blockIdx.x * DACT_COLS + threadIdx.x;
-        float s = sums[0][threadIdx.x];
+        if (threadIdx.x < 64 && col_ok) {             // (threads 32 to 63: the second halves)
+            float4 a = sums[threadIdx.x];
 #pragma unroll
-        for (int w = 1; w < DACT_WARPS; ++w) s += sums[w][threadIdx.x];
-        if (c < p.n) p.partial[(int64_t)blockIdx.y * p.n + c] = s;
+            for (int w = 1; w < DACT_WARPS; ++w) {
+                const float4 b = sums[64 * w + threadIdx.x];
+                a.x += b.x;
+                a.y += b.y;
+                a.z += b.z;
+                a.w += b.w;
+            }
+            reinterpret_cast<float4 *>(p.partial + (int64_t)blockIdx.y * p.n + col)[warp] = a;
+        }
     }
 }
 

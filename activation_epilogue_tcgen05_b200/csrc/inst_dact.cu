@@ -6,31 +6,29 @@
 
 namespace gemm_epi {
 
-// Runs of rows so that the launch has about 148 x 8 blocks, each run a whole number of the 32
-// rows that a block has in flight.
-int64_t dact_rows(int64_t m, int64_t n) {
-    const int64_t strips = (n + DACT_COLS - 1) / DACT_COLS;
-    const int64_t runs = std::max<int64_t>(1, std::min<int64_t>(148 * 8 / strips, 4096));
-    const int64_t rows = (m + runs - 1) / runs;
-    return (rows + 31) / 32 * 32;
+// Rows of a run: nearly whole waves of blocks -- three of three blocks an SM where z is read, two of
+// four elsewhere, on 148 SMs -- or runs of one batch of 32 rows.  With one wave some SMs have a block more
+// than others, and nothing evens that out (8192 x 14336 GELU: 392 blocks 135 us, 1288 blocks 115); a wave
+// with few blocks costs most of one (from the mask: 1120 blocks 86 us, 1232 blocks 99).
+int64_t dact_rows(int64_t m, int64_t n, bool reads_z) {
+    const int64_t strips = (n + DACT_COLS - 1) / DACT_COLS, batches = (m + 31) / 32;
+    const int64_t blocks = 148 * (reads_z ? 9 : 8);
+    const int64_t runs = std::max<int64_t>(1, std::min<int64_t>(blocks / strips, batches));
+    return (batches + runs - 1) / runs * 32;
 }
 
 namespace {
+template <int DT, int ACT, int AXIS>
+cudaError_t dact(const DactParams &p, bool pdl, cudaStream_t s) {
+    static std::atomic<bool> attr_done[64];
+    const dim3 grid((unsigned)((p.n + DACT_COLS - 1) / DACT_COLS), (unsigned)((p.m + p.rows - 1) / p.rows), 1);
+    constexpr int SMEM = dact_reads_z(ACT) ? DACT_SMEM : 0;
+    return launch_as(dact_kernel<DT, ACT, AXIS>, attr_done, grid, 32 * DACT_WARPS, SMEM, pdl, s, p);
+}
+
 template <int DT, int ACT>
 cudaError_t dact(int axis, const DactParams &p, bool pdl, cudaStream_t s) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)((p.n + DACT_COLS - 1) / DACT_COLS), (unsigned)((p.m + p.rows - 1) / p.rows), 1);
-    cfg.blockDim = dim3(32 * DACT_WARPS, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    if (pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    return axis == AXIS_COL ? cudaLaunchKernelEx(&cfg, dact_kernel<DT, ACT, AXIS_COL>, p)
-                            : cudaLaunchKernelEx(&cfg, dact_kernel<DT, ACT, AXIS_ROW>, p);
+    return axis == AXIS_COL ? dact<DT, ACT, AXIS_COL>(p, pdl, s) : dact<DT, ACT, AXIS_ROW>(p, pdl, s);
 }
 
 template <int DT>

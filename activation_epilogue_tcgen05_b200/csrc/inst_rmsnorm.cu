@@ -1,6 +1,5 @@
 // Launchers of the norm and its backward (rmsnorm.cuh).
 #include <algorithm>
-#include <atomic>
 
 #include "kernels.h"
 #include "rmsnorm.cuh"
@@ -8,27 +7,11 @@
 namespace gemm_epi {
 
 namespace {
-template <class... A, class... P>
-cudaError_t launch_as(void (*kern)(A...), int64_t grid, int threads, int smem, bool pdl, cudaStream_t s, P... p) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.dynamicSmemBytes = (size_t)smem;
-    cfg.gridDim = dim3((unsigned)grid, 1, 1);
-    cfg.blockDim = dim3((unsigned)threads, 1, 1);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    if (pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, kern, p...);
-}
-
 template <int DT, int OUT, int TPR, int VPT>
 cudaError_t fwd(const NormParams &p, bool pdl, cudaStream_t s) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR;
-    return launch_as(rmsnorm_kernel<DT, OUT, TPR, VPT>, (p.m + RPB - 1) / RPB, T, 0, pdl, s, p);
+    static std::atomic<bool> attr_done[64];
+    return launch_as(rmsnorm_kernel<DT, OUT, TPR, VPT>, attr_done, dim3((unsigned)((p.m + RPB - 1) / RPB)), T, 0, pdl, s, p);
 }
 
 // Four vectors a thread at every size: with one vector and more threads few rows were not done
@@ -90,16 +73,8 @@ BwdShape bwd_shape(int64_t m, int64_t d) {
 template <int DT, int TPR, int VPT>
 cudaError_t bwd_one(const NormBwdParams &p, int64_t grid, bool pdl, cudaStream_t s) {
     constexpr int T = norm_bwd_threads(TPR, VPT), SMEM = norm_ring_bytes(T, VPT);
-    auto kern = rmsnorm_bwd_kernel<DT, TPR, VPT>;
     static std::atomic<bool> attr_done[64];
-    int dev = 0;
-    cudaGetDevice(&dev);
-    if (dev < 0 || dev >= 64 || !attr_done[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
-        if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr_done[dev].store(true, std::memory_order_release);
-    }
-    return launch_as(kern, grid, T, SMEM, pdl, s, p);
+    return launch_as(rmsnorm_bwd_kernel<DT, TPR, VPT>, attr_done, dim3((unsigned)grid), T, SMEM, pdl, s, p);
 }
 
 template <int DT>
@@ -149,10 +124,14 @@ cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStr
 }
 
 namespace {
+template <int DT, int Y>
+cudaError_t add_parts(const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s) {
+    static std::atomic<bool> attr_done[64];
+    return launch_as(add_parts_kernel<DT, Y>, attr_done, dim3((unsigned)((len + 31) / 32)), 8 * Y, 0, pdl, s, src, parts, len, out);
+}
 template <int DT>
 cudaError_t add_parts(const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s) {
-    if (parts <= 320) return launch_as(add_parts_kernel<DT, 32>, (len + 31) / 32, 256, 0, pdl, s, src, parts, len, out);
-    return launch_as(add_parts_kernel<DT, 64>, (len + 31) / 32, 512, 0, pdl, s, src, parts, len, out);
+    return parts <= 320 ? add_parts<DT, 32>(src, parts, len, out, pdl, s) : add_parts<DT, 64>(src, parts, len, out, pdl, s);
 }
 }  // namespace
 
@@ -161,7 +140,8 @@ cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t le
 }
 
 cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s) {
-    return launch_as(zero_word_kernel, 1, 32, 0, pdl, s, w);
+    static std::atomic<bool> attr_done[64];
+    return launch_as(zero_word_kernel, attr_done, dim3(1), 32, 0, pdl, s, w);
 }
 
 }  // namespace gemm_epi

@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "gemm_splitk.cuh"
@@ -93,8 +94,8 @@ cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStr
 // out[i] = sum_p src[p * len + i], fp32 partials, len a multiple of 8, out in dt
 cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s);
 cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s);
-// rows of a block's run, from (m, n) alone; the launch has ceil(m / rows) runs
-int64_t dact_rows(int64_t m, int64_t n);
+// rows of a block's run, from the sizes and whether z is read; the launch has ceil(m / rows) runs
+int64_t dact_rows(int64_t m, int64_t n, bool reads_z);
 cudaError_t launch_dact(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s);
 
 // per-dtype halves of the lookups (one instantiation unit each)
@@ -129,6 +130,35 @@ bool find_sg_e4m3_q(int epi, int axis, bool w_mn, int nm, SgLauncher *, KernelIn
 constexpr int tc_stages(int stage_bytes) { return (GEMM_EPI_RING_KB * 1024) / stage_bytes; }
 
 // Shared launch helpers used by the instantiation units.
+
+// Launch of a kernel of the norm's or the epilogue's backward's kind; its first launch on a device sets
+// its shared memory.  (Asking for the GEMM kernels' shared-memory split as well takes the L1 that
+// loads in flight need: a block's rows from the mask at 8192 x 14336 100 us instead of 87.)
+template <class... A, class... P>
+cudaError_t launch_as(void (*kern)(A...), std::atomic<bool> (&attr_done)[64], dim3 grid, int threads, int smem, bool pdl,
+                      cudaStream_t s, P... p) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (smem > 0 && (dev < 0 || dev >= 64 || !attr_done[dev].load(std::memory_order_acquire))) {
+        const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev].store(true, std::memory_order_release);
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads, 1, 1);
+    cfg.dynamicSmemBytes = (size_t)smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    if (pdl) {
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, kern, p...);
+}
+
 template <class C>
 cudaError_t launch_tc(const TcLaunch &L) {
     auto kern = tc_gemm_kernel<C>;

@@ -547,6 +547,7 @@ class RmsNorm:
         self._out_t = self._t if out == "same" else torch.float8_e4m3fn
         self._f32 = torch.float32
         self._scales = self.m if out == "e4m3_rows" else 1
+        self._scratch_bytes = gemm_epi_rmsnorm_workspace_bytes(self.m, self.d)
 
     def run(self, X, gamma, Y, residual=None, S=None, scale=None, amax=None, stream=None):
         """S = X + residual (X without one), Y = S / rms(S) * gamma; ``scale`` and ``amax`` as in
@@ -568,7 +569,7 @@ class RmsNorm:
         dev, s = _device_and_stream(stream)
         n, t = self.m * self.d, self._t
         if dgamma is not None:
-            workspace = _workspace(workspace, gemm_epi_rmsnorm_workspace_bytes(self.m, self.d), "RmsNorm.run_bwd", dev, stream)
+            workspace = _workspace(workspace, self._scratch_bytes, "RmsNorm.run_bwd", dev, stream)
         gemm_epi_rmsnorm_bwd(self.m, self.d, self._dt, self.eps, _operand(dY, "RmsNorm.run_bwd: dY", t, n, dev),
                              _operand(S, "RmsNorm.run_bwd: S", t, n, dev),
                              _operand(gamma, "RmsNorm.run_bwd: gamma", t, self.d, dev),
@@ -589,6 +590,8 @@ class ActBackward:
         self._t = torch.float16 if dtype == "f16" else torch.bfloat16
         self._i32 = torch.int32
         self._len = self.m if bias_axis == "row" else self.n
+        self._aux_words = self.m * aux_pitch_words(self.n)
+        self._scratch_bytes = gemm_epi_dact_workspace_bytes(self.m, self.n, AXIS[bias_axis])
 
     def run(self, dD, dZ=None, z=None, aux=None, dbias=None, workspace=None, stream=None):
         """``z``: the pre-activation (ReLU, GELU, tanh); ``aux``: the forward's packed mask as int32 words
@@ -597,12 +600,10 @@ class ActBackward:
         dev, s = _device_and_stream(stream)
         n, t = self.m * self.n, self._t
         if dbias is not None:
-            workspace = _workspace(workspace, gemm_epi_dact_workspace_bytes(self.m, self.n, self._args[2]), "ActBackward.run",
-                                   dev, stream)
+            workspace = _workspace(workspace, self._scratch_bytes, "ActBackward.run", dev, stream)
         gemm_epi_dact(self.m, self.n, *self._args, _operand(dD, "ActBackward.run: dD", t, n, dev),
                       _operand(z, "ActBackward.run: z", t, n, dev, True),
-                      None if aux is None else _operand(aux, "ActBackward.run: aux", self._i32,
-                                                        self.m * aux_pitch_words(self.n), dev),
+                      _operand(aux, "ActBackward.run: aux", self._i32, self._aux_words, dev, True),
                       _operand(dZ, "ActBackward.run: dZ", t, n, dev, True),
                       _operand(dbias, "ActBackward.run: dbias", t, self._len, dev, True),
                       None if dbias is None else workspace.data_ptr(), s)

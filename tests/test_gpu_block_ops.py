@@ -203,6 +203,36 @@ def test_norm_bwd_in_place(d, over):
     assert torch.equal(b[over], dX) and torch.equal(dg2, dg)
 
 
+@pytest.mark.parametrize("over", ["dy", "s", "ds"])
+@pytest.mark.parametrize("m,d", [(5000, 64), (3000, 1024), (1500, 4096), (400, 16384)])
+def test_norm_bwd_in_place_over_many_rows(m, d, over):
+    """A block's later rows are on their way while an earlier one is overwritten."""
+    b = {"dy": randn(m, d, seed=1), "s": randn(m, d, seed=2), "ds": randn(m, d, seed=3)}
+    gamma = randn(d, seed=4)
+    dX, dg = run_norm_bwd(b["dy"], b["s"], gamma, b["ds"], "bf16")
+    ref.check_norm_bwd("bf16", b["dy"], b["s"], gamma, b["ds"], EPS, dX, dg)
+    dg2 = torch.empty_like(gamma)
+    g.RmsNorm(m, d).run_bwd(b["dy"], b["s"], gamma, b[over], dgamma=dg2, dS=b["ds"])
+    assert torch.equal(b[over], dX) and torch.equal(dg2, dg)
+
+
+def test_scratch_of_a_given_stream():
+    """Scratch from torch's allocator belongs to the stream of the call: a Stream, its raw handle, the default."""
+    dy, s, gamma = randn(500, 1024, seed=1), randn(500, 1024, seed=2), randn(1024, seed=3)
+    dX, dg = run_norm_bwd(dy, s, gamma, None, "bf16")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for st in (side, side.cuda_stream, torch.cuda.default_stream(), 0):
+        out, dgamma, db = torch.empty_like(dy), torch.empty_like(gamma), torch.empty_like(gamma)
+        side.wait_stream(torch.cuda.current_stream())
+        for _ in range(3):
+            g.RmsNorm(500, 1024).run_bwd(dy, s, gamma, out, dgamma=dgamma, stream=st)
+            g.ActBackward(500, 1024, "bf16", "bias", "col").run(dy, dbias=db, stream=st)
+        torch.cuda.synchronize()
+        assert torch.equal(out, dX) and torch.equal(dgamma, dg)
+        ref.check_dact("bias", "col", "bf16", dy, torch.zeros(500, 1024), None, db)
+
+
 def test_norm_gradients_against_differences():
     """Along random directions, the kernel's gradients against central differences of the forward formula."""
     m, d = 6, 512
@@ -293,12 +323,13 @@ def test_dact_far_from_zero(epilogue):
     ref.check_dact(epilogue, "col", "f16", dd, z, dZ, db)
 
 
+@pytest.mark.parametrize("m", [70, 20000])
 @pytest.mark.parametrize("over", ["dd", "z"])
-def test_dact_in_place(over):
-    b = {"dd": randn(70, 520, seed=5), "z": randn(70, 520, seed=6)}
+def test_dact_in_place(over, m):
+    b = {"dd": randn(m, 520, seed=5), "z": randn(m, 520, seed=6)}
     want = run_dact(b["dd"], b["z"], "bf16", "gelu_bias", "col")
     db = torch.empty(520, dtype=torch.bfloat16, device="cuda")
-    g.ActBackward(70, 520, "bf16", "gelu_bias", "col").run(b["dd"], dZ=b[over], z=b["z"], dbias=db)
+    g.ActBackward(m, 520, "bf16", "gelu_bias", "col").run(b["dd"], dZ=b[over], z=b["z"], dbias=db)
     assert torch.equal(b[over], want[0]) and torch.equal(db, want[1])
 
 
