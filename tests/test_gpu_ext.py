@@ -253,6 +253,21 @@ def test_captured_and_replayed_and_on_a_side_stream():
             del graph
 
 
+@pytest.mark.parametrize("kernel,block_n", [("tc1", 128), ("tc2", 256)])
+def test_a_wait_that_runs_out_is_reported(kernel, block_n):
+    """The accumulator never comes: the kernel gives up after about a second, with the residual's load landed, and says so; the
+    next run of the same sizes is right."""
+    c = Case(300, 336, 272, "bf16", "bias")
+    D = torch.full((300, 336), 5.0, dtype=torch.bfloat16, device="cuda")
+    with c.plan(kernel=kernel, block_n=block_n, inject_stall=1) as p:
+        p.run_ext(c.a, c.b, c.bias, D, residual=c.res)
+        with pytest.raises(g.GemmEpiError) as e:
+            p.check()
+        assert e.value.status == g.ERR_TIMEOUT
+    assert bool((D == 5).all())
+    c.check(kernel=kernel, block_n=block_n)
+
+
 def test_refusals():
     c = Case(130, 272, 144, "bf16", "bias", rows=True)
     D = c.out()
