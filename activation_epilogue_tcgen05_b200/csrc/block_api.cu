@@ -105,7 +105,8 @@ int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void 
                          const void *dS, void *dX, void *dgamma, void *workspace, void *stream) {
     int rc = check_norm(m, d, dtype, eps, 8);
     if (rc != GEMM_EPI_OK) return rc;
-    if (!dY || !S || !gamma || !dX || (dgamma && !workspace)) return GEMM_EPI_ERR_NULL;
+    const int64_t parts = dgamma ? norm_bwd_parts(m, d) : 0;
+    if (!dY || !S || !gamma || !dX || (parts > 0 && !workspace)) return GEMM_EPI_ERR_NULL;
     if (!aligned(dY, 16) || !aligned(S, 16) || !aligned(gamma, 16) || !aligned(dS, 16) || !aligned(dX, 16) ||
         !aligned(dgamma, 16) || !aligned(workspace, 16))
         return GEMM_EPI_ERR_ALIGN;
@@ -123,11 +124,12 @@ int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void 
     p.gamma = gamma;
     p.ds = dS;
     p.dx = dX;
-    p.partial = dgamma ? static_cast<float *>(workspace) : nullptr;
+    p.partial = parts > 0 ? static_cast<float *>(workspace) : nullptr;
+    p.dgamma = parts > 0 ? nullptr : dgamma;
     const bool pdl = pdl_enabled();
     rc = status(launch_rmsnorm_bwd(dt, p, pdl, s));
-    if (rc != GEMM_EPI_OK || !dgamma) return rc;
-    return status(launch_add_parts(dt, p.partial, norm_bwd_parts(m, d), d, dgamma, pdl, s));
+    if (rc != GEMM_EPI_OK || parts == 0) return rc;
+    return status(launch_add_parts(dt, p.partial, parts, d, dgamma, pdl, s));
 }
 
 int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis) {

@@ -50,6 +50,10 @@ bool few_rows(int64_t m, int64_t d) { return m * (d / 8) <= 148 * 1024; }
 struct BwdShape {
     int tpr, vpt;
 };
+int64_t bwd_blocks(int64_t m, BwdShape b) {
+    const int rpb = norm_bwd_threads(b.tpr, b.vpt) / b.tpr;
+    return std::min<int64_t>((m + rpb - 1) / rpb, NORM_BWD_BLOCKS);
+}
 BwdShape bwd_shape(int64_t m, int64_t d) {
     const int64_t nv = d / 8;
     if (few_rows(m, d)) {
@@ -77,10 +81,26 @@ cudaError_t bwd_one(const NormBwdParams &p, int64_t grid, bool pdl, cudaStream_t
     return launch_as(rmsnorm_bwd_kernel<DT, TPR, VPT>, attr_done, dim3((unsigned)grid), T, SMEM, pdl, s, p);
 }
 
+template <int DT, int TPR>
+cudaError_t bwd_cluster(const NormBwdParams &p, bool pdl, cudaStream_t s) {
+    constexpr int SMEM = norm_ring_bytes(NORM_CLUSTER_T, 1);
+    static std::atomic<bool> attr_done[64];
+    return launch_as_cluster(rmsnorm_bwd_kernel<DT, TPR, 1, true>, attr_done, dim3(NORM_CLUSTER), NORM_CLUSTER_T, SMEM, pdl,
+                             NORM_CLUSTER, s, p);
+}
+
 template <int DT>
 cudaError_t bwd(const NormBwdParams &p, bool pdl, cudaStream_t s) {
     const BwdShape b = bwd_shape(p.m, p.d);
-    const int64_t grid = norm_bwd_parts(p.m, p.d);
+    if (p.dgamma != nullptr) {
+        switch (b.tpr) {
+        case 8: return bwd_cluster<DT, 8>(p, pdl, s);
+        case 32: return bwd_cluster<DT, 32>(p, pdl, s);
+        case 128: return bwd_cluster<DT, 128>(p, pdl, s);
+        default: return bwd_cluster<DT, 512>(p, pdl, s);
+        }
+    }
+    const int64_t grid = bwd_blocks(p.m, b);
     if (b.vpt == 1) {
         switch (b.tpr) {
         case 8: return bwd_one<DT, 8, 1>(p, grid, pdl, s);
@@ -111,8 +131,9 @@ __global__ void zero_word_kernel(unsigned int *w) {
 
 int64_t norm_bwd_parts(int64_t m, int64_t d) {
     const BwdShape b = bwd_shape(m, d);
-    const int rpb = norm_bwd_threads(b.tpr, b.vpt) / b.tpr;
-    return std::min<int64_t>((m + rpb - 1) / rpb, NORM_BWD_BLOCKS);
+    // one vector a thread and at most two turns of a cluster's rows: no partial rows
+    if (b.vpt == 1 && m <= 2 * NORM_CLUSTER * (NORM_CLUSTER_T / b.tpr)) return 0;
+    return bwd_blocks(m, b);
 }
 
 cudaError_t launch_rmsnorm(int dt, int out, const NormParams &p, bool pdl, cudaStream_t s) {

@@ -87,7 +87,8 @@ struct NormParams;
 struct NormBwdParams;
 struct DactParams;
 constexpr int NORM_MAX_D = 16384;
-// blocks of a backward launch = rows of its partial sums, from (m, d) alone
+// partial rows that a backward launch with dgamma writes, from (m, d) alone; 0: the launch writes
+// dgamma itself (NormBwdParams::dgamma)
 int64_t norm_bwd_parts(int64_t m, int64_t d);
 cudaError_t launch_rmsnorm(int dt, int out, const NormParams &p, bool pdl, cudaStream_t s);
 cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStream_t s);
@@ -135,8 +136,8 @@ constexpr int tc_stages(int stage_bytes) { return (GEMM_EPI_RING_KB * 1024) / st
 // its shared memory.  (Asking for the GEMM kernels' shared-memory split as well takes the L1 that
 // loads in flight need: a block's rows from the mask at 8192 x 14336 100 us instead of 87.)
 template <class... A, class... P>
-cudaError_t launch_as(void (*kern)(A...), std::atomic<bool> (&attr_done)[64], dim3 grid, int threads, int smem, bool pdl,
-                      cudaStream_t s, P... p) {
+cudaError_t launch_as_cluster(void (*kern)(A...), std::atomic<bool> (&attr_done)[64], dim3 grid, int threads, int smem, bool pdl,
+                              int cluster, cudaStream_t s, P... p) {
     int dev = 0;
     cudaGetDevice(&dev);
     if (smem > 0 && (dev < 0 || dev >= 64 || !attr_done[dev].load(std::memory_order_acquire))) {
@@ -149,16 +150,30 @@ cudaError_t launch_as(void (*kern)(A...), std::atomic<bool> (&attr_done)[64], di
     cfg.blockDim = dim3((unsigned)threads, 1, 1);
     cfg.dynamicSmemBytes = (size_t)smem;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    if (pdl) {
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (cluster > 1) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = (unsigned)cluster;
+        attr[na].val.clusterDim.y = 1;
+        attr[na].val.clusterDim.z = 1;
+        ++na;
     }
+    if (pdl) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[na].val.programmaticStreamSerializationAllowed = 1;
+        ++na;
+    }
+    cfg.attrs = na ? attr : nullptr;
+    cfg.numAttrs = na;
     return cudaLaunchKernelEx(&cfg, kern, p...);
 }
 
+template <class... A, class... P>
+cudaError_t launch_as(void (*kern)(A...), std::atomic<bool> (&attr_done)[64], dim3 grid, int threads, int smem, bool pdl,
+                      cudaStream_t s, P... p) {
+    return launch_as_cluster(kern, attr_done, grid, threads, smem, pdl, 1, s, p...);
+}
 template <class C>
 cudaError_t launch_tc(const TcLaunch &L) {
     auto kern = tc_gemm_kernel<C>;

@@ -140,6 +140,15 @@ __device__ __forceinline__ void st_async_v4(uint32_t addr, float a, float b, flo
                  ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d), "r"(bar)
                  : "memory");
 }
+// 16 bytes of another CTA's shared memory (address from mapa).
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t addr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
 __device__ __forceinline__ void st_cluster_v4(uint32_t addr, float a, float b, float c, float d) {
     asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b),
                  "f"(c), "f"(d)

@@ -568,7 +568,9 @@ class RmsNorm:
         gemm_epi_rmsnorm_workspace_bytes(m, d) bytes, taken from torch's allocator when left out."""
         dev, s = _device_and_stream(stream)
         n, t = self.m * self.d, self._t
-        if dgamma is not None:
+        if dgamma is None or not self._scratch_bytes:
+            workspace = None
+        else:
             workspace = _workspace(workspace, self._scratch_bytes, "RmsNorm.run_bwd", dev, stream)
         gemm_epi_rmsnorm_bwd(self.m, self.d, self._dt, self.eps, _operand(dY, "RmsNorm.run_bwd: dY", t, n, dev),
                              _operand(S, "RmsNorm.run_bwd: S", t, n, dev),
@@ -576,7 +578,7 @@ class RmsNorm:
                              _operand(dS, "RmsNorm.run_bwd: dS", t, n, dev, True),
                              _operand(dX, "RmsNorm.run_bwd: dX", t, n, dev),
                              _operand(dgamma, "RmsNorm.run_bwd: dgamma", t, self.d, dev, True),
-                             None if dgamma is None else workspace.data_ptr(), s)
+                             None if workspace is None else workspace.data_ptr(), s)
 
 
 class ActBackward:

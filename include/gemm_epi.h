@@ -451,7 +451,7 @@ enum gemm_epi_norm_out {
 int gemm_epi_rmsnorm(int64_t m, int64_t d, int dtype, int out_mode, float eps, const void *X, const void *R,
                      const void *gamma, void *S, void *Y, float *d_scale, float *d_amax, void *stream);
 
-/* Bytes of scratch that gemm_epi_rmsnorm_bwd needs for dgamma (0 for sizes it refuses). */
+/* Bytes of scratch that gemm_epi_rmsnorm_bwd needs for dgamma (0: none, or sizes it refuses). */
 int64_t gemm_epi_rmsnorm_workspace_bytes(int64_t m, int64_t d);
 
 /* Backward of gemm_epi_rmsnorm, from the sum S it stored (X itself without a residual):
@@ -464,9 +464,10 @@ int64_t gemm_epi_rmsnorm_workspace_bytes(int64_t m, int64_t d);
  *   dgamma  length d, in dtype, NULL: not wanted.  Summed in fp32 in an order fixed by (m, d),
  *           rounded once.
  *   workspace  16-byte aligned device memory of gemm_epi_rmsnorm_workspace_bytes(m, d) bytes,
- *           needed with dgamma (else NULL).  It holds nothing between calls; calls that may run
- *           at the same time (other streams, graphs that are replayed together) need one each.
- * Rules, limits and statuses as for gemm_epi_rmsnorm; one launch, two with dgamma. */
+ *           needed with dgamma (may be NULL without it, or where that is 0 bytes).  It holds nothing
+ *           between calls; calls that may run at the same time (other streams, graphs that are
+ *           replayed together) need one each.
+ * Rules, limits and statuses as for gemm_epi_rmsnorm; one launch, two with dgamma and scratch. */
 int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void *dY, const void *S,
                          const void *gamma, const void *dS, void *dX, void *dgamma, void *workspace, void *stream);
 

@@ -51,7 +51,7 @@ def test_norm_refusals(g, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(m=0), "ERR_ARG"), (dict(d=-8), "ERR_ARG"), (dict(dtype=2), "ERR_ARG"), (dict(eps=0.0), "ERR_ARG"),
     (dict(d=4), "ERR_ALIGN"), (dict(d=16392), "ERR_UNSUPPORTED"), (dict(dY=None), "ERR_NULL"), (dict(S=None), "ERR_NULL"),
-    (dict(gamma=None), "ERR_NULL"), (dict(dX=None), "ERR_NULL"), (dict(dgamma=P), "ERR_NULL"),
+    (dict(gamma=None), "ERR_NULL"), (dict(dX=None), "ERR_NULL"), (dict(m=2000, dgamma=P), "ERR_NULL"),
     (dict(dY=P + 8), "ERR_ALIGN"), (dict(dS=P + 8), "ERR_ALIGN"), (dict(dgamma=P, ws=P + 4), "ERR_ALIGN"),
 ])
 def test_norm_bwd_refusals(g, kw, code):
@@ -73,12 +73,14 @@ def test_valid_calls_without_a_gpu_report_no_device(g):
     if torch.cuda.is_available():
         pytest.skip("a GPU is present")
     assert norm_rc(g) == norm_rc(g, R=P, S=P) == norm_rc(g, Y=P) == norm_rc(g, out=2, scale=P) == g.ERR_NO_DEVICE
-    assert bwd_rc(g) == bwd_rc(g, dgamma=P, ws=P, dS=P) == g.ERR_NO_DEVICE
+    assert bwd_rc(g) == bwd_rc(g, dgamma=P, dS=P) == bwd_rc(g, m=2000, dgamma=P, ws=P, dS=P) == g.ERR_NO_DEVICE
     assert dact_rc(g) == dact_rc(g, epi=1, dZ=None, dbias=P, ws=P) == dact_rc(g, epi=3, aux=P, Z=None) == g.ERR_NO_DEVICE
 
 
 def test_scratch_sizes(g):
-    for m, d in [(1, 8), (1, 16384), (37, 1000), (65537, 128), (2_000_000, 4096)]:
+    for m, d in [(1, 8), (37, 1000), (64, 1024), (16, 4096), (1024, 64)]:
+        assert g.gemm_epi_rmsnorm_workspace_bytes(m, d) == 0         # one cluster: no partial rows
+    for m, d in [(1, 16384), (65, 1024), (17, 4096), (1025, 64), (65537, 128), (2_000_000, 4096)]:
         b = g.gemm_epi_rmsnorm_workspace_bytes(m, d)
         assert b > 0 and b % (4 * d) == 0 and b // (4 * d) <= m      # whole rows of fp32, no more than the input's
         assert b <= 4 * d * 148 * 4

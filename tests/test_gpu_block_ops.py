@@ -173,7 +173,7 @@ def run_norm_bwd(dy, s, gamma, ds, dtype, eps=EPS, want=True, **kw):
 
 @pytest.mark.parametrize("skip", [False, True])
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
-@pytest.mark.parametrize("m,d", SHAPES + [(5, 8), (37, 1000), (700, 4104), (1500, 264), (301, 16376)])
+@pytest.mark.parametrize("m,d", SHAPES + [(5, 8), (37, 1000), (64, 1024), (65, 1024), (16, 4096), (17, 4096), (256, 256), (257, 248), (1024, 64), (1025, 64), (700, 4104), (1500, 264), (301, 16376)])
 def test_norm_bwd(m, d, dtype, skip):
     dy, s, gamma = randn(m, d, seed=1, dtype=dtype), randn(m, d, seed=2, dtype=dtype, scale=2.0), randn(d, seed=3, dtype=dtype)
     ds = randn(m, d, seed=4, dtype=dtype) if skip else None
@@ -370,7 +370,9 @@ def test_objects_refuse_tensors_that_do_not_fit():
     with pytest.raises(g.GemmEpiError):
         g.RmsNorm(4, 64, out="e4m3_rows").run(x, gamma, torch.empty(4, 64, dtype=E4M3, device="cuda"))       # no scales
     with pytest.raises(g.GemmEpiError):
-        op.run_bwd(x, x, gamma, y, dgamma=torch.empty_like(gamma), workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        b = randn(2000, 64)
+        g.RmsNorm(2000, 64).run_bwd(b, b, gamma, torch.empty_like(b), dgamma=torch.empty_like(gamma),
+                                    workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(g.GemmEpiError):
         g.ActBackward(4, 64, "bf16", "gelu").run(x, dZ=y)                                                  # no z
     with pytest.raises(g.GemmEpiError):
