@@ -97,7 +97,7 @@ int gemm_epi_rmsnorm(int64_t m, int64_t d, int dtype, int out_mode, float eps, c
 }
 
 int64_t gemm_epi_rmsnorm_workspace_bytes(int64_t m, int64_t d) {
-    if (m <= 0 || d <= 0 || d > NORM_MAX_D || m > 0x7fffffffll) return 0;
+    if (m <= 0 || d <= 0 || d > NORM_MAX_D || d % 8 != 0 || m > 0x7fffffffll) return 0;
     return norm_bwd_parts(m, d) * d * (int64_t)sizeof(float);
 }
 
@@ -134,6 +134,8 @@ int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void 
 
 int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis) {
     if (m <= 0 || n <= 0 || m > 0x7fffffffll || n > 0x7fffffffll) return 0;
+    if (n % 8 != 0) return 0;
+    if (bias_axis == GEMM_EPI_BIAS_ROW && dact_by_rows(m, n)) return 0;
     if (bias_axis == GEMM_EPI_BIAS_ROW) return (n + DACT_COLS - 1) / DACT_COLS * m * (int64_t)sizeof(float);
     if (bias_axis != GEMM_EPI_BIAS_COL) return 0;
     const int64_t rows = std::min(dact_rows(m, n, true), dact_rows(m, n, false));      // whatever the epilogue
@@ -158,7 +160,8 @@ int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, 
     const bool mask = act == DACT_RELU_MASK;
     if (!dD || (mask && !aux) || (!mask && act != DACT_NONE && !Z)) return GEMM_EPI_ERR_NULL;
     if (act == DACT_NONE ? !dbias : !dZ) return GEMM_EPI_ERR_NULL;
-    if (dbias && !workspace) return GEMM_EPI_ERR_NULL;
+    const bool by_rows = dbias && bias_axis == GEMM_EPI_BIAS_ROW && dact_by_rows(m, n);
+    if (dbias && !by_rows && !workspace) return GEMM_EPI_ERR_NULL;
     if (act == DACT_NONE && dZ) return GEMM_EPI_ERR_ARG;          // dZ is dD itself
     if (!aligned(dD, 16) || (act != DACT_NONE && !mask && !aligned(Z, 16)) || (mask && !aligned(aux, 16)) ||
         !aligned(dZ, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
@@ -177,10 +180,11 @@ int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, 
     p.aux = reinterpret_cast<const uint8_t *>(aux);
     p.aux_pitch = gemm_epi_aux_pitch_bytes(n);
     p.dz = dZ;
-    p.partial = dbias ? static_cast<float *>(workspace) : nullptr;
+    p.partial = dbias && !by_rows ? static_cast<float *>(workspace) : nullptr;
+    p.dbias = by_rows ? dbias : nullptr;
     const bool pdl = pdl_enabled();
     rc = status(launch_dact(dt, act, axis, p, pdl, s));
-    if (rc != GEMM_EPI_OK || !dbias) return rc;
+    if (rc != GEMM_EPI_OK || !p.partial) return rc;
     const int64_t parts = axis == AXIS_COL ? (m + p.rows - 1) / p.rows : (n + DACT_COLS - 1) / DACT_COLS;
     const int64_t len = axis == AXIS_COL ? n : m;
     return status(len % 8 == 0 ? launch_add_parts(dt, p.partial, parts, len, dbias, pdl, s)

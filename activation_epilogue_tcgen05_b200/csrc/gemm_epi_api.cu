@@ -539,7 +539,6 @@ int find_ext(const Plan *P, TcLauncher *tc, SkLauncher *sk, int *katoms) {
     const bool b_mn = P->b_layout == GEMM_EPI_B_KN;
     KernelInfo info;
     if (P->a_km || P->sk_grid || P->bwd) return GEMM_EPI_ERR_UNSUPPORTED;
-
     if (P->kernel == GEMM_EPI_KERNEL_SPLITK)
         return find_sk_ext(P->dtype, P->kepi, b_mn, P->nm, P->qout, sk, &info) ? GEMM_EPI_OK : GEMM_EPI_ERR_UNSUPPORTED;
     if (!find_tc_ext(P->kernel == GEMM_EPI_KERNEL_TC2 ? 2 : 1, P->dtype, P->kepi, b_mn, ext_block_n(P), P->qout, tc, &info))

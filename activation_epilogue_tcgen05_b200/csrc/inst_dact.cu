@@ -17,6 +17,11 @@ int64_t dact_rows(int64_t m, int64_t n, bool reads_z) {
     return (batches + runs - 1) / runs * 32;
 }
 
+// Whole rows to a block: where their blocks fill the GPU (148 SMs, three each), or rows of up to three
+// passes (8192 x 14336 GELU 108 us, by strips 117; 1023 x 4104 from the mask 4.7 against 5.5, 64 x 4096 2.9
+// against 3.4; not 300 x 16384, 12.5 against 11.0, nor 16 x 16384, 10.3 against 4.0).
+bool dact_by_rows(int64_t m, int64_t n) { return m >= 148 * 3 * DACT_U || n <= 3 * DACT_WARPS * DACT_COLS; }
+
 namespace {
 template <int DT, int ACT, int AXIS>
 cudaError_t dact(const DactParams &p, bool pdl, cudaStream_t s) {
@@ -27,7 +32,16 @@ cudaError_t dact(const DactParams &p, bool pdl, cudaStream_t s) {
 }
 
 template <int DT, int ACT>
+cudaError_t dact_whole_rows(const DactParams &p, bool pdl, cudaStream_t s) {
+    static std::atomic<bool> attr_done[64];
+    constexpr int SMEM = dact_reads_z(ACT) ? DACT_SMEM : 0;
+    return launch_as(dact_rows_kernel<DT, ACT>, attr_done, dim3((unsigned)((p.m + DACT_U - 1) / DACT_U)), 32 * DACT_WARPS, SMEM,
+                     pdl, s, p);
+}
+
+template <int DT, int ACT>
 cudaError_t dact(int axis, const DactParams &p, bool pdl, cudaStream_t s) {
+    if (p.dbias != nullptr) return dact_whole_rows<DT, ACT>(p, pdl, s);
     return axis == AXIS_COL ? dact<DT, ACT, AXIS_COL>(p, pdl, s) : dact<DT, ACT, AXIS_ROW>(p, pdl, s);
 }
 

@@ -120,6 +120,7 @@ cudaError_t bwd(const NormBwdParams &p, bool pdl, cudaStream_t s) {
     default: return bwd_one<DT, 512, 4>(p, grid, pdl, s);
     }
 }
+
 // Sets the word that a launch max-reduces into to 0: a launch of the library's own, since a memset
 // between two launches keeps the second from being set up during the first (4 us a call).
 __global__ void zero_word_kernel(unsigned int *w) {

@@ -97,6 +97,8 @@ cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t le
 cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s);
 // rows of a block's run, from the sizes and whether z is read; the launch has ceil(m / rows) runs
 int64_t dact_rows(int64_t m, int64_t n, bool reads_z);
+// ROW axis: whether the launch writes dbias itself (DactParams::dbias), without partials
+bool dact_by_rows(int64_t m, int64_t n);
 cudaError_t launch_dact(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s);
 
 // per-dtype halves of the lookups (one instantiation unit each)

@@ -601,14 +601,16 @@ class ActBackward:
         ``workspace``: as for RmsNorm.run_bwd (gemm_epi_dact_workspace_bytes)."""
         dev, s = _device_and_stream(stream)
         n, t = self.m * self.n, self._t
-        if dbias is not None:
+        if dbias is None or not self._scratch_bytes:
+            workspace = None
+        else:
             workspace = _workspace(workspace, self._scratch_bytes, "ActBackward.run", dev, stream)
         gemm_epi_dact(self.m, self.n, *self._args, _operand(dD, "ActBackward.run: dD", t, n, dev),
                       _operand(z, "ActBackward.run: z", t, n, dev, True),
                       _operand(aux, "ActBackward.run: aux", self._i32, self._aux_words, dev, True),
                       _operand(dZ, "ActBackward.run: dZ", t, n, dev, True),
                       _operand(dbias, "ActBackward.run: dbias", t, self._len, dev, True),
-                      None if dbias is None else workspace.data_ptr(), s)
+                      None if workspace is None else workspace.data_ptr(), s)
 
 
 def _workspace(given, nbytes, what, device, stream):

@@ -471,7 +471,7 @@ int64_t gemm_epi_rmsnorm_workspace_bytes(int64_t m, int64_t d);
 int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void *dY, const void *S,
                          const void *gamma, const void *dS, void *dX, void *dgamma, void *workspace, void *stream);
 
-/* Bytes of scratch that gemm_epi_dact needs for dbias (0 for sizes or an axis it refuses). */
+/* Bytes of scratch that gemm_epi_dact needs for dbias (0: none, or sizes or an axis it refuses). */
 int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis);
 
 /* Backward of a forward epilogue D = act(z) (+ R), z = alpha*A.B + bias, from the gradient dD:
@@ -489,7 +489,7 @@ int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis);
  *           unrounded dZ in an order fixed by (m, n), rounded once.
  *   workspace  as for gemm_epi_rmsnorm_bwd: gemm_epi_dact_workspace_bytes(m, n, bias_axis) bytes,
  *           with dbias.
- * One launch, two with dbias.  Returns OK, ERR_ARG, ERR_ALIGN, ERR_NULL, ERR_NO_DEVICE or ERR_CUDA. */
+ * One launch, two with dbias and scratch.  Returns OK, ERR_ARG, ERR_ALIGN, ERR_NULL, ERR_NO_DEVICE or ERR_CUDA. */
 int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, const void *dD, const void *Z,
                   const uint32_t *aux, void *dZ, void *dbias, void *workspace, void *stream);
 

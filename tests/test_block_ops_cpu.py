@@ -87,10 +87,12 @@ def test_scratch_sizes(g):
     assert g.gemm_epi_rmsnorm_workspace_bytes(0, 64) == g.gemm_epi_rmsnorm_workspace_bytes(4, 16392) == 0
     for m, n in [(1, 8), (1023, 4104), (8192, 14336), (1 << 20, 64), (16, 1 << 20), ((1 << 31) - 1, 8)]:
         col, row = (g.gemm_epi_dact_workspace_bytes(m, n, a) for a in (1, 0))
-        assert row == (n + 255) // 256 * m * 4
+        assert row in (0, (n + 255) // 256 * m * 4)                  # 0: a block takes whole rows
+        assert (row == 0) == (m >= 1776 or n <= 6144)
         runs = col // (4 * n)
         assert col == runs * 4 * n and 1 <= runs <= min(65535, (m + 31) // 32)
     assert g.gemm_epi_dact_workspace_bytes(4, 64, 2) == g.gemm_epi_dact_workspace_bytes(4, 0, 1) == 0
+    assert g.gemm_epi_dact_workspace_bytes(4, 60, 1) == g.gemm_epi_rmsnorm_workspace_bytes(2000, 60) == 0
 
 
 def test_objects_refuse_unknown_names(g):
