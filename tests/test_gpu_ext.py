@@ -378,6 +378,48 @@ def test_prenorm_block_e4m3(m, act):
     ref.close(Y, y, ref.rounded(y, "bf16", ff * 2.0 ** -24 * mag), "Y")
 
 
+@pytest.mark.parametrize("m", [8, 260])
+def test_prenorm_block_captured_and_replayed(m):
+    """The serving loop: the stream updated in place by two blocks in one graph, replayed, against the same calls made one by
+    one; then the backward calls in a graph of their own."""
+    dm, ff, eps = 256, 528, 1e-5
+    x, r, gamma, w1, b1, w2, b2 = (t.to(torch.bfloat16).cuda() for t in mlp_inputs(m, dm, ff, "bf16"))
+    N, H = torch.empty(m, dm, dtype=torch.bfloat16, device="cuda"), torch.empty(m, ff, dtype=torch.bfloat16, device="cuda")
+    with g.MlpPlan(m, dm, ff, "bf16", "gelu_bias") as p:
+        def step(a, b):
+            p.run_prenorm(a, gamma, w1, b1, w2, b2, N, H, a, residual=b, S=b, eps=eps)     # b = a + b, a = mlp(norm(b)) + b
+            p.run_prenorm(a, gamma, w1, b1, w2, b2, N, H, a, eps=eps)
+
+        a, b = x.clone(), r.clone()
+        for _ in range(3):
+            step(a, b)
+        p.check()
+        c, d = x.clone(), r.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            step(c, d)
+        c.copy_(x)
+        d.copy_(r)
+        for _ in range(3):
+            graph.replay()
+        p.check()
+        assert torch.equal(a, c) and torch.equal(b, d) and bool(torch.isfinite(a.float()).all())
+        del graph
+    dZ, dX, db, dg, dbr = (torch.empty_like(t) for t in (x, x, gamma, gamma, x[:, 0].contiguous()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        g.ActBackward(m, dm, "bf16", "gelu", "col").run(x, dZ=dZ, z=r, dbias=db)
+        g.ActBackward(m, dm, "bf16", "bias", "row").run(dZ, dbias=dbr)
+        g.RmsNorm(m, dm, eps=eps).run_bwd(dZ, r, gamma, dX, dgamma=dg, dS=x)
+    for _ in range(2):
+        x.mul_(0.5)
+        graph.replay()
+        torch.cuda.synchronize()
+        ref.check_dact("gelu", "col", "bf16", x, r, dZ, db)
+        ref.check_dact("bias", "row", "bf16", dZ, r, None, dbr)
+        ref.check_norm_bwd("bf16", dZ, r, gamma, x, eps, dX, dg)
+
+
 def test_prenorm_block_refusals():
     m, dm, ff = 4, 64, 128
     x, r, gamma, w1, b1, w2, b2 = (t.to(torch.bfloat16).cuda() for t in mlp_inputs(m, dm, ff, "bf16"))
