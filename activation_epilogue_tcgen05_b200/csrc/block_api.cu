@@ -139,7 +139,7 @@ int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis) {
     if (bias_axis == GEMM_EPI_BIAS_ROW) return (n + DACT_COLS - 1) / DACT_COLS * m * (int64_t)sizeof(float);
     if (bias_axis != GEMM_EPI_BIAS_COL) return 0;
     const int64_t rows = std::min(dact_rows(m, n, true), dact_rows(m, n, false));      // whatever the epilogue
-    return (m + rows - 1) / rows * n * (int64_t)sizeof(float);
+    return rows >= m ? 0 : (m + rows - 1) / rows * n * (int64_t)sizeof(float);
 }
 
 int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, const void *dD, const void *Z,
@@ -160,8 +160,10 @@ int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, 
     const bool mask = act == DACT_RELU_MASK;
     if (!dD || (mask && !aux) || (!mask && act != DACT_NONE && !Z)) return GEMM_EPI_ERR_NULL;
     if (act == DACT_NONE ? !dbias : !dZ) return GEMM_EPI_ERR_NULL;
-    const bool by_rows = dbias && bias_axis == GEMM_EPI_BIAS_ROW && dact_by_rows(m, n);
-    if (dbias && !by_rows && !workspace) return GEMM_EPI_ERR_NULL;
+    // the sums end in a block each: rows whole in a block, or all rows in one run
+    const int64_t rows = dact_rows(m, n, dact_reads_z(act));
+    const bool at_once = dbias && (bias_axis == GEMM_EPI_BIAS_ROW ? dact_by_rows(m, n) : rows >= m);
+    if (dbias && !at_once && !workspace) return GEMM_EPI_ERR_NULL;
     if (act == DACT_NONE && dZ) return GEMM_EPI_ERR_ARG;          // dZ is dD itself
     if (!aligned(dD, 16) || (act != DACT_NONE && !mask && !aligned(Z, 16)) || (mask && !aligned(aux, 16)) ||
         !aligned(dZ, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
@@ -174,14 +176,14 @@ int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, 
     DactParams p{};
     p.m = m;
     p.n = (int)n;
-    p.rows = dact_rows(m, n, dact_reads_z(act));
+    p.rows = rows;
     p.dd = dD;
     p.z = Z;
     p.aux = reinterpret_cast<const uint8_t *>(aux);
     p.aux_pitch = gemm_epi_aux_pitch_bytes(n);
     p.dz = dZ;
-    p.partial = dbias && !by_rows ? static_cast<float *>(workspace) : nullptr;
-    p.dbias = by_rows ? dbias : nullptr;
+    p.partial = dbias && !at_once ? static_cast<float *>(workspace) : nullptr;
+    p.dbias = at_once ? dbias : nullptr;
     const bool pdl = pdl_enabled();
     rc = status(launch_dact(dt, act, axis, p, pdl, s));
     if (rc != GEMM_EPI_OK || !p.partial) return rc;

@@ -33,7 +33,7 @@ struct DactParams {
     const uint8_t *aux;      // the mask's bytes
     int64_t aux_pitch;       // bytes a row
     void *dz;
-    void *dbias;             // dact_rows_kernel: length m
+    void *dbias;             // written at once: by dact_rows_kernel (length m), or of a single run (length n)
     float *partial;          // COL: [run][n]; ROW: [strip][m]; or NULL
 };
 
@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
     }
     if constexpr (Z) ptx::cp_async_wait<0>();
     if constexpr (AXIS == AXIS_COL) {
-        if (p.partial == nullptr) return;
+        if (p.partial == nullptr && p.dbias == nullptr) return;
         // the warps' sums, in order: [warp][half of a lane's 8][lane]
         sums[(2 * warp) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         sums[(2 * warp + 1) * 32 + lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
@@ -202,7 +202,11 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
                 a.z += b.z;
                 a.w += b.w;
             }
-            reinterpret_cast<float4 *>(p.partial + (int64_t)blockIdx.y * p.n + col)[warp] = a;
+            if (p.dbias != nullptr)                       // one run: this is the whole sum
+                *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.dbias) + col + 4 * warp) =
+                    make_uint2(OutT<DT>::pack(a.x, a.y), OutT<DT>::pack(a.z, a.w));
+            else
+                reinterpret_cast<float4 *>(p.partial + (int64_t)blockIdx.y * p.n + col)[warp] = a;
         }
     }
 }

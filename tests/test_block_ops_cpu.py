@@ -61,7 +61,7 @@ def test_norm_bwd_refusals(g, kw, code):
 @pytest.mark.parametrize("kw,code", [
     (dict(m=0), "ERR_ARG"), (dict(n=0), "ERR_ARG"), (dict(dtype=3), "ERR_ARG"), (dict(epi=10), "ERR_ARG"),
     (dict(epi=-1), "ERR_ARG"), (dict(axis=2), "ERR_ARG"), (dict(n=60), "ERR_ALIGN"), (dict(dD=None), "ERR_NULL"),
-    (dict(Z=None), "ERR_NULL"), (dict(epi=3), "ERR_NULL"), (dict(dZ=None), "ERR_NULL"), (dict(dbias=P), "ERR_NULL"),
+    (dict(Z=None), "ERR_NULL"), (dict(epi=3), "ERR_NULL"), (dict(dZ=None), "ERR_NULL"), (dict(m=2000, dbias=P), "ERR_NULL"),
     (dict(epi=1, dZ=None), "ERR_NULL"), (dict(epi=1, dbias=P, ws=P), "ERR_ARG"), (dict(Z=P + 8), "ERR_ALIGN"),
     (dict(epi=7, aux=P + 4), "ERR_ALIGN"), (dict(dbias=P, ws=P + 8), "ERR_ALIGN"),
 ])
@@ -90,7 +90,8 @@ def test_scratch_sizes(g):
         assert row in (0, (n + 255) // 256 * m * 4)                  # 0: a block takes whole rows
         assert (row == 0) == (m >= 1776 or n <= 6144)
         runs = col // (4 * n)
-        assert col == runs * 4 * n and 1 <= runs <= min(65535, (m + 31) // 32)
+        assert col == runs * 4 * n and runs != 1 and runs <= min(65535, (m + 31) // 32)      # 0: one run
+        assert m > 64 or runs == 0
     assert g.gemm_epi_dact_workspace_bytes(4, 64, 2) == g.gemm_epi_dact_workspace_bytes(4, 0, 1) == 0
     assert g.gemm_epi_dact_workspace_bytes(4, 60, 1) == g.gemm_epi_rmsnorm_workspace_bytes(2000, 60) == 0
 

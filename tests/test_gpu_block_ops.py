@@ -308,7 +308,7 @@ def test_dact(m, n, dtype, epilogue, axis):
 
 @pytest.mark.parametrize("axis", ["row", "col"])
 @pytest.mark.parametrize("m,n", [(5000, 256), (16, 16384), (1, 20000), (2049, 2056), (70000, 8),
-                                 (1775, 6152), (1776, 6152), (7, 40000), (2, 2048), (5, 4096), (301, 6144), (2001, 16392)])
+                                 (1775, 6152), (1776, 6152), (7, 40000), (2, 2048), (5, 4096), (301, 6144), (2001, 16392), (64, 4104), (65, 4104), (33, 70000)])
 def test_dact_long_and_wide(m, n, axis):
     dd, z = randn(m, n, seed=3), randn(m, n, seed=4)
     dZ, db = run_dact(dd, z, "bf16", "gelu_bias", axis)
