@@ -1010,7 +1010,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             }
             // The residual comes in 32 x 32 boxes like D's, into a buffer of the warp's own: a chunk is taken
             // from there into registers, and the next one asked for, before its arithmetic.  The first is
-            // asked for here, and the others are asked of L2, before the accumulator is waited for.
+            // asked for here, and the others are asked of L2, before the accumulator is waited for.  Extended
+            // against plain epilogue, us: 4096^3 bf16 99.6 and 94.3, 8192 x 4096 x 14336 e4m3 342 and 329,
+            // 1024 x 4096 x 1024 bf16 14.9 and 13.0 (each lane loading its row's 64 bytes itself: 17.4); at k =
+            // 1024 and many tiles the residual's bytes share L2 with the operands' (bf16 65 and 56).
             const bool res = C::RES && p.residual != nullptr && !partial_out;
             if constexpr (C::RES) if (res) {
                 if (lane == 0) {
