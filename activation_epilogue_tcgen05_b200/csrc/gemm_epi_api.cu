@@ -573,6 +573,8 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
     int katoms = P->katoms;
     if (ext && find_ext(P, &tc_ext, &sk_ext, &katoms) != GEMM_EPI_OK) return GEMM_EPI_ERR_UNSUPPORTED;
     if (!P->has_bias) bias = nullptr;
+    // scales by row stand in for A's, which is then not read
+    const float *scale_a = ext && ext->scale_rows ? nullptr : P->scale_a;
     const int bk = 128 / esize(P->dtype);
     const int num_kb = (int)((P->k + bk - 1) / bk);
     const int64_t pitch_words = ((P->n + 127) / 128) * 4;
@@ -591,7 +593,7 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.D = D;
         L.p.aux = aux;
         L.p.aux_pitch_words = pitch_words;
-        L.p.scale_a = P->scale_a;
+        L.p.scale_a = scale_a;
         L.p.scale_b = P->scale_b;
         L.p.status = P->status;
         L.p.dq = P->qout ? static_cast<uint8_t *>(D) : nullptr;
@@ -616,7 +618,7 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.D = D;
         L.p.aux = aux;
         L.p.aux_pitch_words = pitch_words;
-        L.p.scale_a = P->scale_a;
+        L.p.scale_a = scale_a;
         L.p.scale_b = P->scale_b;
         L.p.status = P->status;
         L.p.dq = P->qout ? static_cast<uint8_t *>(D) : nullptr;
@@ -654,7 +656,7 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         L.p.bias = bias;
         L.p.aux = aux;
         L.p.aux_pitch_words = pitch_words;
-        L.p.scale_a = P->scale_a;
+        L.p.scale_a = scale_a;
         L.p.scale_b = P->scale_b;
         L.p.status = P->status;
         L.p.inject_stall = P->opts.inject_stall;
