@@ -1123,6 +1123,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                         }
                     }
                     uint32_t packed[16];
+                    float top[2] = {0.0f, 0.0f};               // QOUT: max |y| of each 16 columns
                     uint32_t bits = 0;
                     const uint32_t mbits = cc == 0 ? mk.x : cc == 1 ? mk.y : cc == 2 ? mk.z : mk.w;
                     (void)mbits;
@@ -1173,7 +1174,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                             y1 = activate<C::EPI>(x1);
                         }
                         if constexpr (C::QOUT) {
-                            amax_l = fmaxf(amax_l, fmaxf(fabsf(y0), fabsf(y1)));
+                            top[j / 16] = fmaxf(top[j / 16], fmaxf(fabsf(y0), fabsf(y1)));
                             // two e4m3 codes, round to nearest even, saturating at +-448; y0 low byte
                             packed[j / 2] = __nv_cvt_float2_to_fp8x2(make_float2(y0 * inv_out, y1 * inv_out),
                                                                      __NV_SATFINITE, __NV_E4M3);
@@ -1189,16 +1190,22 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     }
                     if constexpr (C::QOUT) {
                         // this lane's 32 codes are 32 contiguous bytes of its row (n is a multiple of 16)
+                        // and only what D holds counts for the maximum: the tile's rows and columns past
+                        // its edge hold act(bias)
                         if (row_ok) {
                             uint8_t *dst = p.dq + (int64_t)row * p.n + col0;
-                            if (col0 + 16 <= p.n)
+                            if (col0 + 16 <= p.n) {
+                                amax_l = fmaxf(amax_l, top[0]);
                                 *reinterpret_cast<uint4 *>(dst) =
                                     make_uint4(packed[0] | (packed[1] << 16), packed[2] | (packed[3] << 16),
                                                packed[4] | (packed[5] << 16), packed[6] | (packed[7] << 16));
-                            if (col0 + 32 <= p.n)
+                            }
+                            if (col0 + 32 <= p.n) {
+                                amax_l = fmaxf(amax_l, top[1]);
                                 *reinterpret_cast<uint4 *>(dst + 16) =
                                     make_uint4(packed[8] | (packed[9] << 16), packed[10] | (packed[11] << 16),
                                                packed[12] | (packed[13] << 16), packed[14] | (packed[15] << 16));
+                            }
                         }
                     } else {
                         // stage 32 rows x 32 outputs in the 64-byte swizzled layout the TMA store reads:

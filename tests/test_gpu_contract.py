@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import block_ref as ref
 
 from activation_epilogue_tcgen05_b200 import gemm_epi as g
 
@@ -36,6 +37,57 @@ def cancelled(m, n, axis):
     y = 10.0 + a @ b
     bias = torch.full((m if axis == "row" else n,), 10.0, dtype=torch.bfloat16, device="cuda")
     return a.to(E4M3).cuda(), b.to(E4M3).cuda(), bias, y
+
+
+@pytest.mark.parametrize("rows", [False, True])
+@pytest.mark.parametrize("epilogue", ["bias", "relu_bias", "gelu_bias"])
+@pytest.mark.parametrize("axis", ["col", "row"])
+@pytest.mark.parametrize("m,n,kw", [(129, 272, dict(kernel="tc1", block_n=128)), (129, 272, dict(kernel="tc1", block_n=256)),
+                                    (300, 272, dict(kernel="tc2", block_n=256)), (1, 16, dict(kernel="tc1", block_n=128)),
+                                    (300, 400, dict(kernel="tc2", block_n=256, max_ctas=2)),
+                                    (128, 272, dict(kernel="tc1", block_n=256)), (256, 272, dict(kernel="tc2", block_n=256)), (17, 272, dict(kernel="splitk")),
+                                    (300, 272, {}), (5, 144, {})])
+def test_the_reported_maximum_is_over_the_output(m, n, kw, axis, epilogue, rows):
+    a, b, bias, y = cancelled(m, n, axis)
+    want = ref.act(epilogue, y.double()).abs().max()
+    D, amax = torch.zeros(m, n, dtype=torch.uint8, device="cuda").view(E4M3), f32(9e9)
+    with g.Plan(m, n, 32, "e4m3", epilogue, axis, out_e4m3=True, **kw) as p:
+        p.set_scales(f32(1), f32(2 if rows else 1))
+        p.set_out_scale(f32(0.0625), amax)
+        if rows:
+            p.run_ext(a, b, bias, D, scale_rows=torch.full((m,), 0.5, device="cuda"))
+        else:
+            p.run(a, b, bias, D)
+        p.check()
+    # GELU alone computes: its erfc is within 1.5e-7 (of a value that |x| / 2 scales) and fp32
+    assert abs(float(amax) - float(want)) <= (2.0 ** -20 * 2.125 if epilogue == "gelu_bias" else 0.0)
+
+
+@pytest.mark.parametrize("prenorm", [False, True])
+@pytest.mark.parametrize("act", ["relu_bias", "gelu_bias"])
+@pytest.mark.parametrize("m", [5, 129, 300])
+def test_the_blocks_reported_maximum_is_over_h(m, act, prenorm):
+    dm, ff = 256, 528
+    w1 = torch.zeros(dm, ff)
+    w1[0] = -9.0
+    q1, q2 = w1.to(E4M3).cuda(), torch.zeros(ff, dm).to(E4M3).cuda()
+    b1, b2 = torch.full((ff,), 10.0, dtype=torch.bfloat16, device="cuda"), torch.zeros(dm, dtype=torch.bfloat16, device="cuda")
+    amax, rows = f32(9e9), torch.zeros(m, device="cuda")
+    N = torch.zeros(m, dm).cuda()
+    N[:, 0] = 1
+    X, N = N.bfloat16(), N.to(E4M3)
+    H, Y = torch.zeros(m, ff, dtype=torch.uint8, device="cuda").view(E4M3), torch.zeros(m, dm, dtype=torch.bfloat16, device="cuda")
+    gamma = torch.full((dm,), 0.0625, dtype=torch.bfloat16, device="cuda")        # the norm of a row is 16 in its one column
+    with g.MlpPlan(m, dm, ff, "e4m3", act) as p:
+        p.set_scales(f32(1), f32(1), f32(0.0625), amax, f32(1))
+        if prenorm:
+            p.run_prenorm(X, gamma, q1, b1, q2, b2, N, H, Y, scale_rows=rows, eps=1e-12)
+        else:
+            p.run(N, q1, b1, q2, b2, H, Y)
+        p.check()
+    # h = act(10 - 9 * 1); before a GELU or ReLU of slope up to 1.13 the norm's 1 is off by at most a few 2^-24
+    want = float(ref.act(act, torch.ones((), dtype=torch.float64)))
+    assert abs(float(amax) - want) <= 1.13 * 9 * 2.0 ** -20
 
 
 # ------------------------------------------------------------------ scales
