@@ -4,7 +4,7 @@
 // (RELU_AUX), or from z in the 16-bit type:
 //     ReLU   z > 0
 //     GELU   Phi(z) + z phi(z), Phi and phi the normal distribution and density
-//     tanh   1 - tanh(z)^2
+//     tanh   1 / cosh(z)^2
 // The sums are taken in fp32 on the unrounded dZ, in an order fixed by the shapes.
 //
 // Bound by HBM (dD and z read once, dZ written once).  A warp covers 256 columns of a row, a
@@ -60,15 +60,20 @@ __device__ __forceinline__ f32x2 gelu_slope(float x0, float x1) {
     return add2(fma2(mul2(x, both(0.39894228040143268f)), e, phi), both(0.5f));
 }
 
+// tanh'(x) = 1 / cosh(x)^2 = 4 e / (1 + e)^2, e = exp(-2 |x|): nothing cancels, so the slope of a saturated
+// unit keeps its digits (1 - tanh(x)^2 in fp32 has none left beyond |x| = 8).
+__device__ __forceinline__ f32x2 tanh_slope(float x0, float x1) {
+    const float2 q = split(mul2(pair(fabsf(x0), fabsf(x1)), both(-2.0f * 1.4426950408889634f)));
+    const f32x2 e = pair(ex2_approx(q.x), ex2_approx(q.y));
+    const float2 den = split(add2(e, both(1.0f)));
+    const f32x2 r = pair(rcp_approx(den.x), rcp_approx(den.y));
+    return mul2(mul2(e, both(4.0f)), mul2(r, r));
+}
+
 // act'(z) of two neighbouring elements.
 template <int ACT>
 __device__ __forceinline__ f32x2 slope(float z0, float z1) {
-    if constexpr (ACT == DACT_GELU) {
-        return gelu_slope(z0, z1);
-    } else {
-        const float y0 = tanhf(z0), y1 = tanhf(z1);
-        return pair(fmaf(-y0, y0, 1.0f), fmaf(-y1, y1, 1.0f));
-    }
+    return ACT == DACT_GELU ? gelu_slope(z0, z1) : tanh_slope(z0, z1);
 }
 
 // d *= act'(z) for a lane's eight elements (bits: their mask).

@@ -109,3 +109,33 @@ def test_row_scales_take_the_place_of_the_scale_of_a(m, kw, out_e4m3):
             got.append((D.view(torch.uint8), amax))
     for D, amax in got[1:]:
         assert torch.equal(D, got[0][0]) and torch.equal(amax, got[0][1])
+
+
+# ------------------------------------------------------------------ slopes far from zero
+# e^-(z^2 / 2) is computed as 2^-q, q = (z c)^2: c and z c are rounded and squared, q is rounded, 5 half-steps of q in all, so
+# off by ln 2 q 5 2^-24 <= 1.25 z^2 2^-23 of itself, and ex2.approx by 2^-22; the fraction beside it is fitted and computed to 2^-21 of one half, which is absolute where its two
+# terms cancel (near z = -0.75).  tanh: e^-2|z| = 2^-q with q = 2 |z| log2 e of two roundings, ln 2 q 2^-23 <= |z| 2^-21.
+def slope_allowance(name, z, slope):
+    if name == "gelu":
+        return slope.abs() * (1.25 * z * z * 2.0 ** -23 + 2.0 ** -20) + 2.0 ** -21 * torch.exp(-z * z / 2)
+    return slope.abs() * (z.abs() * 2.0 ** -21 + 2.0 ** -20)
+
+
+@pytest.mark.parametrize("axis", ["row", "col"])
+@pytest.mark.parametrize("epilogue,far", [("tanh_bias", 40.0)])
+def test_slopes_have_their_digits_far_out(epilogue, far, axis):
+    """bf16 holds the slopes of saturated units: GELU's to z = -12.5, tanh's to |z| = 40, with every digit of the type."""
+    z = torch.linspace(-far, far, 4096).bfloat16().view(16, 256)
+    dd = (2.0 ** torch.arange(-2, 2, 1 / 64)).bfloat16().view(1, 256).expand(16, 256).contiguous()
+    dZ, db = torch.empty_like(z, device="cuda"), torch.empty(16 if axis == "row" else 256, dtype=torch.bfloat16, device="cuda")
+    g.ActBackward(16, 256, "bf16", epilogue, axis).run(dd.cuda(), dZ=dZ, z=z.cuda(), dbias=db)
+    name, zd, ddd = epilogue.split("_")[0], z.double(), dd.double()
+    if name == "gelu":       # Phi(z) = erfc(-z / sqrt 2) / 2, without cancellation on the left
+        slope = torch.special.erfc(-zd / math.sqrt(2)) / 2 + zd * torch.exp(-zd * zd / 2) / math.sqrt(2 * math.pi)
+    else:
+        slope = 1 / torch.cosh(zd) ** 2
+    off = ddd * slope_allowance(name, zd, slope)
+    want = ddd * slope
+    ref.close(dZ, want, ref.rounded(want, "bf16", off + 2.0 ** -24 * want.abs()), "dZ")
+    dim = 1 if axis == "row" else 0
+    ref.close(db, want.sum(dim), ref.rounded(want.sum(dim), "bf16", off.sum(dim) + ref.F32 * want.abs().sum(dim)), "dbias")
