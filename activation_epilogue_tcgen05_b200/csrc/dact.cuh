@@ -38,26 +38,34 @@ struct DactParams {
     float *partial;          // COL: [run][n]; ROW: [strip][m]; or NULL
 };
 
-// GELU's slope takes 27 instructions an element one by one and 14 in pairs, below what HBM allows
-// time for.
-// GELU'(x) = Phi(x) + x phi(x), with 1 - Phi(|x|) from the same Abramowitz & Stegun 7.1.26 form as
-// the forward epilogue's GELU (gelu_erf): one exponential serves both terms.
-//     Phi(x) = 1/2 + sign(x) (1/2 - tail),  tail = 1 - Phi(|x|)
+// GELU'(x) = Phi(x) + x phi(x), Phi and phi the normal distribution and density.  With u = |x| and
+// phi(u) = e / sqrt(2 pi), e = exp(-u^2 / 2),
+//     GELU'(-u) = e w(u),   GELU'(u) = 1 - e w(u),   w(u) = exp(u^2 / 2) (1 - Phi(u)) - u / sqrt(2 pi),
+// so that the left side, which falls to 0 as e does, comes from a product and keeps its digits.  (Phi taken as
+// 1/2 - (1/2 - tail) loses a tail below 2^-25, and a tail within 1e-7 absolutely, which is enough for the forward,
+// is 7 % off at -5.7 and gives 0 from -6.)  The term beside u / sqrt(2 pi) is a polynomial of degree 5 in
+// t = 1 / (c u + 2.498) without a constant, fitted by a linear program to its 64-bit values over 0 <= u <= 16: e w is off
+// by at most the larger of 1.8e-7 e and 3.6e-5 of itself (7 % of half an f16 step; two degrees more for 1.4e-7 throughout
+// left no registers: 8192 x 14336 134 us for 112).  u is cut off at 16, where e is 0 in fp32, so that an infinite x has its
+// side's slope.  All but the cut, the signs and the hardware's reciprocal and exponential is done for two elements at once.
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 __device__ __forceinline__ f32x2 gelu_slope(float x0, float x1) {
-    const f32x2 x = pair(x0, x1);
-    const float2 den = split(fma2(pair(fabsf(x0), fabsf(x1)), both(0.3275911f * 0.70710678118654752f), both(1.0f)));
+    constexpr float c = 0.84932180028801907f;                                 // sqrt(log2(e) / 2): e = 2^-(c u)^2
+    const f32x2 v = mul2(pair(min_nan(fabsf(x0), 16.0f), min_nan(fabsf(x1), 16.0f)), both(c));
+    const float2 den = split(add2(v, both(2.498f))), q = split(mul2(v, v));
     const f32x2 t = pair(rcp_approx(den.x), rcp_approx(den.y));
-    f32x2 h = fma2(t, both(0.5307027145f), both(-0.7265760135f));
-    h = fma2(t, h, both(0.7107068705f));
-    h = fma2(t, h, both(-0.142248368f));
-    h = fma2(t, h, both(0.127414796f));
-    h = mul2(t, h);
-    const f32x2 s = mul2(x, both(0.84932180028801907f));        // (c x)^2 = x^2 / 2 * log2(e)
-    const float2 q = split(mul2(s, s));
-    const f32x2 e = pair(ex2_approx(-q.x), ex2_approx(-q.y));     // exp(-x^2 / 2)
-    const float2 half = split(fma2(mul2(h, both(-1.0f)), e, both(0.5f)));
-    const f32x2 phi = pair(copysignf(half.x, x0), copysignf(half.y, x1));
-    return add2(fma2(mul2(x, both(0.39894228040143268f)), e, phi), both(0.5f));
+    f32x2 h = fma2(t, both(20.0101986f), both(-24.893486f));
+    h = fma2(t, h, both(0.832031548f));
+    h = fma2(t, h, both(-2.2361939f));
+    h = fma2(t, h, both(-0.653034389f));
+    const f32x2 w = fma2(v, both(2.0f * 0.39894228040143268f / c), mul2(t, h));        // -2 w(u)
+    const f32x2 left = mul2(pair(ex2_approx(-q.x), ex2_approx(-q.y)), w);
+    const f32x2 side = pair(copysignf(0.5f, x0), copysignf(0.5f, x1));
+    return fma2(left, side, add2(side, both(0.5f)));
 }
 
 // tanh'(x) = 1 / cosh(x)^2 = 4 e / (1 + e)^2, e = exp(-2 |x|): nothing cancels, so the slope of a saturated
@@ -102,13 +110,16 @@ __device__ __forceinline__ void through_act(float (&d)[8], const float (&z)[8], 
 // through a ring 40.6; 1023 x 4104 from the mask 5.4 us against 7.0).
 constexpr int DACT_U = 4;                             // rows of a warp in a batch
 constexpr bool dact_reads_z(int act) { return act != DACT_NONE && act != DACT_RELU_MASK; }
+// Where a slope is computed, two rows of a batch are worked out at a time: with all four interleaved the constants no longer
+// fit the 80 registers that three blocks an SM leave (8192 x 14336 GELU 120 us, two at a time 112).
+constexpr bool dact_computes(int act) { return act == DACT_GELU || act == DACT_TANH; }
 constexpr int DACT_RING = 2;
 constexpr int DACT_SMEM = DACT_RING * 2 * DACT_U * 32 * DACT_WARPS * 16;
 
 template <int DT, int ACT, int AXIS>
 __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_kernel(const DactParams p) {
     constexpr int T = 32 * DACT_WARPS, U = DACT_U;
-    constexpr bool Z = dact_reads_z(ACT);
+    constexpr bool Z = dact_reads_z(ACT), SLOPE = dact_computes(ACT);
     extern __shared__ uint4 ring[];                   // Z: [DACT_RING][U][dd, z][T]
     __shared__ float4 sums[AXIS == AXIS_COL ? 64 * DACT_WARPS : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -156,7 +167,7 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
                 }
             }
         }
-#pragma unroll
+#pragma unroll (SLOPE ? 2 : U)
         for (int u = 0; u < U; ++u) {
             const int64_t i = row + u * DACT_WARPS;
             const bool ok = i < r1 && col_ok;
@@ -224,7 +235,7 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
 template <int DT, int ACT>
 __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_rows_kernel(const DactParams p) {
     constexpr int T = 32 * DACT_WARPS, U = DACT_U, PASS = DACT_WARPS * DACT_COLS;
-    constexpr bool Z = dact_reads_z(ACT);
+    constexpr bool Z = dact_reads_z(ACT), SLOPE = dact_computes(ACT);
     extern __shared__ uint4 ring[];                   // Z: [DACT_RING][U][dd, z][T]
     __shared__ float sums[DACT_WARPS][U];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -273,21 +284,31 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
                 }
             }
         }
+        // (two rows at a time; their sums go round, so that each is in its place again after the batch)
+#pragma unroll (SLOPE ? 1 : U / 2)
+        for (int u0 = 0; u0 < U; u0 += 2) {
+            float sum[2];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint4 *src = ring + (stage * U + u) * 2 * T + threadIdx.x;
-            float d[8], z[8];
-            if constexpr (Z) {
-                unpack8<DT>(u < rows ? src[0] : make_uint4(0u, 0u, 0u, 0u), d);
-                unpack8<DT>(u < rows ? src[T] : make_uint4(0u, 0u, 0u, 0u), z);
-            } else {
-                unpack8<DT>(dv[u], d);
+            for (int k = 0; k < 2; ++k) {
+                const int u = u0 + k;
+                const uint4 *src = ring + (stage * U + u) * 2 * T + threadIdx.x;
+                float d[8], z[8];
+                if constexpr (Z) {
+                    unpack8<DT>(u < rows ? src[0] : make_uint4(0u, 0u, 0u, 0u), d);
+                    unpack8<DT>(u < rows ? src[T] : make_uint4(0u, 0u, 0u, 0u), z);
+                } else {
+                    unpack8<DT>(dv[u], d);
+                }
+                through_act<ACT>(d, z, bits[u]);
+                if constexpr (ACT != DACT_NONE) {
+                    if (u < rows) *reinterpret_cast<uint4 *>(dz + (int64_t)u * p.n + col) = pack8<DT>(d);
+                }
+                sum[k] = acc[k] + (((d[0] + d[1]) + (d[2] + d[3])) + ((d[4] + d[5]) + (d[6] + d[7])));
             }
-            through_act<ACT>(d, z, bits[u]);
-            if constexpr (ACT != DACT_NONE) {
-                if (u < rows) *reinterpret_cast<uint4 *>(dz + (int64_t)u * p.n + col) = pack8<DT>(d);
-            }
-            acc[u] += ((d[0] + d[1]) + (d[2] + d[3])) + ((d[4] + d[5]) + (d[6] + d[7]));
+#pragma unroll
+            for (int k = 0; k < U - 2; ++k) acc[k] = acc[k + 2];
+            acc[U - 2] = sum[0];
+            acc[U - 1] = sum[1];
         }
         if constexpr (Z) {
             fetch(col + DACT_RING * PASS, stage);

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 import block_ref as ref
+from block_ref import T16
 
 from activation_epilogue_tcgen05_b200 import gemm_epi as g
 
@@ -25,6 +26,11 @@ def _cuda():
 
 def f32(*v):
     return torch.tensor(v, dtype=torch.float32, device="cuda")
+
+
+def randn(*shape, seed=0, dtype="bf16", scale=1.0):
+    gen = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=gen) * scale).to(T16[dtype]).cuda()
 
 
 # ------------------------------------------------------------------ the maximum of an e4m3 output
@@ -113,16 +119,17 @@ def test_row_scales_take_the_place_of_the_scale_of_a(m, kw, out_e4m3):
 
 # ------------------------------------------------------------------ slopes far from zero
 # e^-(z^2 / 2) is computed as 2^-q, q = (z c)^2: c and z c are rounded and squared, q is rounded, 5 half-steps of q in all, so
-# off by ln 2 q 5 2^-24 <= 1.25 z^2 2^-23 of itself, and ex2.approx by 2^-22; the fraction beside it is fitted and computed to 2^-21 of one half, which is absolute where its two
-# terms cancel (near z = -0.75).  tanh: e^-2|z| = 2^-q with q = 2 |z| log2 e of two roundings, ln 2 q 2^-23 <= |z| 2^-21.
+# off by ln 2 q 5 2^-24 <= 1.25 z^2 2^-23 of itself, and ex2.approx by 2^-22; the fraction beside it is fitted to the larger of
+# 1.8e-7 and 3.6e-5 of itself and computed to 2^-21 of one half, which is absolute where its two terms cancel (near z = -0.75).
+# tanh: e^-2|z| = 2^-q with q = 2 |z| log2 e of two roundings, ln 2 q 2^-23 <= |z| 2^-21.
 def slope_allowance(name, z, slope):
     if name == "gelu":
-        return slope.abs() * (1.25 * z * z * 2.0 ** -23 + 2.0 ** -20) + 2.0 ** -21 * torch.exp(-z * z / 2)
+        return slope.abs() * (1.25 * z * z * 2.0 ** -23 + 2.0 ** -20 + 3.6e-5) + (2.0 ** -21 + 1.8e-7) * torch.exp(-z * z / 2)
     return slope.abs() * (z.abs() * 2.0 ** -21 + 2.0 ** -20)
 
 
 @pytest.mark.parametrize("axis", ["row", "col"])
-@pytest.mark.parametrize("epilogue,far", [("tanh_bias", 40.0)])
+@pytest.mark.parametrize("epilogue,far", [("gelu", 12.5), ("tanh_bias", 40.0)])
 def test_slopes_have_their_digits_far_out(epilogue, far, axis):
     """bf16 holds the slopes of saturated units: GELU's to z = -12.5, tanh's to |z| = 40, with every digit of the type."""
     z = torch.linspace(-far, far, 4096).bfloat16().view(16, 256)
@@ -139,3 +146,16 @@ def test_slopes_have_their_digits_far_out(epilogue, far, axis):
     ref.close(dZ, want, ref.rounded(want, "bf16", off + 2.0 ** -24 * want.abs()), "dZ")
     dim = 1 if axis == "row" else 0
     ref.close(db, want.sum(dim), ref.rounded(want.sum(dim), "bf16", off.sum(dim) + ref.F32 * want.abs().sum(dim)), "dbias")
+
+
+@pytest.mark.parametrize("epilogue,left,right", [("gelu", 0.0, 1.0), ("tanh", 0.0, 0.0), ("relu", 0.0, 1.0)])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_slopes_at_infinity(dtype, epilogue, left, right):
+    """A pre-activation that overflowed its 16 bits has the slope of the side that it is on."""
+    z = randn(8, 64, seed=1, dtype=dtype)
+    z[:, 5], z[:, 6], z[:, 7], z[:, 8] = math.inf, -math.inf, 65504.0, -65504.0
+    dd = torch.full_like(z, 3.0)
+    dZ, db = torch.empty_like(z), torch.empty(64, dtype=z.dtype, device="cuda")
+    g.ActBackward(8, 64, dtype, epilogue, "col").run(dd, dZ=dZ, z=z, dbias=db)
+    assert bool((dZ[:, [5, 7]] == 3 * right).all()) and bool((dZ[:, [6, 8]] == 3 * left).all())
+    assert db[5:9].tolist() == [24 * right, 24 * left] * 2 and bool(torch.isfinite(db.float()).all())
