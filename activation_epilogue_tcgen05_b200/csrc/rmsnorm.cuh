@@ -277,7 +277,7 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
         }
         row_reduce<TPR, T, false>(ss, c, red[buf][grp], grp);
         const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-        const float k = rho * rho * (c * p.inv_d);
+        const float k = rho * (rho * (c * p.inv_d));      // (rho^2 is beyond fp32 beside the smallest eps)
         uint16_t *out = static_cast<uint16_t *>(p.dx) + row * p.d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {

@@ -117,6 +117,24 @@ def test_row_scales_take_the_place_of_the_scale_of_a(m, kw, out_e4m3):
         assert torch.equal(D, got[0][0]) and torch.equal(amax, got[0][1])
 
 
+# ------------------------------------------------------------------ the norm
+@pytest.mark.parametrize("eps", [1e-30, 1e-38, 1e-40, 1e-44])
+@pytest.mark.parametrize("m,d", [(3, 64), (3, 1024), (200, 4096), (2, 8192)])
+def test_norm_and_its_backward_with_the_smallest_eps(m, d, eps):
+    """eps may be any positive number: a row of zeros beside it has rho = eps^-1/2, which fp32 holds although its square is beyond it."""
+    x, gamma = randn(m, d, seed=1), randn(d, seed=2)
+    x[1] = 0
+    Y, dX, dg = torch.empty_like(x), torch.empty_like(x), torch.empty_like(gamma)
+    op = g.RmsNorm(m, d, eps=eps)
+    op.run(x, gamma, Y)
+    e = float(torch.tensor(eps, dtype=torch.float32))
+    ref.check_norm("same", "bf16", x, None, gamma, e, Y)
+    dy, ds = randn(m, d, seed=3), randn(m, d, seed=4)
+    dy[1] *= 1e-12
+    op.run_bwd(dy, x, gamma, dX, dgamma=dg, dS=ds)
+    ref.check_norm_bwd("bf16", dy, x, gamma, ds, e, dX, dg)
+
+
 # ------------------------------------------------------------------ slopes far from zero
 # e^-(z^2 / 2) is computed as 2^-q, q = (z c)^2: c and z c are rounded and squared, q is rounded, 5 half-steps of q in all, so
 # off by ln 2 q 5 2^-24 <= 1.25 z^2 2^-23 of itself, and ex2.approx by 2^-22; the fraction beside it is fitted to the larger of
