@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
         if (C::EXT && p.scale_rows != nullptr) alpha = p.scale_b != nullptr ? __ldg(p.scale_b) : 1.0f;
         else if (p.scale_a != nullptr) alpha = __ldg(p.scale_a) * __ldg(p.scale_b);
-        if constexpr (C::QOUT) inv_out = 1.0f / __ldg(p.out_scale);
+        if constexpr (C::QOUT) inv_out = per_scale(1.0f, p.out_scale);
         if constexpr (C::EXT) {
 #pragma unroll
             for (int b = 0; b < 4; ++b) {

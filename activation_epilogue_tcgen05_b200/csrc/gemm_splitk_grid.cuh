@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         if (p.scale_a != nullptr) alpha = __ldg(p.scale_a) * __ldg(p.scale_b);
         const bool has_bias = p.bias != nullptr;
         float inv_out = 1.0f, amax_l = 0.0f;
-        if constexpr (C::QOUT) inv_out = 1.0f / __ldg(p.out_scale);
+        if constexpr (C::QOUT) inv_out = per_scale(1.0f, p.out_scale);
         T *D = reinterpret_cast<T *>(p.D);
         uint32_t acc = 0, acc_phase = 0;
         bool ok = true;

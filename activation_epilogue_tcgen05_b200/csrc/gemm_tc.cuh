@@ -304,6 +304,10 @@ struct OutT<DT_BF16> {
 template <>
 struct OutT<DT_E4M3> : OutT<DT_BF16> {};   // e4m3 operands -> bf16 bias and output
 
+// a / *scale, a > 0, as the factor of an e4m3 output; the largest fp32 number where the quotient is beyond it: what
+// is not 0 saturates all the same, and 0 stays 0.
+__device__ __forceinline__ float per_scale(float a, const float *scale) { return fminf(a / __ldg(scale), 3.402823466e38f); }
+
 // 16-bit bias values -> fp32 (8 packed values from one 16-byte load).
 template <int DT>
 __device__ __forceinline__ void unpack8(const uint4 &u, float (&f)[8]) {
@@ -924,7 +928,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         const bool bgrad = C::BWD && p.dbias_ws != nullptr;   // backward: bias-gradient partials
         float inv_out = 1.0f, amax_l = 0.0f;                  // FP8 output: 1 / scale, running max |y|
         const uint64_t pol_d = p.l2_mode >= 1 ? ptx::policy_evict_first() : ptx::policy_evict_normal();
-        if constexpr (C::QOUT) inv_out = 1.0f / __ldg(p.out_scale);
+        if constexpr (C::QOUT) inv_out = per_scale(1.0f, p.out_scale);
         uint32_t acc = 0, acc_phase = 0, tr_i = 0;
         bool ok = true;
         // RES: chunks of the residual that this warp has taken and has asked for, its barrier, one load

@@ -33,7 +33,7 @@ __global__ void __launch_bounds__(256) quantize_bf16_e4m3_kernel(const void *__r
                                                                  const float *__restrict__ scale, uint8_t *q) {
     const uint4 *v = reinterpret_cast<const uint4 *>(x);
     uint2 *out = reinterpret_cast<uint2 *>(q);
-    const float inv = 1.0f / __ldg(scale);
+    const float inv = per_scale(1.0f, scale);
     for (int64_t i = blockIdx.x * (int64_t)blockDim.x + threadIdx.x; i < count / 8;
          i += (int64_t)gridDim.x * blockDim.x) {
         float f[8];

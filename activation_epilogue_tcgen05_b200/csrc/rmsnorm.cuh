@@ -154,7 +154,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
     const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
     float mul = rho;
     if constexpr (OUT == NORM_E4M3) {
-        mul = rho / __ldg(p.scale);
+        mul = per_scale(rho, p.scale);
         if (p.amax != nullptr && (TPR <= 32 || t < 32)) {
             // one word a warp (rows past the last hold zeros); most are below the maximum so far and
             // only read it

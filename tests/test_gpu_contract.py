@@ -117,6 +117,32 @@ def test_row_scales_take_the_place_of_the_scale_of_a(m, kw, out_e4m3):
         assert torch.equal(D, got[0][0]) and torch.equal(amax, got[0][1])
 
 
+@pytest.mark.parametrize("d", [64, 1024, 8192])
+def test_norm_with_the_smallest_scales(d):
+    """Any scale above 0: a quotient beyond fp32 saturates, and 0 / scale is 0."""
+    x, gamma = randn(5, d, seed=1), torch.ones(d, dtype=torch.bfloat16, device="cuda")
+    x[1] = 0
+    x[2, ::3] = 0
+    for scale in (1e-37, 1e-42):
+        Y = torch.empty(5, d, dtype=torch.uint8, device="cuda").view(E4M3)
+        g.RmsNorm(5, d, "bf16", "e4m3").run(x, gamma, Y, scale=f32(scale))
+        assert torch.equal(Y.float(), 448 * torch.sign(x.float()))
+
+
+@pytest.mark.parametrize("m,kw", [(5, {}), (129, dict(kernel="tc1", block_n=128)), (300, dict(kernel="tc2", block_n=256))])
+def test_e4m3_output_with_the_smallest_scales(m, kw):
+    a, b, bias, y = cancelled(m, 272, "col")
+    for scale in (1e-37, 1e-42):
+        with g.Plan(m, 272, 32, "e4m3", "relu_bias", "col", out_e4m3=True, **kw) as p:
+            p.set_scales(f32(1), f32(1))
+            p.set_out_scale(f32(scale), None)
+            for rows in (torch.ones(m, device="cuda"), None):
+                D = torch.empty(m, 272, dtype=torch.uint8, device="cuda").view(E4M3)
+                p.run_ext(a, b, bias, D, scale_rows=rows)
+                p.check()
+                assert torch.equal(D.float().cpu(), 448.0 * (y > 0))
+
+
 # ------------------------------------------------------------------ the norm
 @pytest.mark.parametrize("eps", [1e-30, 1e-38, 1e-40, 1e-44])
 @pytest.mark.parametrize("m,d", [(3, 64), (3, 1024), (200, 4096), (2, 8192)])
