@@ -11,6 +11,7 @@ there is no fallback implementation.
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 import threading
 
@@ -342,7 +343,8 @@ class Plan:
                  kernel="auto", block_n=0, split_k=0, max_ctas=0, inject_stall=0, stream_k="auto",
                  out_e4m3=False, a_layout="mk"):
         self.m, self.n, self.k = int(m), int(n), int(k)
-        self.dtype, self.epilogue, self.bias_axis, self.b_layout = dtype, epilogue, bias_axis, b_layout
+        self.dtype, self.epilogue, self.bias_axis = dtype, epilogue, bias_axis
+        self.a_layout, self.b_layout = a_layout, b_layout
         opts = Options(KERNEL[kernel], int(block_n), int(split_k), int(max_ctas), int(inject_stall),
                        STREAM_K[stream_k], 1 if out_e4m3 else 0)
         layout = LAYOUT[b_layout] | (A_KM if a_layout == "km" else 0)
@@ -375,15 +377,15 @@ class Plan:
         (see gemm_epi_run_ext in include/gemm_epi.h).  ``residual`` may be D."""
         dev, s = _device_and_stream(stream)
         t_in, t_bias, t_out, f32, i32 = self._types()
-        m, n = self.m, self.n
+        m, n, k = self.m, self.n, self.k
         bias_len = (m if self.bias_axis == "row" else n) if self.epilogue in HAS_BIAS else None
-        gemm_epi_run_ext(self.handle, _operand(A, "Plan.run_ext: A", t_in, m * self.k, dev),
-                         _operand(B, "Plan.run_ext: B", t_in, n * self.k, dev),
-                         None if bias_len is None else _operand(bias, "Plan.run_ext: bias", t_bias, bias_len, dev),
-                         _operand(residual, "Plan.run_ext: residual", t_bias, m * n, dev, True),
-                         _operand(scale_rows, "Plan.run_ext: scale_rows", f32, m, dev, True),
-                         _operand(D, "Plan.run_ext: D", t_out, m * n, dev),
-                         _operand(aux, "Plan.run_ext: aux", i32, m * aux_pitch_words(n), dev)
+        gemm_epi_run_ext(self.handle, _operand(A, "Plan.run_ext: A", t_in, (k, m) if self.a_layout == "km" else (m, k), dev),
+                         _operand(B, "Plan.run_ext: B", t_in, (n, k) if self.b_layout == "nk" else (k, n), dev),
+                         None if bias_len is None else _operand(bias, "Plan.run_ext: bias", t_bias, (bias_len,), dev),
+                         _operand(residual, "Plan.run_ext: residual", t_bias, (m, n), dev, True),
+                         _operand(scale_rows, "Plan.run_ext: scale_rows", f32, (m,), dev, True),
+                         _operand(D, "Plan.run_ext: D", t_out, (m, n), dev),
+                         _operand(aux, "Plan.run_ext: aux", i32, (m, aux_pitch_words(n)), dev)
                          if self.epilogue in HAS_AUX else None, s)
 
     def _types(self):
@@ -467,13 +469,14 @@ class MlpPlan:
         t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[self.dtype]
         wide = torch.bfloat16 if self.dtype == "e4m3" else t
         m, dm, ff, w = self.m, self.d_model, self.d_ff, "MlpPlan.run_prenorm: "
+        w1, w2 = ((ff, dm), (dm, ff)) if self.w_layout == "nk" else ((dm, ff), (ff, dm))
         gemm_epi_mlp_run_prenorm(
-            self.handle, _operand(X, w + "X", wide, m * dm, dev), _operand(residual, w + "residual", wide, m * dm, dev, True),
-            _operand(gamma, w + "gamma", wide, dm, dev), float(eps), _operand(W1, w + "W1", t, dm * ff, dev),
-            _operand(b1, w + "b1", wide, ff, dev), _operand(W2, w + "W2", t, dm * ff, dev), _operand(b2, w + "b2", wide, dm, dev),
-            _operand(S, w + "S", wide, m * dm, dev, True), _operand(N, w + "N", t, m * dm, dev),
-            _operand(scale_rows, w + "scale_rows", torch.float32, m, dev, True), _operand(H, w + "H", t, m * ff, dev),
-            _operand(Y, w + "Y", wide, m * dm, dev), s)
+            self.handle, _operand(X, w + "X", wide, (m, dm), dev), _operand(residual, w + "residual", wide, (m, dm), dev, True),
+            _operand(gamma, w + "gamma", wide, (dm,), dev), float(eps), _operand(W1, w + "W1", t, w1, dev),
+            _operand(b1, w + "b1", wide, (ff,), dev), _operand(W2, w + "W2", t, w2, dev), _operand(b2, w + "b2", wide, (dm,), dev),
+            _operand(S, w + "S", wide, (m, dm), dev, True), _operand(N, w + "N", t, (m, dm), dev),
+            _operand(scale_rows, w + "scale_rows", torch.float32, (m,), dev, True), _operand(H, w + "H", t, (m, ff), dev),
+            _operand(Y, w + "Y", wide, (m, dm), dev), s)
 
     def check(self, stream=None):
         gemm_epi_mlp_check(self.handle, _stream_ptr(stream))
@@ -496,17 +499,34 @@ class MlpPlan:
             pass
 
 
-def _operand(t, name, dtype, count, device, optional=False):
-    """Device address of a tensor that has to be ``count`` dense values of ``dtype`` on the
-    current device (None for an optional one left out)."""
+def _operand(t, name, dtype, shape, device, optional=False):
+    """Device address of a tensor that has to be dense values of ``dtype`` on the current device (None
+    for an optional one left out), ``shape`` its (rows, columns) or (length,): flat, or with an axis
+    split, the rows are the same; another shape of as many values is a mistake."""
     if t is None:
         if optional:
             return None
         raise GemmEpiError(ERR_NULL, name)
-    if t.dtype is not dtype or t.numel() != count or not t.is_contiguous() or t.get_device() != device:
-        raise GemmEpiError(ERR_ARG, f"{name}: wanted {count} contiguous {dtype} values on cuda:{device}, got "
+    if (t.dtype is not dtype or (t.shape != shape and not _same_rows(t.shape, shape)) or not t.is_contiguous()
+            or t.get_device() != device):
+        raise GemmEpiError(ERR_ARG, f"{name}: wanted contiguous {shape} {dtype} on cuda:{device}, got "
                                     f"{tuple(t.shape)} {t.dtype} on {t.device}, strides {t.stride()}")
     return t.data_ptr()
+
+
+def _same_rows(got, want):
+    """Whether contiguous values of shape ``got`` are the rows of ``want``: as many of them, and flat or with
+    an axis's end where a row ends."""
+    if math.prod(got) != math.prod(want):
+        return False
+    if len(want) == 1 or len(got) <= 1:
+        return True
+    n = 1
+    for k in got:
+        if n == want[0]:
+            return True
+        n *= k
+    return n == want[0]
 
 
 def _device_and_stream(stream):
@@ -546,38 +566,39 @@ class RmsNorm:
         self._dt, self._mode = DTYPE[dtype], NORM_OUT[out]
         self._out_t = self._t if out == "same" else torch.float8_e4m3fn
         self._f32 = torch.float32
-        self._scales = self.m if out == "e4m3_rows" else 1
+        self._shape, self._row, self._one = (self.m, self.d), (self.d,), (1,)
+        self._scales = (self.m,) if out == "e4m3_rows" else (1,)
         self._scratch_bytes = gemm_epi_rmsnorm_workspace_bytes(self.m, self.d)
 
     def run(self, X, gamma, Y, residual=None, S=None, scale=None, amax=None, stream=None):
         """S = X + residual (X without one), Y = S / rms(S) * gamma; ``scale`` and ``amax`` as in
         include/gemm_epi.h.  S or Y may be X or residual."""
         dev, s = _device_and_stream(stream)
-        n, t = self.m * self.d, self._t
-        gemm_epi_rmsnorm(self.m, self.d, self._dt, self._mode, self.eps, _operand(X, "RmsNorm.run: X", t, n, dev),
-                         _operand(residual, "RmsNorm.run: residual", t, n, dev, True),
-                         _operand(gamma, "RmsNorm.run: gamma", t, self.d, dev),
-                         _operand(S, "RmsNorm.run: S", t, n, dev, True),
-                         _operand(Y, "RmsNorm.run: Y", self._out_t, n, dev),
+        shape, t = self._shape, self._t
+        gemm_epi_rmsnorm(self.m, self.d, self._dt, self._mode, self.eps, _operand(X, "RmsNorm.run: X", t, shape, dev),
+                         _operand(residual, "RmsNorm.run: residual", t, shape, dev, True),
+                         _operand(gamma, "RmsNorm.run: gamma", t, self._row, dev),
+                         _operand(S, "RmsNorm.run: S", t, shape, dev, True),
+                         _operand(Y, "RmsNorm.run: Y", self._out_t, shape, dev),
                          _operand(scale, "RmsNorm.run: scale", self._f32, self._scales, dev, True),
-                         _operand(amax, "RmsNorm.run: amax", self._f32, 1, dev, True), s)
+                         _operand(amax, "RmsNorm.run: amax", self._f32, self._one, dev, True), s)
 
     def run_bwd(self, dY, S, gamma, dX, dgamma=None, dS=None, workspace=None, stream=None):
         """dX (of X and of the residual alike) and, if given, dgamma, from the sum S of the forward run
         (X without a residual); dS: the skip connection's gradient.  ``workspace``: a uint8 tensor of
         gemm_epi_rmsnorm_workspace_bytes(m, d) bytes, taken from torch's allocator when left out."""
         dev, s = _device_and_stream(stream)
-        n, t = self.m * self.d, self._t
+        shape, t = self._shape, self._t
         if dgamma is None or not self._scratch_bytes:
             workspace = None
         else:
             workspace = _workspace(workspace, self._scratch_bytes, "RmsNorm.run_bwd", dev, stream)
-        gemm_epi_rmsnorm_bwd(self.m, self.d, self._dt, self.eps, _operand(dY, "RmsNorm.run_bwd: dY", t, n, dev),
-                             _operand(S, "RmsNorm.run_bwd: S", t, n, dev),
-                             _operand(gamma, "RmsNorm.run_bwd: gamma", t, self.d, dev),
-                             _operand(dS, "RmsNorm.run_bwd: dS", t, n, dev, True),
-                             _operand(dX, "RmsNorm.run_bwd: dX", t, n, dev),
-                             _operand(dgamma, "RmsNorm.run_bwd: dgamma", t, self.d, dev, True),
+        gemm_epi_rmsnorm_bwd(self.m, self.d, self._dt, self.eps, _operand(dY, "RmsNorm.run_bwd: dY", t, shape, dev),
+                             _operand(S, "RmsNorm.run_bwd: S", t, shape, dev),
+                             _operand(gamma, "RmsNorm.run_bwd: gamma", t, self._row, dev),
+                             _operand(dS, "RmsNorm.run_bwd: dS", t, shape, dev, True),
+                             _operand(dX, "RmsNorm.run_bwd: dX", t, shape, dev),
+                             _operand(dgamma, "RmsNorm.run_bwd: dgamma", t, self._row, dev, True),
                              None if workspace is None else workspace.data_ptr(), s)
 
 
@@ -591,8 +612,8 @@ class ActBackward:
         self._args = (DTYPE[dtype], EPILOGUE[epilogue], AXIS[bias_axis])
         self._t = torch.float16 if dtype == "f16" else torch.bfloat16
         self._i32 = torch.int32
-        self._len = self.m if bias_axis == "row" else self.n
-        self._aux_words = self.m * aux_pitch_words(self.n)
+        self._shape, self._len = (self.m, self.n), (self.m if bias_axis == "row" else self.n,)
+        self._aux_words = (self.m, aux_pitch_words(self.n))
         self._scratch_bytes = gemm_epi_dact_workspace_bytes(self.m, self.n, AXIS[bias_axis])
 
     def run(self, dD, dZ=None, z=None, aux=None, dbias=None, workspace=None, stream=None):
@@ -600,15 +621,15 @@ class ActBackward:
         (relu_aux, relu_aux_bias); dZ: left out without an activation; dbias: left out if not wanted;
         ``workspace``: as for RmsNorm.run_bwd (gemm_epi_dact_workspace_bytes)."""
         dev, s = _device_and_stream(stream)
-        n, t = self.m * self.n, self._t
+        shape, t = self._shape, self._t
         if dbias is None or not self._scratch_bytes:
             workspace = None
         else:
             workspace = _workspace(workspace, self._scratch_bytes, "ActBackward.run", dev, stream)
-        gemm_epi_dact(self.m, self.n, *self._args, _operand(dD, "ActBackward.run: dD", t, n, dev),
-                      _operand(z, "ActBackward.run: z", t, n, dev, True),
+        gemm_epi_dact(self.m, self.n, *self._args, _operand(dD, "ActBackward.run: dD", t, shape, dev),
+                      _operand(z, "ActBackward.run: z", t, shape, dev, True),
                       _operand(aux, "ActBackward.run: aux", self._i32, self._aux_words, dev, True),
-                      _operand(dZ, "ActBackward.run: dZ", t, n, dev, True),
+                      _operand(dZ, "ActBackward.run: dZ", t, shape, dev, True),
                       _operand(dbias, "ActBackward.run: dbias", t, self._len, dev, True),
                       None if workspace is None else workspace.data_ptr(), s)
 

@@ -203,3 +203,46 @@ def test_slopes_at_infinity(dtype, epilogue, left, right):
     g.ActBackward(8, 64, dtype, epilogue, "col").run(dd, dZ=dZ, z=z, dbias=db)
     assert bool((dZ[:, [5, 7]] == 3 * right).all()) and bool((dZ[:, [6, 8]] == 3 * left).all())
     assert db[5:9].tolist() == [24 * right, 24 * left] * 2 and bool(torch.isfinite(db.float()).all())
+
+
+# ------------------------------------------------------------------ shapes
+def test_objects_refuse_tensors_of_another_shape():
+    """As many values in another shape, transposed ones above all, are refused; flat buffers and split axes are the same rows."""
+    x, gamma, Y = randn(4, 64), randn(64), randn(4, 64)
+    op = g.RmsNorm(4, 64)
+    for bad in (randn(64, 4), randn(8, 32), randn(32, 8), randn(2, 64, 2)):
+        for kw in (dict(X=bad), dict(Y=bad), dict(residual=bad)):
+            with pytest.raises(g.GemmEpiError) as e:
+                op.run(**{**dict(X=x, gamma=gamma, Y=Y), **kw})
+            assert e.value.status == g.ERR_ARG
+        with pytest.raises(g.GemmEpiError):
+            op.run_bwd(x, bad, gamma, Y)
+        with pytest.raises(g.GemmEpiError):
+            g.ActBackward(4, 64, "bf16", "gelu").run(x, dZ=Y, z=bad)
+    op.run(x, gamma, Y)
+    for shape in ((256,), (2, 2, 64), (4, 8, 8), (1, 4, 64), (4, 64, 1), (2, 2, 4, 16)):
+        Z = torch.empty_like(Y)
+        op.run(x.view(shape), gamma.view(1, 64), Z.view(shape))
+        assert torch.equal(Z, Y)
+    a, b, bias, D = randn(32, 64), randn(64, 48), randn(48), torch.empty(32, 48, dtype=torch.bfloat16, device="cuda")
+    res, out = randn(32, 48), []
+    for layout in ("kn", "nk"):
+        with g.Plan(32, 48, 64, "bf16", "bias", "col", layout) as p:
+            right, wrong = (b, b.t().contiguous()) if layout == "kn" else (b.t().contiguous(), b)
+            with pytest.raises(g.GemmEpiError):
+                p.run_ext(a, wrong, bias, D, residual=res)
+            with pytest.raises(g.GemmEpiError):
+                p.run_ext(a.view(64, 32), right, bias, D, residual=res)
+            with pytest.raises(g.GemmEpiError):
+                p.run_ext(a, right, bias, D, residual=res.view(48, 32))
+            p.run_ext(a, right, bias.view(1, 48), D, residual=res)
+            p.check()
+            out.append(D.clone())
+    assert torch.equal(*out)
+    x2, w1, w2, b1 = randn(4, 64), randn(64, 128), randn(128, 64), randn(128)
+    N, H, Y2 = torch.empty_like(x2), torch.empty(4, 128, dtype=torch.bfloat16, device="cuda"), torch.empty_like(x2)
+    with g.MlpPlan(4, 64, 128, "bf16", "bias") as p:
+        with pytest.raises(g.GemmEpiError):
+            p.run_prenorm(x2, gamma, w2, b1, w1, gamma, N, H, Y2)
+        p.run_prenorm(x2, gamma, w1, b1, w2, gamma, N, H, Y2)
+        p.check()
