@@ -251,7 +251,10 @@ int gemm_epi_run(gemm_epi_plan_t plan, const void *A, const void *B, const void 
  * The other arguments, rules and errors are gemm_epi_run's, and so is the result without R and
  * d_scale_rows.  The mask of RELU_AUX(_BIAS) is that of the pre-activation, as ever.  Plans with
  * A stored (k, m) return ERR_UNSUPPORTED, plans with an e4m3 output take row scales but no R
- * (ERR_UNSUPPORTED).  The gradient of R is that of D; gemm_epi_dact gives the rest. */
+ * (ERR_UNSUPPORTED), and small-m plans in the grid-wide split-K form (those made with
+ * GEMM_EPI_SK_GRID=1 in the environment) take neither (ERR_UNSUPPORTED).  A plan that chose
+ * 512-wide tiles by itself runs 256-wide ones here, without a split tail; gemm_epi_plan_query
+ * reports the plan of gemm_epi_run.  The gradient of R is that of D; gemm_epi_dact gives the rest. */
 int gemm_epi_run_ext(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, const void *R,
                      const float *d_scale_rows, void *D, uint32_t *aux, void *stream);
 
@@ -391,8 +394,9 @@ int gemm_epi_mlp_run(gemm_epi_mlp_t mlp, const void *X, const void *W1, const vo
  *           beforehand: d_scale_x of gemm_epi_mlp_set_scales is not read by this call.
  *           16-bit plans ignore d_scale_rows.
  *   H, Y, W1, b1, W2, b2  as for gemm_epi_mlp_run.
- * Returns what gemm_epi_mlp_run and gemm_epi_rmsnorm return; every argument is checked before
- * the first launch. */
+ * Returns what gemm_epi_mlp_run, gemm_epi_rmsnorm and gemm_epi_run_ext return (ERR_UNSUPPORTED
+ * for a block planned with GEMM_EPI_SK_GRID=1 and m <= 64); every argument is checked before the
+ * first launch. */
 int gemm_epi_mlp_run_prenorm(gemm_epi_mlp_t mlp, const void *X, const void *R, const void *gamma, float eps,
                              const void *W1, const void *b1, const void *W2, const void *b2, void *S, void *N,
                              float *d_scale_rows, void *H, void *Y, void *stream);
@@ -421,8 +425,9 @@ enum gemm_epi_norm_out {
     GEMM_EPI_NORM_SAME = 0,       /* y in the type of X                                             */
     GEMM_EPI_NORM_E4M3 = 1,       /* e4m3(y / *d_scale): one scale the caller gives, as A's of a
                                      plan (gemm_epi_set_scales)                                     */
-    GEMM_EPI_NORM_E4M3_ROWS = 2   /* e4m3(y / d_scale[i]), d_scale[i] = max_j |y_ij| / 448 (1 for a
-                                     row of zeros): one scale a row, which the call writes          */
+    GEMM_EPI_NORM_E4M3_ROWS = 2   /* e4m3(y / d_scale[i]), d_scale[i] = max_j |y_ij| / 448: one scale a
+                                     row, which the call writes.  A row whose largest |s_ij gamma_j|
+                                     is at most 1e-35 counts as one of zeros: scale 1, codes 0      */
 };
 
 /* Root-mean-square norm of the rows of a residual stream, the residual's addition before it:
@@ -441,8 +446,8 @@ enum gemm_epi_norm_out {
  *   d_amax  E4M3, may be NULL (else ignored): DEVICE pointer to one float, set to 0 on the stream
  *           and max-reduced: max |y| before quantisation, as for gemm_epi_set_out_scale.
  * All arithmetic is fp32, and the norm is taken of the unrounded sum; y and s are rounded to
- * nearest even once, an e4m3 y saturates at +-448.  Inputs are finite, and a row's sum of squares
- * stays below the largest fp32 number.  Every pointer is 16-byte aligned (d_scale and d_amax:
+ * nearest even once, an e4m3 y saturates at +-448.  Inputs are finite, and a row's sum of squares and,
+ * for an e4m3 Y, its |s_ij gamma_j| stay below the largest fp32 number.  Every pointer is 16-byte aligned (d_scale and d_amax:
  * 4-byte).  One launch (two with d_amax), nothing allocated, any stream;
  * calls may overlap as far as their buffers do.  Returns OK, ERR_ARG (a size, type, mode or eps
  * out of range; S without R; buffers that may not coincide), ERR_ALIGN, ERR_NULL,
@@ -481,7 +486,8 @@ int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis);
  *           (E4M3: dD, Z, dZ and dbias are bf16).  n is a multiple of 8.
  *   dD      (m, n), dense.
  *   Z       (m, n): the pre-activation z, as a NONE or BIAS plan writes it.  RELU(_BIAS),
- *           GELU(_BIAS), TANH(_BIAS); else ignored.  ReLU's slope at z = 0 is 0.
+ *           GELU(_BIAS), TANH(_BIAS); else ignored.  ReLU's slope at z = 0 is 0.  A z that overflowed
+ *           to +-inf has the slope of its side (GELU and ReLU 1 or 0, tanh 0).
  *   aux     RELU_AUX(_BIAS): the packed mask that the forward run wrote (bits past column n-1
  *           are ignored); else ignored.
  *   dZ      (m, n), may be dD or Z.  NONE and BIAS: NULL (dZ is dD; ERR_ARG otherwise).
@@ -489,6 +495,8 @@ int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis);
  *           unrounded dZ in an order fixed by (m, n), rounded once.
  *   workspace  as for gemm_epi_rmsnorm_bwd: gemm_epi_dact_workspace_bytes(m, n, bias_axis) bytes,
  *           with dbias.
+ * Where dD is a product that a backward plan can compute and the forward kept a mask, DRELU(_BGRAD) does this
+ * in that product's epilogue; this call is for the other activations and for a dD that comes from elsewhere.
  * One launch, two with dbias and scratch.  Returns OK, ERR_ARG, ERR_ALIGN, ERR_NULL, ERR_NO_DEVICE or ERR_CUDA. */
 int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, const void *dD, const void *Z,
                   const uint32_t *aux, void *dZ, void *dbias, void *workspace, void *stream);

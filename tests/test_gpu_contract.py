@@ -205,6 +205,29 @@ def test_slopes_at_infinity(dtype, epilogue, left, right):
     assert db[5:9].tolist() == [24 * right, 24 * left] * 2 and bool(torch.isfinite(db.float()).all())
 
 
+# ------------------------------------------------------------------ plans
+def test_the_grid_wide_small_m_form_has_no_extended_epilogue(monkeypatch):
+    from test_gpu_ext import Case
+    c = Case(9, 272, 1040, "bf16", "bias", rows=True)
+    x = torch.zeros(9, 64, dtype=torch.bfloat16, device="cuda")
+    w1, w2 = torch.zeros(64, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros(128, 64, dtype=torch.bfloat16, device="cuda")
+    gamma, b1 = x[0].contiguous(), w1[0].contiguous()
+    H, N, Y = torch.zeros(9, 128, dtype=torch.bfloat16, device="cuda"), torch.zeros_like(x), torch.zeros_like(x)
+    monkeypatch.setenv("GEMM_EPI_SK_GRID", "1")
+    with c.plan() as p, g.MlpPlan(9, 64, 128, "bf16", "bias") as mlp:
+        for call in (lambda: p.run_ext(c.a, c.b, c.bias, c.out(), residual=c.res),
+                     lambda: p.run_ext(c.a, c.b, c.bias, c.out(), scale_rows=c.rows),
+                     lambda: mlp.run_prenorm(x, gamma, w1, b1, w2, gamma, N, H, Y)):
+            with pytest.raises(g.GemmEpiError) as e:
+                call()
+            assert e.value.status == g.ERR_UNSUPPORTED
+        D = c.out()
+        p.run_ext(c.a, c.b, c.bias, D)              # without either, gemm_epi_run
+        p.check()
+    c.rows = None
+    ref.close(D, *c.want(residual=False))
+
+
 # ------------------------------------------------------------------ shapes
 def test_objects_refuse_tensors_of_another_shape():
     """As many values in another shape, transposed ones above all, are refused; flat buffers and split axes are the same rows."""
