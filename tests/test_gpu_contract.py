@@ -144,6 +144,23 @@ def test_e4m3_output_with_the_smallest_scales(m, kw):
 
 
 # ------------------------------------------------------------------ the norm
+def test_norm_of_a_sum_whose_rounding_would_show():
+    """S rounds 256.99 down to 256 and 257.01 up to 258: a norm taken of the rounded S would be off by two half-steps in the
+    columns that round the other way, twice what Y's own rounding may be."""
+    r = torch.full((4, 256), 256.0, dtype=torch.bfloat16)
+    x = torch.full((4, 256), 0.98828125, dtype=torch.bfloat16)
+    x[:, ::16] = 1.0078125
+    gamma = torch.linspace(0.5, 2.0, 256).bfloat16()
+    Y, S = torch.empty(4, 256, dtype=torch.bfloat16, device="cuda"), torch.empty(4, 256, dtype=torch.bfloat16, device="cuda")
+    g.RmsNorm(4, 256).run(x.cuda(), gamma.cuda(), Y, residual=r.cuda(), S=S)
+    ref.check_norm("same", "bf16", x, r, gamma, 1e-6, Y, S)
+    s = S.cpu()
+    assert set(s.float().unique().tolist()) == {256.0, 258.0}
+    wrong = ref.norm(s, None, gamma, 1e-6)[1].bfloat16()
+    with pytest.raises(AssertionError):
+        ref.check_norm("same", "bf16", x, r, gamma, 1e-6, wrong, s)
+
+
 @pytest.mark.parametrize("eps", [1e-30, 1e-38, 1e-40, 1e-44])
 @pytest.mark.parametrize("m,d", [(3, 64), (3, 1024), (200, 4096), (2, 8192)])
 def test_norm_and_its_backward_with_the_smallest_eps(m, d, eps):
@@ -159,6 +176,51 @@ def test_norm_and_its_backward_with_the_smallest_eps(m, d, eps):
     dy[1] *= 1e-12
     op.run_bwd(dy, x, gamma, dX, dgamma=dg, dS=ds)
     ref.check_norm_bwd("bf16", dy, x, gamma, ds, e, dX, dg)
+
+
+def column_sums(make, m, step):
+    """Sums over m rows of a term's rows in 64 bits, `step` rows at a time: (sum, sum of magnitudes)."""
+    total = size = 0.0
+    for i in range(0, m, step):
+        t = make(i, min(m, i + step))
+        total, size = total + t.sum(0), size + t.abs().sum(0)
+    return total.cpu(), size.cpu()
+
+
+def test_norm_bwd_sums_over_many_rows():
+    """dgamma of hundreds of rows to each of the 148 blocks.  A sum of N terms in fp32 is off by at most N 2^-24 of the sum of
+    their magnitudes: a thread adds m / 148 rows, its results pass 148 more; a term is off by at most 2^-20 of itself (the
+    sum of squares has d positive terms in chains of at most 64, whose root halves its error, and four more operations)."""
+    m, d = 37000, 8208
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    s = torch.randn(m, d, generator=gen, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randn(m, d, generator=gen, device="cuda", dtype=torch.bfloat16)
+    gamma = randn(d, seed=8)
+    dX, dg = torch.empty_like(s), torch.empty_like(gamma)
+    op = g.RmsNorm(m, d)
+    op.run_bwd(dy, s, gamma, dX, dgamma=dg)
+
+    def terms(i, j):
+        v = s[i:j].double()
+        return dy[i:j].double() * v / torch.sqrt((v * v).mean(1, keepdim=True) + 1e-6)
+
+    want, size = column_sums(terms, m, 1000)
+    ref.close(dg, want, ref.rounded(want, "bf16", ((m / 148 + 148) * 2.0 ** -24 + 2.0 ** -20) * size), "dgamma")
+    again = torch.empty_like(dg)
+    op.run_bwd(dy, s, gamma, dX, dgamma=again)
+    assert torch.equal(again, dg)
+
+
+def test_bias_gradient_of_many_rows_in_one_run():
+    """So many strips that every row is in one run: a lane adds m / 8 rows in a chain, then the 8 warps' sums."""
+    m, n = 1500, 303360
+    gen = torch.Generator(device="cuda").manual_seed(9)
+    dd = torch.randn(m, n, generator=gen, device="cuda", dtype=torch.bfloat16)
+    db = torch.empty(n, dtype=torch.bfloat16, device="cuda")
+    assert g.gemm_epi_dact_workspace_bytes(m, n, g.BIAS_COL) == 0
+    g.ActBackward(m, n, "bf16", "bias", "col").run(dd, dbias=db)
+    want, size = column_sums(lambda i, j: dd[i:j].double(), m, 100)
+    ref.close(db, want, ref.rounded(want, "bf16", (m / 8 + 8) * 2.0 ** -24 * size), "dbias")
 
 
 # ------------------------------------------------------------------ slopes far from zero
@@ -206,6 +268,31 @@ def test_slopes_at_infinity(dtype, epilogue, left, right):
 
 
 # ------------------------------------------------------------------ plans
+@pytest.mark.parametrize("layout", ["kn", "nk"])
+@pytest.mark.parametrize("epilogue", ["bias", "relu_aux_bias"])
+@pytest.mark.parametrize("m,n,k", [(700, 1040, 520), (1025, 2056, 136)])
+def test_plans_that_chose_wide_tiles_by_themselves(m, n, k, epilogue, layout):
+    """Few SMs make a plan choose 512-wide tiles; its runs with a residual then take 256-wide ones, with ring stages, tiles and a
+    raster of their own.  Its plain runs, before and after, keep their bits."""
+    from test_gpu_ext import Case
+    for rows in (False, True):
+        c = Case(m, n, k, "bf16", epilogue, "col", layout, rows=rows)
+        with c.plan(max_ctas=4) as p:
+            assert p.info["block_n"] == 512 and p.info["kernel"] == g.KERNEL_TC2
+            plain = []
+            for _ in range(2):
+                D = c.out()
+                p.run(c.a, c.b, c.bias, D, c.aux())
+                plain.append(D)
+                c.check(plan=p)
+                if rows:
+                    E, aux = c.out(), c.aux()
+                    p.run_ext(c.a, c.b, c.bias, E, scale_rows=c.rows, aux=aux)
+                    p.check()
+                    ref.close(E, *c.want(residual=False), what="row scales alone")
+            assert torch.equal(*plain)
+
+
 def test_the_grid_wide_small_m_form_has_no_extended_epilogue(monkeypatch):
     from test_gpu_ext import Case
     c = Case(9, 272, 1040, "bf16", "bias", rows=True)
