@@ -351,7 +351,7 @@ class Plan:
         self.handle = gemm_epi_plan_opts(self.m, self.n, self.k, DTYPE[dtype], EPILOGUE[epilogue],
                                          AXIS[bias_axis], layout, opts)
         self.out_e4m3 = bool(out_e4m3)
-        self._scales = None
+        self._scales = self._ext = None
 
     @property
     def info(self) -> dict:
@@ -376,24 +376,26 @@ class Plan:
         """D = act(alpha_i * A.B + bias) + residual; ``scale_rows``: m fp32 values, one scale a row of A
         (see gemm_epi_run_ext in include/gemm_epi.h).  ``residual`` may be D."""
         dev, s = _device_and_stream(stream)
-        t_in, t_bias, t_out, f32, i32 = self._types()
-        m, n, k = self.m, self.n, self.k
-        bias_len = (m if self.bias_axis == "row" else n) if self.epilogue in HAS_BIAS else None
-        gemm_epi_run_ext(self.handle, _operand(A, "Plan.run_ext: A", t_in, (k, m) if self.a_layout == "km" else (m, k), dev),
-                         _operand(B, "Plan.run_ext: B", t_in, (n, k) if self.b_layout == "nk" else (k, n), dev),
-                         None if bias_len is None else _operand(bias, "Plan.run_ext: bias", t_bias, (bias_len,), dev),
-                         _operand(residual, "Plan.run_ext: residual", t_bias, (m, n), dev, True),
-                         _operand(scale_rows, "Plan.run_ext: scale_rows", f32, (m,), dev, True),
-                         _operand(D, "Plan.run_ext: D", t_out, (m, n), dev),
-                         _operand(aux, "Plan.run_ext: aux", i32, (m, aux_pitch_words(n)), dev)
-                         if self.epilogue in HAS_AUX else None, s)
+        if self._ext is None:
+            self._ext = self._ext_operands()
+        (a, b, bias_of, res, rows, d, mask) = self._ext
+        gemm_epi_run_ext(self.handle, _operand(A, "Plan.run_ext: A", *a, dev), _operand(B, "Plan.run_ext: B", *b, dev),
+                         None if bias_of is None else _operand(bias, "Plan.run_ext: bias", *bias_of, dev),
+                         _operand(residual, "Plan.run_ext: residual", *res, dev, True),
+                         _operand(scale_rows, "Plan.run_ext: scale_rows", *rows, dev, True),
+                         _operand(D, "Plan.run_ext: D", *d, dev),
+                         None if mask is None else _operand(aux, "Plan.run_ext: aux", *mask, dev), s)
 
-    def _types(self):
-        """torch types of the operands, of bias and residual, and of D; of scales and mask words."""
+    def _ext_operands(self):
+        """(type, shape) of run_ext's operands: A, B, bias (None without one), residual, row scales, D, mask."""
         import torch
         t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[self.dtype]
         wide = torch.bfloat16 if self.dtype == "e4m3" else t
-        return t, wide, t if self.out_e4m3 else wide, torch.float32, torch.int32
+        m, n, k = self.m, self.n, self.k
+        return ((t, (k, m) if self.a_layout == "km" else (m, k)), (t, (n, k) if self.b_layout == "nk" else (k, n)),
+                (wide, (m if self.bias_axis == "row" else n,)) if self.epilogue in HAS_BIAS else None, (wide, (m, n)),
+                (torch.float32, (m,)), (t if self.out_e4m3 else wide, (m, n)),
+                (torch.int32, (m, aux_pitch_words(n))) if self.epilogue in HAS_AUX else None)
 
     def run_bwd(self, A, B, aux, D, dbias=None, stream=None, fused=True):
         """Backward plans (``drelu``/``drelu_bgrad``): D = mask ? alpha*A.B : 0 (+ dbias)."""
@@ -529,14 +531,18 @@ def _same_rows(got, want):
     return n == want[0]
 
 
+_current = None
+
+
 def _device_and_stream(stream):
     """(current device index, raw stream): the device's current stream when none is given."""
-    import torch
-    device = torch.cuda.current_device()
-    if stream is not None:
-        return device, getattr(stream, "cuda_stream", stream)
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # 0.1 us; a Stream object costs 1.3 us
-    return device, raw(device) if raw else torch.cuda.current_stream(device).cuda_stream
+    global _current
+    if _current is None:               # looked up once: 0.15 us of every call
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # 0.1 us; a Stream object costs 1.3 us
+        _current = torch.cuda.current_device, raw or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+    device = _current[0]()
+    return device, _current[1](device) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
 def _scratch(nbytes, device, stream):
