@@ -378,24 +378,25 @@ class Plan:
         dev, s = _device_and_stream(stream)
         if self._ext is None:
             self._ext = self._ext_operands()
-        (a, b, bias_of, res, rows, d, mask) = self._ext
-        gemm_epi_run_ext(self.handle, _operand(A, "Plan.run_ext: A", *a, dev), _operand(B, "Plan.run_ext: B", *b, dev),
-                         None if bias_of is None else _operand(bias, "Plan.run_ext: bias", *bias_of, dev),
-                         _operand(residual, "Plan.run_ext: residual", *res, dev, True),
-                         _operand(scale_rows, "Plan.run_ext: scale_rows", *rows, dev, True),
-                         _operand(D, "Plan.run_ext: D", *d, dev),
-                         None if mask is None else _operand(aux, "Plan.run_ext: aux", *mask, dev), s)
+        t, a, b, wide, bias_of, out, d, f32, rows, i32, mask = self._ext
+        gemm_epi_run_ext(self.handle, _operand(A, "Plan.run_ext: A", t, a, dev), _operand(B, "Plan.run_ext: B", t, b, dev),
+                         None if bias_of is None else _operand(bias, "Plan.run_ext: bias", wide, bias_of, dev),
+                         None if residual is None else _operand(residual, "Plan.run_ext: residual", wide, d, dev),
+                         None if scale_rows is None else _operand(scale_rows, "Plan.run_ext: scale_rows", f32, rows, dev),
+                         _operand(D, "Plan.run_ext: D", out, d, dev),
+                         None if mask is None else _operand(aux, "Plan.run_ext: aux", i32, mask, dev), s)
 
     def _ext_operands(self):
-        """(type, shape) of run_ext's operands: A, B, bias (None without one), residual, row scales, D, mask."""
+        """Types and shapes of run_ext's operands: of A and B, of the bias (None without one) and the residual, of D,
+        of the row scales, of the mask (None without one)."""
         import torch
         t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[self.dtype]
         wide = torch.bfloat16 if self.dtype == "e4m3" else t
         m, n, k = self.m, self.n, self.k
-        return ((t, (k, m) if self.a_layout == "km" else (m, k)), (t, (n, k) if self.b_layout == "nk" else (k, n)),
-                (wide, (m if self.bias_axis == "row" else n,)) if self.epilogue in HAS_BIAS else None, (wide, (m, n)),
-                (torch.float32, (m,)), (t if self.out_e4m3 else wide, (m, n)),
-                (torch.int32, (m, aux_pitch_words(n))) if self.epilogue in HAS_AUX else None)
+        return (t, (k, m) if self.a_layout == "km" else (m, k), (n, k) if self.b_layout == "nk" else (k, n),
+                wide, (m if self.bias_axis == "row" else n,) if self.epilogue in HAS_BIAS else None,
+                t if self.out_e4m3 else wide, (m, n), torch.float32, (m,),
+                torch.int32, (m, aux_pitch_words(n)) if self.epilogue in HAS_AUX else None)
 
     def run_bwd(self, A, B, aux, D, dbias=None, stream=None, fused=True):
         """Backward plans (``drelu``/``drelu_bgrad``): D = mask ? alpha*A.B : 0 (+ dbias)."""
