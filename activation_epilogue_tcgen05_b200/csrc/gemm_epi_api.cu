@@ -249,8 +249,8 @@ int choose(Plan *P) {
         if (split <= 0) {
             // Every cluster of the launch must be resident at once, or the last ones wait for a
             // second wave.  Measured (m = 16, k = 4096, fp16): clusters of up to 4 CTAs, at most
-            // 128 CTAs, all fit (n = 2048: 4 x 16 CTAs 7.9 us against 8 x 16 11.1 us; n = 3072:
-            // 4 x 24 8.1 against 6 x 24 13.1; n = 6144: 2 x 48 12.8 against 3 x 48 20.1), and
+            // 128 CTAs, all fit (n = 2048: 4 x 16 CTAs 7.9 us against 8 x 16 11.1 us; n = 6144:
+            // 2 x 48 12.8 against 3 x 48 20.1), and
             // so do 8 clusters of 8 (n = 1024: 5.1 us).
             const int64_t cap = std::min<int64_t>(128, sms);
             if (tiles_n * 8 <= 64 && max_split >= 8 && 64 <= cap) {

@@ -22,7 +22,9 @@ int64_t dact_rows(int64_t m, int64_t n, bool reads_z) {
 
 // Whole rows to a block: where their blocks fill the GPU (148 SMs, three each), or rows of up to three
 // passes (8192 x 14336 GELU 108 us, by strips 117; 1023 x 4104 from the mask 4.7 against 5.5, 64 x 4096 2.9
-// against 3.4; not 300 x 16384, 12.5 against 11.0, nor 16 x 16384, 10.3 against 4.0).
+// against 3.4; not 300 x 16384, 12.5 against 11.0, nor 16 x 16384, 10.3 against 4.0).  Rows below 2048 columns leave
+// threads without any: up to a few thousand rows the one launch still wins (300 x 128 1.9 against 4.0, 4096 x 1024
+// 6.4 against 8.4, 8192 x 512 9.1 and 8.5), many such rows lose (16384 x 512 20.6 against 14.7, 65536 x 128 63 against 25).
 bool dact_by_rows(int64_t m, int64_t n) { return m >= 148 * 3 * DACT_U || n <= 3 * DACT_WARPS * DACT_COLS; }
 
 namespace {

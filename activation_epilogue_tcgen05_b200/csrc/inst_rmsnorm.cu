@@ -42,7 +42,7 @@ cudaError_t fwd_out(int out, const NormParams &p, bool pdl, cudaStream_t s) {
 }
 
 // Whether a backward call has few rows: up to one vector of 8 to each of 1024 threads an SM.  Then a
-// thread takes one vector, so that a row is done soonest (37 x 1000: 3.2 us, with four vectors 6.2;
+// thread takes one vector, so that a row is done soonest (with partial rows 37 x 1000: 3.2 us, with four vectors 6.2;
 // 64 x 4096 4.7 against 6.0); above, four (300 x 4096 the same, 1200 x 1024 6.3 against 6.7).
 bool few_rows(int64_t m, int64_t d) { return m * (d / 8) <= 148 * 1024; }
 

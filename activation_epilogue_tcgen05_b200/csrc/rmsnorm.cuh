@@ -18,11 +18,11 @@
 //     dg_j = sum_i dy_ij s_ij rho_i
 // rho is taken again from S in the pass that c needs anyway: no statistic is kept by the forward pass.
 //
-// Both are bound by HBM: a row is read once, held in registers as fp32 (forward) or packed
-// (backward), reduced, and written once.  A row is shared by TPR threads, each holding VPT
-// vectors of 8 elements (16-byte loads, neighbouring threads on neighbouring vectors): four
-// vectors a thread where there are rows enough to fill the GPU, so that a thread has many loads in
-// flight and a block enough work; one where the backward has few, so that a row is done soonest.
+// Both are bound by HBM: a row is read once, held in registers as fp32 (forward) or in a ring in shared
+// memory, from where it is read twice (backward), reduced, and written once.  A row is shared by TPR
+// threads, each with VPT vectors of 8 elements (16 bytes at a time, neighbouring threads on neighbouring
+// vectors): four vectors a thread, so that a thread has many loads in flight and a block enough work;
+// one where the backward has few rows, so that a row is done soonest.
 // Measured (a copy moves 6.55 TB/s): 8192 x 4096 bf16 with a residual to e4m3 by rows 36.6 us, 6.4 TB/s;
 // 16384 x 8192 bf16 to bf16 159 us, 6.75 TB/s; backward with the skip gradient 8192 x 4096 43.9 us, 6.1 TB/s,
 // and 4.5 us for dgamma's second launch; 4096 x 14336 f16 70.4 us, 6.7 TB/s, and 5.5 us.
@@ -208,8 +208,12 @@ constexpr int norm_bwd_threads(int tpr, int vpt) { return vpt == 1 ? norm_thread
 constexpr int NORM_BWD_BLOCKS = 148;                  // a B200's SMs
 // So few rows that one cluster of 8 blocks (512 threads each, one vector a thread) takes them in two turns:
 // it adds its blocks' sums through distributed shared memory and writes dgamma itself, in one launch
-// and without scratch.  What that saves is the host's: 37 x 1000 takes 6.8 us a call from Python, with
-// partial rows and a second launch 11.0 (in a graph 4.2 against 3.2).
+// and without scratch.  What that saves is the host's and the scratch: a call from Python takes 6.7 us, with
+// partial rows and a second launch 9.2 (scratch given; 11.0 with torch's allocator).  On the device, in a
+// graph, it is the slower form at most sizes: one turn 4.6 us against 3.9 (8 x 4096), 3.1 and 3.1 (32 x 1024), 2.6 and
+// 3.1 (128 x 256); two 5.4 against 4.0 (16 x 4096), 3.8 and 3.1 (64 x 1024), 3.4 and 3.0 (256 x 256, 1024 x 64); four would be
+// 6.9 against 4.5 (32 x 4096), 5.1 and 3.6 (128 x 1024).  So two turns are the limit: there the host's saving is still
+// above the device's loss.
 constexpr int NORM_CLUSTER = 8;
 constexpr int NORM_CLUSTER_T = 512;
 
