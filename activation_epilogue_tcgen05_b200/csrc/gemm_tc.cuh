@@ -305,8 +305,11 @@ template <>
 struct OutT<DT_E4M3> : OutT<DT_BF16> {};   // e4m3 operands -> bf16 bias and output
 
 // a / *scale, a > 0, as the factor of an e4m3 output; the largest fp32 number where the quotient is beyond it: what
-// is not 0 saturates all the same, and 0 stays 0.
-__device__ __forceinline__ float per_scale(float a, const float *scale) { return fminf(a / __ldg(scale), 3.402823466e38f); }
+// is not 0 saturates all the same, and 0 stays 0.  (Not by fminf: a scale that is NaN has to show.)
+__device__ __forceinline__ float per_scale(float a, const float *scale) {
+    const float f = a / __ldg(scale);
+    return f > 3.402823466e38f ? 3.402823466e38f : f;
+}
 
 // 16-bit bias values -> fp32 (8 packed values from one 16-byte load).
 template <int DT>

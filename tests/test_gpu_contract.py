@@ -127,6 +127,8 @@ def test_norm_with_the_smallest_scales(d):
         Y = torch.empty(5, d, dtype=torch.uint8, device="cuda").view(E4M3)
         g.RmsNorm(5, d, "bf16", "e4m3").run(x, gamma, Y, scale=f32(scale))
         assert torch.equal(Y.float(), 448 * torch.sign(x.float()))
+    g.RmsNorm(5, d, "bf16", "e4m3").run(x, gamma, Y, scale=f32(math.nan))
+    assert bool(Y.float().isnan().all())               # a scale that is no number shows
 
 
 @pytest.mark.parametrize("m,kw", [(5, {}), (129, dict(kernel="tc1", block_n=128)), (300, dict(kernel="tc2", block_n=256))])
@@ -141,6 +143,11 @@ def test_e4m3_output_with_the_smallest_scales(m, kw):
                 p.run_ext(a, b, bias, D, scale_rows=rows)
                 p.check()
                 assert torch.equal(D.float().cpu(), 448.0 * (y > 0))
+                p.set_out_scale(f32(math.nan), None)
+                p.run_ext(a, b, bias, D, scale_rows=rows)
+                p.check()
+                assert bool(D.float().isnan().all())
+                p.set_out_scale(f32(scale), None)
 
 
 # ------------------------------------------------------------------ the norm
