@@ -133,7 +133,9 @@ enum gemm_epi_status {
  * partial tiles plus their flags; a DRELU_BGRAD plan also owns an fp32 workspace for
  * the bias-gradient partial sums (ROW: m x ceil(n/block_n) floats; COL: n x
  * ceil(m/32) floats).  A plan may be run any number of times, on any stream,
- * from one host thread at a time. */
+ * from one host thread at a time.  Its runs may not overlap on the GPU: the workspaces,
+ * flags, status word and amax word are the plan's, so runs on two streams are ordered by
+ * an event, and streams or graphs that run at the same time have a plan each. */
 typedef struct gemm_epi_plan_s *gemm_epi_plan_t;
 
 /* Optional tuning knobs; zero-initialise for automatic choices. */
@@ -368,7 +370,7 @@ int gemm_epi_run_noalloc(int64_t m, int64_t n, int64_t k, int dtype, int epilogu
  * in e4m3 as e4m3(h / s_H) and reports max |h| (the per-tensor requantisation), so
  * alpha1 = s_X * s_W1, alpha2 = s_H * s_W2, and b1, b2, Y are bf16.  Two launches, the
  * second a programmatic dependent of the first; no kernel between them.
- * The handle owns two plans (see gemm_epi_plan); errors as there. */
+ * The handle owns two plans (see gemm_epi_plan): its runs may not overlap either; errors as there. */
 typedef struct gemm_epi_mlp_s *gemm_epi_mlp_t;
 
 int gemm_epi_mlp_plan(int64_t m, int64_t d_model, int64_t d_ff, int dtype, int act, int w_layout,
