@@ -14,9 +14,13 @@
 // a row.  Either way the block writes fp32 partials, one a run of rows or a strip, that a second
 // small kernel adds in order, unless the sums end in the block.  Measured (a copy moves 6.55 TB/s):
 // 8192 x 14336 bf16 GELU with dbias 114 us, 6.2 TB/s, tanh 113; from the mask 87 us, 5.6 TB/s; dbias alone 38.6 us, 6.1 TB/s.
+//
+// z may also come from its checkpoint in 8 bits (CK; ckpt.cuh): codes through the ring, 8 bytes a lane, one exponent for 32
+// columns a batch ahead in registers; and act(z) may be written beside dZ, from the slope's own terms.
 #pragma once
 #include <cstdint>
 
+#include "ckpt.cuh"
 #include "rmsnorm.cuh"
 
 namespace gemm_epi {
@@ -36,6 +40,9 @@ struct DactParams {
     void *dz;
     void *dbias;             // written at once: by dact_rows_kernel (length m), or of a single run (length n)
     float *partial;          // COL: [run][n]; ROW: [strip][m]; or NULL
+    const int8_t *codes;     // CK: z's checkpoint in place of z
+    const uint8_t *exps;     // [m][ckpt_groups(n)]
+    void *h;                 // CK: act(z) in the 16-bit type, or NULL
 };
 
 // GELU'(x) = Phi(x) + x phi(x), Phi and phi the normal distribution and density.  With u = |x| and
@@ -53,7 +60,8 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-__device__ __forceinline__ f32x2 gelu_slope(float x0, float x1) {
+// Phi's own tail comes out on the way, and with it the value: GELU(x) = max(x, 0) - u (1 - Phi(u)) (val; for finite x).
+__device__ __forceinline__ f32x2 gelu_slope(float x0, float x1, f32x2 *val = nullptr) {
     constexpr float c = 0.84932180028801907f;                                 // sqrt(log2(e) / 2): e = 2^-(c u)^2
     const f32x2 v = mul2(pair(min_nan(fabsf(x0), 16.0f), min_nan(fabsf(x1), 16.0f)), both(c));
     const float2 den = split(add2(v, both(2.498f))), q = split(mul2(v, v));
@@ -62,8 +70,12 @@ __device__ __forceinline__ f32x2 gelu_slope(float x0, float x1) {
     h = fma2(t, h, both(0.832031548f));
     h = fma2(t, h, both(-2.2361939f));
     h = fma2(t, h, both(-0.653034389f));
-    const f32x2 w = fma2(v, both(2.0f * 0.39894228040143268f / c), mul2(t, h));        // -2 w(u)
-    const f32x2 left = mul2(pair(ex2_approx(-q.x), ex2_approx(-q.y)), w);
+    h = mul2(t, h);                                                           // -2 exp(u^2 / 2) (1 - Phi(u))
+    const f32x2 w = fma2(v, both(2.0f * 0.39894228040143268f / c), h);        // -2 w(u)
+    const f32x2 e = pair(ex2_approx(-q.x), ex2_approx(-q.y));
+    const f32x2 left = mul2(e, w);
+    if (val != nullptr)
+        *val = fma2(pair(0.5f * fabsf(x0), 0.5f * fabsf(x1)), mul2(e, h), pair(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
     const f32x2 side = pair(copysignf(0.5f, x0), copysignf(0.5f, x1));
     return fma2(left, side, add2(side, both(0.5f)));
 }
@@ -80,25 +92,36 @@ __device__ __forceinline__ f32x2 tanh_slope(float x0, float x1) {
 
 // act'(z) of two neighbouring elements.
 template <int ACT>
-__device__ __forceinline__ f32x2 slope(float z0, float z1) {
-    return ACT == DACT_GELU ? gelu_slope(z0, z1) : tanh_slope(z0, z1);
+__device__ __forceinline__ f32x2 slope(float z0, float z1, f32x2 *val = nullptr) {
+    if constexpr (ACT == DACT_GELU) return gelu_slope(z0, z1, val);
+    if (val != nullptr) *val = tanh2(z0, z1);
+    return tanh_slope(z0, z1);
 }
 
-// d *= act'(z) for a lane's eight elements (bits: their mask).
-template <int ACT>
-__device__ __forceinline__ void through_act(float (&d)[8], const float (&z)[8], uint32_t bits) {
+// d *= act'(z) for a lane's eight elements (bits: their mask); VAL: z becomes act(z).
+template <int ACT, bool VAL = false>
+__device__ __forceinline__ void through_act(float (&d)[8], float (&z)[8], uint32_t bits) {
     if constexpr (ACT == DACT_RELU_MASK) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) d[e] = ((bits >> e) & 1u) ? d[e] : 0.0f;
     } else if constexpr (ACT == DACT_RELU) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = z[e] > 0.0f ? d[e] : 0.0f;
+        for (int e = 0; e < 8; ++e) {
+            d[e] = z[e] > 0.0f ? d[e] : 0.0f;
+            if constexpr (VAL) z[e] = z[e] < 0.0f ? 0.0f : z[e];
+        }
     } else if constexpr (ACT != DACT_NONE) {
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
-            const float2 f = split(mul2(pair(d[e], d[e + 1]), slope<ACT>(z[e], z[e + 1])));
+            f32x2 val;
+            const float2 f = split(mul2(pair(d[e], d[e + 1]), slope<ACT>(z[e], z[e + 1], VAL ? &val : nullptr)));
             d[e] = f.x;
             d[e + 1] = f.y;
+            if constexpr (VAL) {
+                const float2 y = split(val);
+                z[e] = y.x;
+                z[e + 1] = y.y;
+            }
         }
     }
 }
@@ -108,19 +131,41 @@ __device__ __forceinline__ void through_act(float (&d)[8], const float (&z)[8], 
 // worked out (8192 x 14336 GELU 114 us, loaded where it is used 134).  Without z there is little to work
 // out, and a batch is loaded into registers by four blocks an SM instead of three (bias alone 38.6 us,
 // through a ring 40.6; 1023 x 4104 from the mask 5.4 us against 7.0).
-constexpr int DACT_U = 4;                             // rows of a warp in a batch
+constexpr int DACT_U = 4;                             // rows of a warp in a batch (CK: their exponents share a word)
 constexpr bool dact_reads_z(int act) { return act != DACT_NONE && act != DACT_RELU_MASK; }
 // Where a slope is computed, two rows of a batch are worked out at a time: with all four interleaved the constants no longer
 // fit the 80 registers that three blocks an SM leave (8192 x 14336 GELU 120 us, two at a time 112).
 constexpr bool dact_computes(int act) { return act == DACT_GELU || act == DACT_TANH; }
 constexpr int DACT_RING = 2;
-constexpr int DACT_SMEM = DACT_RING * 2 * DACT_U * 32 * DACT_WARPS * 16;
+constexpr int dact_smem(bool ck) { return DACT_RING * DACT_U * 32 * DACT_WARPS * (ck ? 24 : 32); }
 
-template <int DT, int ACT, int AXIS>
+// What a thread has of one row of a stage in the ring: [DACT_RING][U][T] of dD, then as many of z or of its codes.
+template <bool CK>
+struct DactRing {
+    using Zv = std::conditional_t<CK, uint2, uint4>;
+    static constexpr int N = DACT_RING * DACT_U * 32 * DACT_WARPS;
+    static __device__ __forceinline__ uint4 *dd(uint4 *ring, int stage, int u) {
+        return ring + (stage * DACT_U + u) * 32 * DACT_WARPS + threadIdx.x;
+    }
+    static __device__ __forceinline__ Zv *z(uint4 *ring, int stage, int u) {
+        return reinterpret_cast<Zv *>(ring + N) + (stage * DACT_U + u) * 32 * DACT_WARPS + threadIdx.x;
+    }
+};
+
+// A lane's eight values of z in the ring (ok: whether they are there); ex: CK, their exponent.
+template <int DT, bool CK>
+__device__ __forceinline__ void dact_z(uint4 *ring, int stage, int u, bool ok, uint32_t ex, float (&z)[8]) {
+    if constexpr (CK) ckpt_decode8(ok ? *DactRing<CK>::z(ring, stage, u) : make_uint2(0u, 0u), ckpt_step(ok ? ex : 7u), z);
+    else unpack8<DT>(ok ? *DactRing<CK>::z(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), z);
+}
+
+template <int DT, int ACT, int AXIS, bool CK = false, bool VAL = false>
 __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_kernel(const DactParams p) {
     constexpr int T = 32 * DACT_WARPS, U = DACT_U;
     constexpr bool Z = dact_reads_z(ACT), SLOPE = dact_computes(ACT);
-    extern __shared__ uint4 ring[];                   // Z: [DACT_RING][U][dd, z][T]
+    static_assert(Z || !CK, "a checkpoint is one of z");
+    (void)T;
+    extern __shared__ uint4 ring[];                   // Z: DactRing
     __shared__ float4 sums[AXIS == AXIS_COL ? 64 * DACT_WARPS : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * DACT_COLS + 8 * lane;
@@ -133,12 +178,21 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
         for (int u = 0; u < U; ++u) {
             const int64_t i = row + u * DACT_WARPS;
             if (i < r1 && col_ok) {
-                uint4 *dst = ring + (stage * U + u) * 2 * T + threadIdx.x;
-                ptx::cp_async_16(dst, static_cast<const uint16_t *>(p.dd) + i * p.n + col);
-                ptx::cp_async_16(dst + T, static_cast<const uint16_t *>(p.z) + i * p.n + col);
+                ptx::cp_async_16(DactRing<CK>::dd(ring, stage, u), static_cast<const uint16_t *>(p.dd) + i * p.n + col);
+                if constexpr (CK) ptx::cp_async_8(DactRing<CK>::z(ring, stage, u), p.codes + i * p.n + col);
+                else ptx::cp_async_16(DactRing<CK>::z(ring, stage, u), static_cast<const uint16_t *>(p.z) + i * p.n + col);
             }
         }
         ptx::cp_async_commit();                       // (an empty group keeps the count)
+    };
+    const int groups = ckpt_groups(p.n);
+    uint32_t next[U] = {};                            // CK: the coming batch's exponents
+    auto exponents = [&](int64_t row) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int64_t i = row + u * DACT_WARPS;
+            if (i < r1 && col_ok) next[u] = __ldg(p.exps + i * groups + col / CKPT_GROUP);
+        }
     };
     float acc[8];
 #pragma unroll
@@ -148,12 +202,17 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
     if constexpr (Z) {
 #pragma unroll
         for (int i = 0; i < DACT_RING; ++i) fetch(row + i * step, i);
+        if constexpr (CK) exponents(row);
     }
     int stage = 0;
     for (; row < r1; row += step) {
         uint4 dv[U];
-        uint32_t bits[U];
+        uint32_t bits[U], ex = 0u;                    // the mask's; CK: the rows' exponents, a byte each
         if constexpr (Z) {
+            if constexpr (CK) {
+                ex = next[0] | next[1] << 8 | next[2] << 16 | next[3] << 24;
+                exponents(row + step);
+            }
             ptx::cp_async_wait<DACT_RING - 1>();
         } else {
 #pragma unroll
@@ -171,17 +230,19 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
         for (int u = 0; u < U; ++u) {
             const int64_t i = row + u * DACT_WARPS;
             const bool ok = i < r1 && col_ok;
-            const uint4 *src = ring + (stage * U + u) * 2 * T + threadIdx.x;
             float d[8], z[8];
             if constexpr (Z) {
-                unpack8<DT>(ok ? src[0] : make_uint4(0u, 0u, 0u, 0u), d);
-                unpack8<DT>(ok ? src[T] : make_uint4(0u, 0u, 0u, 0u), z);
+                unpack8<DT>(ok ? *DactRing<CK>::dd(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), d);
+                dact_z<DT, CK>(ring, stage, u, ok, ex >> 8 * u & 255u, z);
             } else {
                 unpack8<DT>(dv[u], d);
             }
-            through_act<ACT>(d, z, bits[u]);
+            through_act<ACT, VAL>(d, z, bits[u]);
             if constexpr (ACT != DACT_NONE) {
                 if (ok) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + i * p.n + col) = pack8<DT>(d);
+            }
+            if constexpr (VAL) {
+                if (ok) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.h) + i * p.n + col) = pack8<DT>(z);
             }
             if constexpr (AXIS == AXIS_COL) {
 #pragma unroll
@@ -232,18 +293,21 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
 // time, so that a row's sum ends in the block and dbias is written at once: one launch, no scratch, and one
 // butterfly a row instead of one every 256 columns (8192 x 14336 ReLU 106 us against 115, 1023 x 4104 from the
 // mask 6.7 us a call from Python against 11.0).  The same ring, along the columns.
-template <int DT, int ACT>
+template <int DT, int ACT, bool CK = false, bool VAL = false>
 __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_rows_kernel(const DactParams p) {
-    constexpr int T = 32 * DACT_WARPS, U = DACT_U, PASS = DACT_WARPS * DACT_COLS;
+    constexpr int U = DACT_U, PASS = DACT_WARPS * DACT_COLS;
     constexpr bool Z = dact_reads_z(ACT), SLOPE = dact_computes(ACT);
-    extern __shared__ uint4 ring[];                   // Z: [DACT_RING][U][dd, z][T]
+    static_assert(Z || !CK, "a checkpoint is one of z");
+    extern __shared__ uint4 ring[];                   // Z: DactRing
     __shared__ float sums[DACT_WARPS][U];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = (int64_t)blockIdx.x * U;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const uint16_t *dd = static_cast<const uint16_t *>(p.dd) + r0 * p.n;
-    const uint16_t *zz = Z ? static_cast<const uint16_t *>(p.z) + r0 * p.n : nullptr;
+    const uint16_t *zz = Z && !CK ? static_cast<const uint16_t *>(p.z) + r0 * p.n : nullptr;
+    const int8_t *codes = CK ? p.codes + r0 * p.n : nullptr;
+    uint16_t *hh = VAL ? static_cast<uint16_t *>(p.h) + r0 * p.n : nullptr;
     uint16_t *dz = static_cast<uint16_t *>(p.dz) + r0 * p.n;
     const int rows = (int)min((int64_t)U, p.m - r0);
     auto fetch = [&](int64_t col, int stage) {
@@ -251,13 +315,20 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (u < rows) {
-                    uint4 *dst = ring + (stage * U + u) * 2 * T + threadIdx.x;
-                    ptx::cp_async_16(dst, dd + (int64_t)u * p.n + col);
-                    ptx::cp_async_16(dst + T, zz + (int64_t)u * p.n + col);
+                    ptx::cp_async_16(DactRing<CK>::dd(ring, stage, u), dd + (int64_t)u * p.n + col);
+                    if constexpr (CK) ptx::cp_async_8(DactRing<CK>::z(ring, stage, u), codes + (int64_t)u * p.n + col);
+                    else ptx::cp_async_16(DactRing<CK>::z(ring, stage, u), zz + (int64_t)u * p.n + col);
                 }
             }
         }
         ptx::cp_async_commit();
+    };
+    const int groups = ckpt_groups(p.n);
+    uint32_t next[U] = {};                            // CK: the coming pass's exponents
+    auto exponents = [&](int64_t col) {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u < rows && col < p.n) next[u] = __ldg(p.exps + (r0 + u) * groups + col / CKPT_GROUP);
     };
     float acc[U];
 #pragma unroll
@@ -266,12 +337,17 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
     if constexpr (Z) {
 #pragma unroll
         for (int i = 0; i < DACT_RING; ++i) fetch(col + i * PASS, i);
+        if constexpr (CK) exponents(col);
     }
     int stage = 0;
     for (; col < p.n; col += PASS) {
         uint4 dv[U];
-        uint32_t bits[U];
+        uint32_t bits[U], ex = 0u;                    // the mask's; CK: the rows' exponents, a byte each
         if constexpr (Z) {
+            if constexpr (CK) {
+                ex = next[0] | next[1] << 8 | next[2] << 16 | next[3] << 24;
+                exponents(col + PASS);
+            }
             ptx::cp_async_wait<DACT_RING - 1>();
         } else {
 #pragma unroll
@@ -291,17 +367,19 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int u = u0 + k;
-                const uint4 *src = ring + (stage * U + u) * 2 * T + threadIdx.x;
                 float d[8], z[8];
                 if constexpr (Z) {
-                    unpack8<DT>(u < rows ? src[0] : make_uint4(0u, 0u, 0u, 0u), d);
-                    unpack8<DT>(u < rows ? src[T] : make_uint4(0u, 0u, 0u, 0u), z);
+                    unpack8<DT>(u < rows ? *DactRing<CK>::dd(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), d);
+                    dact_z<DT, CK>(ring, stage, u, u < rows, ex >> 8 * u & 255u, z);
                 } else {
                     unpack8<DT>(dv[u], d);
                 }
-                through_act<ACT>(d, z, bits[u]);
+                through_act<ACT, VAL>(d, z, bits[u]);
                 if constexpr (ACT != DACT_NONE) {
                     if (u < rows) *reinterpret_cast<uint4 *>(dz + (int64_t)u * p.n + col) = pack8<DT>(d);
+                }
+                if constexpr (VAL) {
+                    if (u < rows) *reinterpret_cast<uint4 *>(hh + (int64_t)u * p.n + col) = pack8<DT>(z);
                 }
                 sum[k] = acc[k] + (((d[0] + d[1]) + (d[2] + d[3])) + ((d[4] + d[5]) + (d[6] + d[7])));
             }

@@ -10,10 +10,10 @@ template <int DTV, bool Q>
 struct TcFindExt {
     template <int CG, int EPI, bool BMN, int BN>
     static bool leaf(TcLauncher *l, KernelInfo *i) {
-        constexpr int ES = DTV == DT_E4M3 ? 1 : 2;
+        constexpr int ES = dt_size(DTV);
         constexpr int STG = tc_stages(tc_katoms(128 * 128 + (BN / CG) * 128) * (128 * 128 + (BN / CG) * 128));
-        if constexpr ((BMN && (BN / CG) % (128 / ES) != 0) || (BN == 512 && (CG != 2 || Q))) {
-            return false;     // as for the plain kernels
+        if constexpr ((BMN && (BN / CG) % (128 / ES) != 0) || (BN == 512 && (CG != 2 || Q || DTV == DT_I8))) {
+            return false;     // as for the plain kernels; no 512-wide tiles of 8-bit integers, whose mainloop is e4m3's
         } else {
             using C = TcCfg<DTV, EPI, AXIS_COL, BMN, BN, CG, STG, Q, false, true>;
             *l = &launch_tc<C>;

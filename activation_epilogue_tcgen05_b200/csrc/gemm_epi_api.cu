@@ -94,7 +94,9 @@ bool live(gemm_epi_plan_t h) {
     return h && g_plans.count(p) && p->magic == kPlanMagic;
 }
 
-int esize(int dt) { return dt == GEMM_EPI_E4M3 ? 1 : 2; }
+int esize(int dt) { return dt_size(dt); }
+// The type of bias, residual and D.
+int wide_type(int dt) { return esize(dt) == 1 ? GEMM_EPI_BF16 : dt; }
 
 // Public epilogue -> kernel activation, and whether it adds a bias.  The
 // bias-free epilogues run the bias kernels with a NULL bias pointer.
@@ -216,11 +218,12 @@ int choose(Plan *P) {
         return GEMM_EPI_ERR_UNSUPPORTED;
     P->kernel = kernel;
     const bool b_mn = P->b_layout == GEMM_EPI_B_KN;
+    const bool i8 = P->dtype == GEMM_EPI_I8;          // one kernel a plan, with the extended epilogue
     const int bk = 128 / esize(P->dtype);
     const int64_t num_kb = (P->k + bk - 1) / bk;
     const int sms = P->opts.max_ctas > 0 ? std::min(P->opts.max_ctas, P->num_sms) : P->num_sms;
 
-    if (kernel == GEMM_EPI_KERNEL_SPLITK && !P->no_workspace && getenv_flag("GEMM_EPI_SK_GRID")) {
+    if (kernel == GEMM_EPI_KERNEL_SPLITK && !P->no_workspace && !i8 && getenv_flag("GEMM_EPI_SK_GRID")) {
         // grid-wide form: every SM takes an equal share of the (tile, k-block) units; a split
         // tile is finished by the CTA holding its first k-block, from partials the others
         // publish in a plan-owned workspace
@@ -274,6 +277,7 @@ int choose(Plan *P) {
         if (const char *g = getenv("GEMM_EPI_SK_PRE")) P->sk_pre_kb = atoi(g);   // tuning knob (< 0: all)
         P->sk_pre_x = getenv_flag("GEMM_EPI_SK_PRE_X") ? 1 : 0;
         KernelInfo none_info;
+        if (i8) return find_sk_ext(P->dtype, P->kepi, b_mn, P->nm, false, &P->sk_launch, &P->info) ? GEMM_EPI_OK : GEMM_EPI_ERR_UNSUPPORTED;
         if (!find_sk(P->dtype, GEMM_EPI_NONE, 0, b_mn, P->nm, false, &P->sk_none_launch, &none_info))
             return GEMM_EPI_ERR_UNSUPPORTED;
         if (!find_sk(P->dtype, P->kepi, P->axis, b_mn, P->nm, P->qout, &P->sk_launch, &P->info))
@@ -285,8 +289,8 @@ int choose(Plan *P) {
         if (bn == 0) {
             const int64_t tiles256 = ((m + bm - 1) / bm) * ((n + 255) / 256);
             bn = tiles256 >= sms / cg ? 256 : 128;
-            // a pair's e4m3 B half-tile stored (k, n) must be a whole 128-byte box: 128 columns
-            if (cg == 2 && P->dtype == GEMM_EPI_E4M3 && b_mn) bn = 256;
+            // a pair's 8-bit B half-tile stored (k, n) must be a whole 128-byte box: 128 columns
+            if (cg == 2 && esize(P->dtype) == 1 && b_mn) bn = 256;
             if (P->a_km) bn = 256;     // A stored (k, m) is built with 256-wide tiles only
             // Many waves of 16-bit work with a light epilogue: 512-wide pair tiles.  They move a
             // quarter fewer operand bytes per flop into each SM, which under the power cap buys
@@ -296,7 +300,7 @@ int choose(Plan *P) {
             const int64_t tiles512 = ((m + 255) / 256) * ((n + 511) / 512);
             const bool light = P->kepi == EPI_NONE || P->kepi == EPI_BIAS || P->kepi == EPI_RELU ||
                                P->kepi == EPI_RELU_AUX;
-            if (cg == 2 && light && P->dtype != GEMM_EPI_E4M3 && !P->a_km && !P->qout && tiles512 >= 4 * (sms / 2))
+            if (cg == 2 && light && esize(P->dtype) == 2 && !P->a_km && !P->qout && tiles512 >= 4 * (sms / 2))
                 bn = 512;
         }
         if (bn != 128 && bn != 256 && bn != 512) return GEMM_EPI_ERR_ARG;
@@ -383,12 +387,17 @@ int choose(Plan *P) {
             P->fused = ok_k && ok_b && ok_a && g && g[0] == '1';
         }
         KernelInfo none_info;
+        P->split = 1;
+        if (i8) {
+            if (!find_tc_ext(cg, P->dtype, P->kepi, b_mn, bn, false, &P->tc_launch, &P->info) || P->info.katoms != P->katoms)
+                return GEMM_EPI_ERR_UNSUPPORTED;
+            return GEMM_EPI_OK;
+        }
         if (!find_tc(cg, P->dtype, GEMM_EPI_NONE, 0, b_mn, bn, false, P->a_km, &P->tc_none_launch, &none_info))
             return GEMM_EPI_ERR_UNSUPPORTED;
         if (!find_tc(cg, P->dtype, P->kepi, P->axis, b_mn, bn, P->qout, P->a_km, &P->tc_launch, &P->info))
             return GEMM_EPI_ERR_UNSUPPORTED;
         if (P->info.katoms != P->katoms || none_info.katoms != P->katoms) return GEMM_EPI_ERR_UNSUPPORTED;
-        P->split = 1;
     }
     if (P->kepi != EPI_NONE && !P->qout && !find_bias_act(P->dtype, P->kepi, P->axis, &P->ba_launch))
         return GEMM_EPI_ERR_UNSUPPORTED;
@@ -432,8 +441,9 @@ bool on_plan_device(const Plan *P) {
     return dev == P->device;
 }
 
-int check_run_args(Plan *P, const void *A, const void *B, const void *bias, void *D, uint32_t *aux) {
+int check_run_args(Plan *P, const void *A, const void *B, const void *bias, void *D, uint32_t *aux, bool i8 = false) {
     if (!on_plan_device(P)) return GEMM_EPI_ERR_ARG;
+    if ((P->dtype == GEMM_EPI_I8) != i8) return GEMM_EPI_ERR_ARG; // 8-bit integers run through gemm_epi_run_scaled
     if (P->bwd) return GEMM_EPI_ERR_ARG;          // backward plans run through gemm_epi_run_bwd
     if (!A || !B || !D) return GEMM_EPI_ERR_NULL;
     if (P->has_bias && !bias) return GEMM_EPI_ERR_NULL;
@@ -503,7 +513,7 @@ int ensure_maps(Plan *P, const void *A, const void *B, void *D) {
             ok = ok && (P->a_km ? make_map(&P->tmA, dt, A, m, k, box_n, bk) : make_map(&P->tmA, dt, A, k, m, bk, 128));
             ok = ok && (b_kn ? make_map(&P->tmB, dt, B, n, k, box_n, bk) : make_map(&P->tmB, dt, B, k, n, bk, bn_local));
         }
-        const int out_dt = dt == GEMM_EPI_E4M3 ? GEMM_EPI_BF16 : dt;
+        const int out_dt = wide_type(dt);
         if (P->qout)   // e4m3 output goes out with direct stores; the map is valid but unused
             ok = ok && make_map(&P->tmD, GEMM_EPI_E4M3, D, n, m, 32, 32, CU_TENSOR_MAP_SWIZZLE_NONE);
         else           // the epilogue stages 32 rows x 32 outputs (64 bytes a row, 64-byte swizzle) per store
@@ -520,10 +530,11 @@ int ensure_maps(Plan *P, const void *A, const void *B, void *D) {
     return GEMM_EPI_OK;
 }
 
-// The extended epilogue of one launch: the residual and the scales by row (either may be NULL).
+// The extended epilogue of one launch: the residual and the scales by row (either may be NULL), and by column (8-bit integers).
 struct Ext {
     const void *R;
     const float *scale_rows;
+    const float *scale_cols = nullptr;
 };
 
 // Tile width of a TC plan's launches with the extended epilogue: 256 where the plan chose 512 by
@@ -549,7 +560,7 @@ int find_ext(const Plan *P, TcLauncher *tc, SkLauncher *sk, int *katoms) {
 
 int check_ext_args(const Plan *P, const Ext &x) {
     if (P->qout && x.R) return GEMM_EPI_ERR_UNSUPPORTED;      // a residual stream is kept in 16 bits
-    if (!aligned16(x.R) || (reinterpret_cast<uintptr_t>(x.scale_rows) & 3u)) return GEMM_EPI_ERR_ALIGN;
+    if (!aligned16(x.R) || !aligned16(x.scale_cols) || (reinterpret_cast<uintptr_t>(x.scale_rows) & 3u)) return GEMM_EPI_ERR_ALIGN;
     TcLauncher tc;
     SkLauncher sk;
     int katoms;
@@ -559,9 +570,8 @@ int check_ext_args(const Plan *P, const Ext &x) {
 // The residual's tensor map: boxes and swizzle as D's.
 int ensure_res_map(Plan *P, const Ext &x) {
     if (!x.R || P->kernel == GEMM_EPI_KERNEL_SPLITK || P->cR == x.R) return GEMM_EPI_OK;
-    const int out_dt = P->dtype == GEMM_EPI_E4M3 ? GEMM_EPI_BF16 : P->dtype;
     P->cR = nullptr;
-    if (!make_map(&P->tmR, out_dt, x.R, P->n, P->m, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return GEMM_EPI_ERR_CUDA;
+    if (!make_map(&P->tmR, wide_type(P->dtype), x.R, P->n, P->m, 32, 32, CU_TENSOR_MAP_SWIZZLE_64B)) return GEMM_EPI_ERR_CUDA;
     P->cR = x.R;
     return GEMM_EPI_OK;
 }
@@ -630,6 +640,7 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
         if (ext) {
             L.p.residual = ext->R;
             L.p.scale_rows = ext->scale_rows;
+            L.p.scale_cols = ext->scale_cols;
             L.p.bias_row = P->axis == GEMM_EPI_BIAS_ROW;
         }
         L.grid = P->grid;
@@ -677,6 +688,7 @@ int launch_main(Plan *P, bool fused, const void *bias, void *D, uint32_t *aux, c
             L.tmR = ext->R ? P->tmR : P->tmD;
             L.p.residual = ext->R;
             L.p.scale_rows = ext->scale_rows;
+            L.p.scale_cols = ext->scale_cols;
             L.p.bias_row = P->axis == GEMM_EPI_BIAS_ROW;
         }
         L.grid = P->grid;
@@ -694,7 +706,7 @@ int plan_fields(Plan *P, int64_t m, int64_t n, int64_t k, int dtype, int epilogu
     if (m <= 0 || n <= 0 || k <= 0) return GEMM_EPI_ERR_ARG;
     if (m > 0x7fffffffll || n > 0x7fffffffll || k > 0x7fffffffll) return GEMM_EPI_ERR_ARG;
     if (((m + 127) / 128) * ((n + 127) / 128) > 0x7fffffffll) return GEMM_EPI_ERR_ARG;   // tile count is an int
-    if (dtype < GEMM_EPI_F16 || dtype > GEMM_EPI_E4M3) return GEMM_EPI_ERR_ARG;
+    if ((dtype < GEMM_EPI_F16 || dtype > GEMM_EPI_E4M3) && dtype != GEMM_EPI_I8) return GEMM_EPI_ERR_ARG;
     if (epilogue < GEMM_EPI_NONE || epilogue > GEMM_EPI_DRELU_BGRAD) return GEMM_EPI_ERR_ARG;
     if (bias_axis != GEMM_EPI_BIAS_ROW && bias_axis != GEMM_EPI_BIAS_COL) return GEMM_EPI_ERR_ARG;
     if (b_layout & ~(GEMM_EPI_B_NK | GEMM_EPI_A_KM)) return GEMM_EPI_ERR_ARG;
@@ -715,6 +727,9 @@ int plan_fields(Plan *P, int64_t m, int64_t n, int64_t k, int dtype, int epilogu
                             epilogue == GEMM_EPI_GELU_BIAS || epilogue == GEMM_EPI_RELU || epilogue == GEMM_EPI_GELU;
         if (dtype != GEMM_EPI_E4M3 || !epi_ok) return GEMM_EPI_ERR_UNSUPPORTED;
     }
+    // 8-bit integers: forward plans, A stored (m, k), sums that int32 holds whatever the codes (2^14 k < 2^31)
+    if (dtype == GEMM_EPI_I8 && (epilogue > GEMM_EPI_TANH || a_km || k > GEMM_EPI_I8_MAX_K || o.block_n == 512))
+        return GEMM_EPI_ERR_UNSUPPORTED;
     // 16-byte row pitches (TMA strides; the pages' 16-byte alignment rule)
     const int es = esize(dtype);
     const int out_es = 2;
@@ -859,6 +874,7 @@ bool find_tc_ext(int cg, int dt, int epi, bool b_mn, int bn, bool qout, TcLaunch
     case DT_F16: return find_tc_f16_ext(cg, epi, b_mn, bn, l, i);
     case DT_BF16: return find_tc_bf16_ext(cg, epi, b_mn, bn, l, i);
     case DT_E4M3: return find_tc_e4m3_ext(cg, epi, b_mn, bn, l, i);
+    case DT_I8: return find_tc_i8_ext(cg, epi, b_mn, bn, l, i);
     }
     return false;
 }
@@ -868,6 +884,7 @@ bool find_sk_ext(int dt, int epi, bool w_mn, int nm, bool qout, SkLauncher *l, K
     case DT_F16: return find_sk_f16_ext(epi, w_mn, nm, l, i);
     case DT_BF16: return find_sk_bf16_ext(epi, w_mn, nm, l, i);
     case DT_E4M3: return find_sk_e4m3_ext(epi, w_mn, nm, l, i);
+    case DT_I8: return find_sk_i8_ext(epi, w_mn, nm, l, i);
     }
     return false;
 }
@@ -916,6 +933,7 @@ int gemm_epi_plan_opts(int64_t m, int64_t n, int64_t k, int dtype, int epilogue,
 int gemm_epi_set_scales(gemm_epi_plan_t plan, const float *d_scale_a, const float *d_scale_b) {
     if (!live(plan)) return GEMM_EPI_ERR_ARG;
     Plan *P = reinterpret_cast<Plan *>(plan);
+    if (P->dtype == GEMM_EPI_I8) return GEMM_EPI_ERR_ARG;          // their scales come with each run
     if (!d_scale_a && !d_scale_b && P->dtype != GEMM_EPI_E4M3) {   // 16-bit: back to alpha = 1
         P->scale_a = P->scale_b = nullptr;
         return GEMM_EPI_OK;
@@ -968,6 +986,20 @@ int gemm_epi_run_ext(gemm_epi_plan_t plan, const void *A, const void *B, const v
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (P->qout && P->amax && cudaMemsetAsync(P->amax, 0, sizeof(float), s) != cudaSuccess) return GEMM_EPI_ERR_CUDA;
     return launch_main(P, true, bias, D, aux, s, nullptr, &x);
+}
+
+int gemm_epi_run_scaled(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, const void *R, const float *d_scale_rows,
+                    const float *d_scale_cols, void *D, uint32_t *aux, void *stream) {
+    if (!live(plan)) return GEMM_EPI_ERR_ARG;
+    Plan *P = reinterpret_cast<Plan *>(plan);
+    const Ext x{R, d_scale_rows, d_scale_cols};
+    int rc = check_run_args(P, A, B, bias, D, aux, true);
+    if (rc == GEMM_EPI_OK && (!d_scale_rows || !d_scale_cols)) rc = GEMM_EPI_ERR_NULL;
+    if (rc == GEMM_EPI_OK) rc = check_ext_args(P, x);
+    if (rc == GEMM_EPI_OK) rc = ensure_maps(P, A, B, D);
+    if (rc == GEMM_EPI_OK) rc = ensure_res_map(P, x);
+    if (rc != GEMM_EPI_OK) return rc;
+    return launch_main(P, true, bias, D, aux, reinterpret_cast<cudaStream_t>(stream), nullptr, &x);
 }
 
 int gemm_epi_unfused_run(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, void *D,
@@ -1172,6 +1204,7 @@ int gemm_epi_mlp_plan(int64_t m, int64_t d_model, int64_t d_ff, int dtype, int a
     if (!out) return GEMM_EPI_ERR_ARG;
     if (act != GEMM_EPI_BIAS && act != GEMM_EPI_RELU_BIAS && act != GEMM_EPI_GELU_BIAS) return GEMM_EPI_ERR_ARG;
     if (w_layout != GEMM_EPI_B_KN && w_layout != GEMM_EPI_B_NK) return GEMM_EPI_ERR_ARG;
+    if (dtype == GEMM_EPI_I8) return GEMM_EPI_ERR_UNSUPPORTED;
     Mlp *M = new (std::nothrow) Mlp();
     if (!M) return GEMM_EPI_ERR_CUDA;
     M->magic = kMlpMagic;

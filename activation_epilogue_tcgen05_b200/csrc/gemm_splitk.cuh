@@ -64,6 +64,7 @@ struct SkParams {
     const void *residual;        // EXT kernels: as TcParams::residual, scale_rows, bias_row
     const float *scale_rows;
     int bias_row;
+    const float *scale_cols;     // as TcParams::scale_cols
 };
 
 template <int DT_, int EPI_, int AXIS_, bool W_MN_, int NM_, int STAGES_, bool QOUT_ = false, bool EXT_ = false>
@@ -72,9 +73,10 @@ struct SkCfg {
     static constexpr int DT = DT_, EPI = EPI_, AXIS = AXIS_, NM = NM_, STAGES = STAGES_;
     static constexpr bool QOUT = QOUT_;             // e4m3 output quantised in the epilogue
     static constexpr bool W_MN = W_MN_;             // weight stored (k, n): MMA operand A is MN-major
-    static constexpr int ESIZE = DT == DT_E4M3 ? 1 : 2;
-    static constexpr int KIND = DT == DT_E4M3 ? 1 : 0;
-    static constexpr uint32_t FMT = DT == DT_BF16 ? 1u : 0u;
+    static constexpr bool I8 = DT == DT_I8;         // int32 accumulators and partials (TcCfg::I8)
+    static constexpr int ESIZE = dt_size(DT);
+    static constexpr int KIND = dt_kind(DT);
+    static constexpr uint32_t FMT = dt_format(DT);
     static constexpr int BK = 128 / ESIZE;
     static constexpr int UMMA_K = 32 / ESIZE;
     static constexpr int KSTEPS = BK / UMMA_K;
@@ -98,6 +100,7 @@ struct SkCfg {
     static_assert(SMEM_BYTES <= 232448, "shared memory budget");
     static_assert(X_BYTES % 1024 == 0, "stage alignment");
     static_assert(!QOUT || (DT == DT_E4M3 && EPI != EPI_RELU_AUX), "FP8 output: e4m3 forward plans");
+    static_assert(!I8 || (EXT && !QOUT), "8-bit integers: the extended epilogue, 16-bit outputs");
 };
 
 // grid = tiles_n * S CTAs, cluster (S, 1, 1): cluster c owns output columns
@@ -188,6 +191,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // ready, so that their latency is off the reduction's path.
     const bool epi = warp >= 2;
     float cbias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float cscale[C::I8 ? 4 : 1] = {};                 // I8: the columns' scales
     float alpha = 1.0f, inv_out = 1.0f;
     // EXT: residual values and row scales of the first four blocks of rows that this warp finishes
     // (all there are for up to 16 rows, or 64 with a cluster of four); later blocks read theirs when they
@@ -217,6 +221,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             for (int gl = 0; gl < 4; ++gl) {
                 const int col = n0 + 32 * ((int)rank + gl * (int)csize) + lane;
                 if (gl < groups && col < p.n && p.bias != nullptr) cbias[gl] = OutT<C::DT>::load(p.bias, col);
+            }
+        }
+        if constexpr (C::I8) {
+#pragma unroll
+            for (int gl = 0; gl < 4; ++gl) {
+                const int col = n0 + 32 * ((int)rank + gl * (int)csize) + lane;
+                if (gl < groups && col < p.n) cscale[gl] = __ldg(p.scale_cols + col);
             }
         }
         if (C::EXT && p.scale_rows != nullptr) alpha = p.scale_b != nullptr ? __ldg(p.scale_b) : 1.0f;
@@ -272,7 +283,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
         }
     } else if (warp == 1) {
         if (lane == 0) {
-            constexpr uint32_t idesc = make_idesc(C::FMT, C::W_MN, false, 128, C::NM);
+            constexpr uint32_t idesc = make_idesc(C::FMT, C::W_MN, false, 128, C::NM, dt_acc_format(C::DT));
             uint32_t stage = 0, phase = 0;
             bool ok = true;
             for (int i = 0; i < my_kb; ++i) {
@@ -312,8 +323,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     // The fused epilogue of rows 4u .. 4u+3 of column group `grp` (this thread's column
     // n0 + 32 grp + lane), from their fp32 sums `part`: the four rows' values first, without
     // branches, then their stores.
-    // (EXT: its residual values r and row scales a.)
-    auto emit4 = [&](int grp, int u, const float (&part)[4], float cb, const R16(&r)[C::EXT ? 4 : 1],
+    // (EXT: its residual values r and row scales a; I8: the sums are int32, cs is the column's scale.)
+    auto emit4 = [&](int grp, int u, const float (&part)[4], float cb, float cs, const R16(&r)[C::EXT ? 4 : 1],
                      const float (&a)[C::EXT ? 4 : 1]) {
         const int col = n0 + 32 * grp + lane;
         const bool col_ok = col < p.n;
@@ -326,7 +337,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             const int i = 4 * u + c;
             float al = alpha;
             if constexpr (C::EXT) if (p.scale_rows != nullptr) al = a[c] * alpha;
-            float x = part[c] * al;
+            float x = (C::I8 ? acc_f32<C::I8>(__float_as_uint(part[c])) * cs : part[c]) * al;
             if constexpr (C::EPI != EPI_NONE) {
                 if constexpr (C::AXIS == AXIS_COL) x += cb;
                 if constexpr (C::EXT) {
@@ -383,24 +394,27 @@ __global__ void __launch_bounds__(C::THREADS, 1)
             // a cluster of one CTA: the accumulator is the whole sum; each warp finishes its own
             // column group straight from its registers
             if (have) {
-                float cb = 0.0f;
+                float cb = 0.0f, cs = 1.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (j == q) cb = cbias[j];
+                    if (j == q) {
+                        cb = cbias[j];
+                        if constexpr (C::I8) cs = cscale[C::I8 ? j : 0];
+                    }
 #pragma unroll
                 for (int u = 0; u < C::NM / 4; ++u) {
                     const float part[4] = {acc[4 * u], acc[4 * u + 1], acc[4 * u + 2], acc[4 * u + 3]};
                     if constexpr (C::EXT) {
                         if (u < 4) {
-                            emit4(q, u, part, cb, pre_r[u < 4 ? u : 0], pre_a[u < 4 ? u : 0]);
+                            emit4(q, u, part, cb, cs, pre_r[u < 4 ? u : 0], pre_a[u < 4 ? u : 0]);
                         } else {
                             R16 r[4];
                             float a[4];
                             load_ext(q, u, r, a);
-                            emit4(q, u, part, cb, r, a);
+                            emit4(q, u, part, cb, cs, r, a);
                         }
                     } else {
-                        emit4(q, u, part, cb, pre_r[0], pre_a[0]);
+                        emit4(q, u, part, cb, cs, pre_r[0], pre_a[0]);
                     }
                 }
             }
@@ -436,18 +450,21 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                 for (int r = 1; r < C::MAX_SPLIT; ++r) {
                     if (r < (int)csize) {
-                        sum.x += pv[r].x;
-                        sum.y += pv[r].y;
-                        sum.z += pv[r].z;
-                        sum.w += pv[r].w;
+                        sum.x = __uint_as_float(acc_add<C::I8>(__float_as_uint(sum.x), pv[r].x));
+                        sum.y = __uint_as_float(acc_add<C::I8>(__float_as_uint(sum.y), pv[r].y));
+                        sum.z = __uint_as_float(acc_add<C::I8>(__float_as_uint(sum.z), pv[r].z));
+                        sum.w = __uint_as_float(acc_add<C::I8>(__float_as_uint(sum.w), pv[r].w));
                     }
                 }
                 const float part[4] = {sum.x, sum.y, sum.z, sum.w};
                 if (warp == 2 && lane == 0) trace_stage(p.trace, 2, tr_i, 33, tile_n, unit);
-                float cb = 0.0f;
+                float cb = 0.0f, cs = 1.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    if (j == gl) cb = cbias[j];
+                    if (j == gl) {
+                        cb = cbias[j];
+                        if constexpr (C::I8) cs = cscale[C::I8 ? j : 0];
+                    }
                 const int grp = (int)rank + gl * (int)csize;
                 if constexpr (C::EXT) {
                     const int b = (unit - ew) / 4;          // this warp's b-th block
@@ -463,9 +480,9 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     } else {
                         load_ext(grp, u, r, a);
                     }
-                    emit4(grp, u, part, cb, r, a);
+                    emit4(grp, u, part, cb, cs, r, a);
                 } else {
-                    emit4(grp, u, part, cb, pre_r[0], pre_a[0]);
+                    emit4(grp, u, part, cb, cs, pre_r[0], pre_a[0]);
                 }
                 if (warp == 2 && lane == 0) trace_stage(p.trace, 2, tr_i, 34, tile_n, unit);
             }

@@ -59,7 +59,12 @@
 
 namespace gemm_epi {
 
-enum : int { DT_F16 = 0, DT_BF16 = 1, DT_E4M3 = 2 };
+enum : int { DT_F16 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_I8 = 4 };
+constexpr int dt_size(int dt) { return dt == DT_E4M3 || dt == DT_I8 ? 1 : 2; }
+// Operand kind and format of tcgen05.mma, format of its accumulator (ptx::mma, make_idesc).
+constexpr int dt_kind(int dt) { return dt == DT_I8 ? 2 : dt == DT_E4M3 ? 1 : 0; }
+constexpr uint32_t dt_format(int dt) { return dt == DT_BF16 || dt == DT_I8 ? 1u : 0u; }
+constexpr uint32_t dt_acc_format(int dt) { return dt == DT_I8 ? 2u : 1u; }
 // Kernel epilogues (activation after alpha*A.B + bias).  A bias pointer of
 // NULL means no bias: the bias-free public epilogues run these same kernels.
 // EPI_DRELU is the ReLU backward: D = mask ? alpha*A.B : 0 with the mask read
@@ -119,6 +124,7 @@ struct TcParams {
     const void *residual;        // R, (m, n) in the output type, or NULL; may be D
     const float *scale_rows;     // m floats that take the place of *scale_a, or NULL
     int bias_row;                // the bias runs along the rows (length m)
+    const float *scale_cols;     // 8-bit integers: n floats, alpha_ij = scale_rows[i] * scale_cols[j]; else NULL
 };
 // Parameters of the kernels that add a residual: R's tensor map (boxes as D's) beside the rest.
 struct TcResParams : TcParams {
@@ -303,6 +309,18 @@ struct OutT<DT_BF16> {
 };
 template <>
 struct OutT<DT_E4M3> : OutT<DT_BF16> {};   // e4m3 operands -> bf16 bias and output
+template <>
+struct OutT<DT_I8> : OutT<DT_BF16> {};     // and so for 8-bit integers
+
+// The sum of two accumulators in their bits, fp32 or (I8) int32; and an accumulator as fp32.
+template <bool I8>
+__device__ __forceinline__ uint32_t acc_add(uint32_t a, float b) {
+    return I8 ? a + __float_as_uint(b) : __float_as_uint(__uint_as_float(a) + b);
+}
+template <bool I8>
+__device__ __forceinline__ float acc_f32(uint32_t a) {
+    return I8 ? __int2float_rn((int)a) : __uint_as_float(a);
+}
 
 // a / *scale, a > 0, as the factor of an e4m3 output; the largest fp32 number where the quotient is beyond it: what
 // is not 0 saturates all the same, and 0 stays 0.  (Not by fminf: a scale that is NaN has to show.)
@@ -438,9 +456,12 @@ struct TcCfg {
     static constexpr int DT = DT_, EPI = EPI_, AXIS = AXIS_, BN = BN_, CG = CG_, STAGES = STAGES_;
     static constexpr bool B_MN = B_MN_;             // B stored (k, n): N contiguous
     static constexpr bool A_MN = A_MN_;             // A stored (k, m): M contiguous
-    static constexpr int ESIZE = DT == DT_E4M3 ? 1 : 2;
-    static constexpr int KIND = DT == DT_E4M3 ? 1 : 0;
-    static constexpr uint32_t FMT = DT == DT_BF16 ? 1u : 0u;
+    // 8-bit integers: the accumulators, partial tiles among them, are int32 and exact, and become fp32 in the epilogue,
+    // where each meets its row's and its column's scale
+    static constexpr bool I8 = DT == DT_I8;
+    static constexpr int ESIZE = dt_size(DT);
+    static constexpr int KIND = dt_kind(DT);
+    static constexpr uint32_t FMT = dt_format(DT);
     static constexpr int BM = 128;                  // output rows per CTA
     static constexpr int BK = 128 / ESIZE;          // k per stage: one 128-byte swizzle row
     static constexpr int UMMA_K = 32 / ESIZE;       // k per tcgen05.mma
@@ -517,6 +538,7 @@ struct TcCfg {
     static_assert(!BWD || (EPI_WARPS == 4 && CPG == 4), "backward epilogue: one mask uint4 per chunk group");
     static_assert(!QOUT || (DT == DT_E4M3 && !BWD && EPI != EPI_RELU_AUX), "FP8 output: e4m3 forward plans");
     static_assert(!EXT || (FWD_BIAS && AXIS == AXIS_COL && !A_MN), "extended epilogue: forward kernels, A stored (m, k)");
+    static_assert(!I8 || RES, "8-bit integers: the extended epilogue, 16-bit outputs");
     static_assert(!A_MN || BM % A_BOX_M == 0, "MN-major A tile must be whole boxes");
     static_assert(EPI_WARPS * NCH_W * 2048 <= STAGES * (A_STAGE + B_STAGE),
                   "the last tile's output staging fits in the operand ring");
@@ -796,7 +818,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
         if (lane == 0 && leader) {
-            constexpr uint32_t idesc = make_idesc(C::FMT, C::A_MN, C::B_MN, 128 * C::CG, C::MMA_N);
+            constexpr uint32_t idesc = make_idesc(C::FMT, C::A_MN, C::B_MN, 128 * C::CG, C::MMA_N, dt_acc_format(C::DT));
             uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0, tr_i = 0;
             bool ok = true;
             // with inject_stall nothing is issued or committed: the epilogue's
@@ -1078,6 +1100,14 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     const int c = chunk_of<C>(ew, cl);         // chunk index within the tile
                     uint32_t(&v)[32] = vb[cc & 1];
                     uint4 rv[C::RES ? 4 : 1] = {};             // RES: this chunk's residual
+                    // I8: its columns' scales, one address for the whole warp, on their way while the chunk is
+                    float4 sc[C::I8 ? 8 : 1] = {};
+                    if constexpr (C::I8) if (!partial_out) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            if (n0 + 32 * c + 4 * i < p.n)
+                                sc[i] = __ldg(reinterpret_cast<const float4 *>(p.scale_cols + n0 + 32 * c) + i);
+                    }
                     ptx::tmem_wait_ld(v);                      // the only load in flight: this chunk's
                     if (cl + 1 < C::NCH_W) ptx::tmem_ld_32x32b_x32(tbase + chunk_of<C>(ew, cl + 1) * 32, vb[(cc + 1) & 1]);
                     // accumulator (or, SPLIT_HALVES, one half of it) fully read by this warp: hand
@@ -1107,10 +1137,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
                             const float4 f = __ldcg(src + 32 * j);
-                            v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
-                            v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
-                            v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
-                            v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
+                            v[4 * j] = acc_add<C::I8>(v[4 * j], f.x);
+                            v[4 * j + 1] = acc_add<C::I8>(v[4 * j + 1], f.y);
+                            v[4 * j + 2] = acc_add<C::I8>(v[4 * j + 2], f.z);
+                            v[4 * j + 3] = acc_add<C::I8>(v[4 * j + 3], f.w);
                         }
                     }
                     const int col0 = n0 + 32 * c;
@@ -1137,7 +1167,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
                     (void)mbits;
 #pragma unroll
                     for (int j = 0; j < 32; j += 2) {
-                        float x0 = __uint_as_float(v[j]), x1 = __uint_as_float(v[j + 1]);
+                        float x0 = acc_f32<C::I8>(v[j]), x1 = acc_f32<C::I8>(v[j + 1]);
+                        if constexpr (C::I8) {
+                            const float4 &f = sc[C::I8 ? j / 4 : 0];
+                            const float2 x = split(mul2(pair(x0, x1), j % 4 ? pair(f.z, f.w) : pair(f.x, f.y)));
+                            x0 = x.x;
+                            x1 = x.y;
+                        }
                         if constexpr (C::RES) {
                             const float2 b = O::unpack(word(cb, j));
                             const float2 x = split(fma2(pair(x0, x1), both(alpha), pair(b.x, b.y)));

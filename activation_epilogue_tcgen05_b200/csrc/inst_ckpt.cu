@@ -1,0 +1,64 @@
+// Launchers of the 8-bit checkpoints (ckpt.cuh) and of the epilogue's backward from them (dact.cuh).
+#include "ckpt.cuh"
+#include "dact.cuh"
+#include "kernels.h"
+
+namespace gemm_epi {
+
+namespace {
+template <int DT, int EPI>
+cudaError_t ckpt(bool save, const CkptParams &p, bool pdl, cudaStream_t s) {
+    static std::atomic<bool> attr_done[64];
+    const dim3 grid((p.total + CKPT_T / 4 * CKPT_U - 1) / (CKPT_T / 4 * CKPT_U));
+    return save ? launch_as(ckpt_save_kernel<DT, EPI>, attr_done, grid, CKPT_T, 0, pdl, s, p)
+                : launch_as(ckpt_load_kernel<DT, EPI>, attr_done, grid, CKPT_T, 0, pdl, s, p);
+}
+template <int DT>
+cudaError_t ckpt_of(bool save, int epi, const CkptParams &p, bool pdl, cudaStream_t s) {
+    switch (epi) {
+    case EPI_RELU: return ckpt<DT, EPI_RELU>(save, p, pdl, s);
+    case EPI_GELU: return ckpt<DT, EPI_GELU>(save, p, pdl, s);
+    case EPI_TANH: return ckpt<DT, EPI_TANH>(save, p, pdl, s);
+    default: return ckpt<DT, EPI_NONE>(save, p, pdl, s);
+    }
+}
+
+template <int DT, int ACT, bool VAL>
+cudaError_t dact_ckpt(int axis, const DactParams &p, bool pdl, cudaStream_t s) {
+    constexpr int SMEM = dact_smem(true), T = 32 * DACT_WARPS;
+    const dim3 grid((unsigned)((p.n + DACT_COLS - 1) / DACT_COLS), (unsigned)((p.m + p.rows - 1) / p.rows), 1);
+    if (axis == AXIS_ROW && p.dbias != nullptr) {
+        static std::atomic<bool> attr_done[64];
+        return launch_as(dact_rows_kernel<DT, ACT, true, VAL>, attr_done, dim3((unsigned)((p.m + DACT_U - 1) / DACT_U)), T, SMEM, pdl,
+                         s, p);
+    }
+    if (axis == AXIS_COL) {
+        static std::atomic<bool> attr_done[64];
+        return launch_as(dact_kernel<DT, ACT, AXIS_COL, true, VAL>, attr_done, grid, T, SMEM, pdl, s, p);
+    }
+    static std::atomic<bool> attr_done[64];
+    return launch_as(dact_kernel<DT, ACT, AXIS_ROW, true, VAL>, attr_done, grid, T, SMEM, pdl, s, p);
+}
+template <int DT, int ACT>
+cudaError_t dact_ckpt(int axis, const DactParams &p, bool pdl, cudaStream_t s) {
+    return p.h != nullptr ? dact_ckpt<DT, ACT, true>(axis, p, pdl, s) : dact_ckpt<DT, ACT, false>(axis, p, pdl, s);
+}
+template <int DT>
+cudaError_t dact_ckpt_of(int act, int axis, const DactParams &p, bool pdl, cudaStream_t s) {
+    switch (act) {
+    case DACT_RELU: return dact_ckpt<DT, DACT_RELU>(axis, p, pdl, s);
+    case DACT_GELU: return dact_ckpt<DT, DACT_GELU>(axis, p, pdl, s);
+    default: return dact_ckpt<DT, DACT_TANH>(axis, p, pdl, s);
+    }
+}
+}  // namespace
+
+cudaError_t launch_ckpt(int dt, bool save, int epi, const CkptParams &p, bool pdl, cudaStream_t s) {
+    return dt == DT_F16 ? ckpt_of<DT_F16>(save, epi, p, pdl, s) : ckpt_of<DT_BF16>(save, epi, p, pdl, s);
+}
+
+cudaError_t launch_dact_ckpt(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s) {
+    return dt == DT_F16 ? dact_ckpt_of<DT_F16>(act, axis, p, pdl, s) : dact_ckpt_of<DT_BF16>(act, axis, p, pdl, s);
+}
+
+}  // namespace gemm_epi

@@ -32,14 +32,14 @@ template <int DT, int ACT, int AXIS>
 cudaError_t dact(const DactParams &p, bool pdl, cudaStream_t s) {
     static std::atomic<bool> attr_done[64];
     const dim3 grid((unsigned)((p.n + DACT_COLS - 1) / DACT_COLS), (unsigned)((p.m + p.rows - 1) / p.rows), 1);
-    constexpr int SMEM = dact_reads_z(ACT) ? DACT_SMEM : 0;
+    constexpr int SMEM = dact_reads_z(ACT) ? dact_smem(false) : 0;
     return launch_as(dact_kernel<DT, ACT, AXIS>, attr_done, grid, 32 * DACT_WARPS, SMEM, pdl, s, p);
 }
 
 template <int DT, int ACT>
 cudaError_t dact_whole_rows(const DactParams &p, bool pdl, cudaStream_t s) {
     static std::atomic<bool> attr_done[64];
-    constexpr int SMEM = dact_reads_z(ACT) ? DACT_SMEM : 0;
+    constexpr int SMEM = dact_reads_z(ACT) ? dact_smem(false) : 0;
     return launch_as(dact_rows_kernel<DT, ACT>, attr_done, dim3((unsigned)((p.m + DACT_U - 1) / DACT_U)), 32 * DACT_WARPS, SMEM,
                      pdl, s, p);
 }

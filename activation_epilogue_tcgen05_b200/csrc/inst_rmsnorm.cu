@@ -37,6 +37,7 @@ cudaError_t fwd_out(int out, const NormParams &p, bool pdl, cudaStream_t s) {
     switch (out) {
     case NORM_SAME: return fwd_shape<DT, NORM_SAME>(p, pdl, s);
     case NORM_E4M3: return fwd_shape<DT, NORM_E4M3>(p, pdl, s);
+    case NORM_I8_ROWS: return fwd_shape<DT, NORM_I8_ROWS>(p, pdl, s);
     default: return fwd_shape<DT, NORM_E4M3_ROWS>(p, pdl, s);
     }
 }
@@ -147,18 +148,26 @@ cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStr
 
 namespace {
 template <int DT, int Y>
-cudaError_t add_parts(const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s) {
+cudaError_t add_parts(const float *src, int64_t parts, int64_t len, void *out, void *out2, int64_t cut, bool pdl, cudaStream_t s) {
     static std::atomic<bool> attr_done[64];
-    return launch_as(add_parts_kernel<DT, Y>, attr_done, dim3((unsigned)((len + 31) / 32)), 8 * Y, 0, pdl, s, src, parts, len, out);
+    return launch_as(add_parts_kernel<DT, Y>, attr_done, dim3((unsigned)((len + 31) / 32)), 8 * Y, 0, pdl, s, src, parts, len, out,
+                     out2, cut);
 }
 template <int DT>
-cudaError_t add_parts(const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s) {
-    return parts <= 320 ? add_parts<DT, 32>(src, parts, len, out, pdl, s) : add_parts<DT, 64>(src, parts, len, out, pdl, s);
+cudaError_t add_parts(const float *src, int64_t parts, int64_t len, void *out, void *out2, int64_t cut, bool pdl, cudaStream_t s) {
+    return parts <= 320 ? add_parts<DT, 32>(src, parts, len, out, out2, cut, pdl, s)
+                        : add_parts<DT, 64>(src, parts, len, out, out2, cut, pdl, s);
 }
 }  // namespace
 
 cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s) {
-    return dt == DT_F16 ? add_parts<DT_F16>(src, parts, len, out, pdl, s) : add_parts<DT_BF16>(src, parts, len, out, pdl, s);
+    return launch_add_parts2(dt, src, parts, len, out, nullptr, len, pdl, s);
+}
+
+cudaError_t launch_add_parts2(int dt, const float *src, int64_t parts, int64_t len, void *out, void *out2, int64_t cut, bool pdl,
+                              cudaStream_t s) {
+    return dt == DT_F16 ? add_parts<DT_F16>(src, parts, len, out, out2, cut, pdl, s)
+                        : add_parts<DT_BF16>(src, parts, len, out, out2, cut, pdl, s);
 }
 
 cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s) {

@@ -62,7 +62,7 @@ bool find_tc(int cg, int dt, int epi, int axis, bool b_mn, int bn, bool qout, bo
 bool find_sk(int dt, int epi, int axis, bool w_mn, int nm, bool qout, SkLauncher *launch, KernelInfo *info);
 bool find_sg(int dt, int epi, int axis, bool w_mn, int nm, bool qout, SgLauncher *launch, KernelInfo *info);
 bool find_bias_act(int dt, int epi, int axis, BiasActLauncher *launch);
-// The same kernels with the extended epilogue (residual, scales by row; the bias axis at run time).
+// The same kernels with the extended epilogue (residual, scales by row; the bias axis at run time), the only ones of 8-bit integers.
 bool find_tc_ext(int cg, int dt, int epi, bool b_mn, int bn, bool qout, TcLauncher *launch, KernelInfo *info);
 bool find_sk_ext(int dt, int epi, bool w_mn, int nm, bool qout, SkLauncher *launch, KernelInfo *info);
 
@@ -94,12 +94,26 @@ cudaError_t launch_rmsnorm(int dt, int out, const NormParams &p, bool pdl, cudaS
 cudaError_t launch_rmsnorm_bwd(int dt, const NormBwdParams &p, bool pdl, cudaStream_t s);
 // out[i] = sum_p src[p * len + i], fp32 partials, len a multiple of 8, out in dt
 cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t len, void *out, bool pdl, cudaStream_t s);
+// the same with two outputs: sums from `cut` on go to out2 (either may be NULL: not wanted)
+cudaError_t launch_add_parts2(int dt, const float *src, int64_t parts, int64_t len, void *out, void *out2, int64_t cut, bool pdl,
+                              cudaStream_t s);
 cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s);
 // rows of a block's run, from the sizes and whether z is read; the launch has ceil(m / rows) runs
 int64_t dact_rows(int64_t m, int64_t n, bool reads_z);
 // ROW axis: whether the launch writes dbias itself (DactParams::dbias), without partials
 bool dact_by_rows(int64_t m, int64_t n);
 cudaError_t launch_dact(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s);
+// The layer norm, the quantisation of rows (layernorm.cuh; NormParams' x, y and scale alone) and the 8-bit
+// checkpoints (ckpt.cuh).  ln_bwd_parts: as norm_bwd_parts, each part two rows (dgamma's and dbeta's).
+struct LnParams;
+struct LnBwdParams;
+struct CkptParams;
+int64_t ln_bwd_parts(int64_t m, int64_t d);
+cudaError_t launch_layernorm(int dt, int out, const LnParams &p, bool pdl, cudaStream_t s);
+cudaError_t launch_layernorm_bwd(int dt, const LnBwdParams &p, bool pdl, cudaStream_t s);
+cudaError_t launch_quant_rows(int dt, int out, const NormParams &p, bool pdl, cudaStream_t s);
+cudaError_t launch_ckpt(int dt, bool save, int epi, const CkptParams &p, bool pdl, cudaStream_t s);
+cudaError_t launch_dact_ckpt(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s);
 
 // per-dtype halves of the lookups (one instantiation unit each)
 bool find_tc_f16(int cg, int epi, int axis, bool b_mn, int bn, TcLauncher *, KernelInfo *);
@@ -121,6 +135,8 @@ bool find_tc_e4m3_ext(int cg, int epi, bool b_mn, int bn, TcLauncher *, KernelIn
 bool find_sk_e4m3_ext(int epi, bool w_mn, int nm, SkLauncher *, KernelInfo *);
 bool find_tc_e4m3q_ext(int cg, int epi, bool b_mn, int bn, TcLauncher *, KernelInfo *);
 bool find_sk_e4m3q_ext(int epi, bool w_mn, int nm, SkLauncher *, KernelInfo *);
+bool find_tc_i8_ext(int cg, int epi, bool b_mn, int bn, TcLauncher *, KernelInfo *);
+bool find_sk_i8_ext(int epi, bool w_mn, int nm, SkLauncher *, KernelInfo *);
 bool find_sg_f16(int epi, int axis, bool w_mn, int nm, SgLauncher *, KernelInfo *);
 bool find_sg_bf16(int epi, int axis, bool w_mn, int nm, SgLauncher *, KernelInfo *);
 bool find_sg_e4m3(int epi, int axis, bool w_mn, int nm, SgLauncher *, KernelInfo *);

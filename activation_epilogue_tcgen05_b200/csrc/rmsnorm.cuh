@@ -8,8 +8,9 @@
 //     y_j = s_j rho g_j
 // y goes out in the 16-bit type, or in e4m3 as y / scale: with a scale the caller gives for the
 // whole tensor (max |y| reported), or with one scale a row, max_j |y_j| / 448 (1 for a row of
-// zeros).  The row maximum needs no second pass: max |y| = rho max |s g|, so the sum of squares
-// and the maximum are reduced together, and e4m3(y / scale) = e4m3(s g * 448 / max |s g|).
+// zeros); or in 8-bit integers, with one scale a row, max_j |y_j| / 127.  The row maximum needs no second pass:
+// max |y| = rho max |s g|, so the sum of squares and the maximum are reduced together, and
+// e4m3(y / scale) = e4m3(s g * 448 / max |s g|).
 // The norm is taken of the unrounded fp32 sum: the only roundings are the ones of S and Y.
 //
 // Backward, from dY, the stored sum S, the gain g and the gradient dS that reaches s past the norm:
@@ -33,7 +34,10 @@
 
 namespace gemm_epi {
 
-enum : int { NORM_SAME = 0, NORM_E4M3 = 1, NORM_E4M3_ROWS = 2 };
+enum : int { NORM_SAME = 0, NORM_E4M3 = 1, NORM_E4M3_ROWS = 2, NORM_I8_ROWS = 4 };
+constexpr bool norm_by_rows(int out) { return out == NORM_E4M3_ROWS || out == NORM_I8_ROWS; }
+// The largest code of an output with one scale a row.
+constexpr float norm_top_code(int out) { return out == NORM_I8_ROWS ? 127.0f : 448.0f; }
 
 struct NormParams {
     int64_t m;
@@ -61,6 +65,25 @@ template <int DT>
 __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     using O = OutT<DT>;
     return make_uint4(O::pack(f[0], f[1]), O::pack(f[2], f[3]), O::pack(f[4], f[5]), O::pack(f[6], f[7]));
+}
+
+// Eight values times mul as 8-bit codes of the output type.  Integers (|v mul| within half of 127): 1.5 * 2^23 is added, which
+// leaves the nearest integer, ties to even, in the sum's low byte; one rounding, of the product.
+template <int OUT>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float mul) {
+    if constexpr (OUT == NORM_I8_ROWS) {
+        uint32_t b[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(fmaf(v[e], mul, 12582912.0f));
+        return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
+                          __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+    } else {
+        uint32_t w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            w[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e] * mul, v[2 * e + 1] * mul), __NV_SATFINITE, __NV_E4M3);
+        return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+    }
 }
 
 // Sum of `a` and combination of `b` (maximum, or sum) over the TPR threads of a row, the same
@@ -161,11 +184,12 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
             const unsigned int a = __reduce_max_sync(0xffffffffu, __float_as_uint(rho * top));
             if ((threadIdx.x & 31) == 0 && a > *reinterpret_cast<volatile unsigned int *>(p.amax)) atomicMax(p.amax, a);
         }
-    } else if constexpr (OUT == NORM_E4M3_ROWS) {
-        // 448 / top overflows below 1.4e-36; such a row is one of zeros in e4m3 at any scale in use
+    } else if constexpr (norm_by_rows(OUT)) {
+        // 448 / top overflows below 1.4e-36; such a row is one of zeros in 8 bits at any scale in use
+        constexpr float C = norm_top_code(OUT);
         const bool zero = !(top > 1e-35f);
-        mul = zero ? rho : 448.0f / top;
-        if (t == 0 && row_ok) p.scale[row] = zero ? 1.0f : rho * top * (1.0f / 448.0f);
+        mul = zero ? (OUT == NORM_I8_ROWS ? 0.0f : rho) : C / top;
+        if (t == 0 && row_ok) p.scale[row] = zero ? 1.0f : rho * top * (1.0f / C);
     }
     if (!row_ok) return;
 #pragma unroll
@@ -179,13 +203,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
             for (int e = 0; e < 8; ++e) s[j][e] = s[j][e] * mul * g[e];
             *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.y) + base + 8 * v) = pack8<DT>(s[j]);
         } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                w[e] = __nv_cvt_float2_to_fp8x2(make_float2(s[j][2 * e] * mul, s[j][2 * e + 1] * mul), __NV_SATFINITE,
-                                                __NV_E4M3);
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + base + 8 * v) =
-                make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.y) + base + 8 * v) = codes8<OUT>(s[j], mul);
         }
     }
 }
@@ -377,13 +395,14 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
     }
 }
 
-// out[i] = sum_p src[p * len + i] over fp32 partials, len a multiple of 8.  A block takes 32 outputs:
+// out[i] = sum_p src[p * len + i] over fp32 partials, len a multiple of 8; from i = cut on (a multiple of 4) the sums go to
+// out2[i - cut], and to neither array where its pointer is NULL.  A block takes 32 outputs:
 // thread (x, y) adds parts y, y + Y, ... of four neighbouring outputs, ten loads in flight (it is
 // latency that counts here: all of a thread's loads should go out at once), then the Y sums are added in
 // a fixed tree; the order depends on (parts, len) alone.
 template <int DT, int Y>
 __global__ void __launch_bounds__(8 * Y) add_parts_kernel(const float *__restrict__ src, int64_t parts, int64_t len,
-                                                          void *out) {
+                                                          void *out, void *out2, int64_t cut) {
     constexpr int U = 10;
     __shared__ float4 red[Y][8];
     const int x = threadIdx.x & 7, y = threadIdx.x >> 3;
@@ -430,8 +449,9 @@ __global__ void __launch_bounds__(8 * Y) add_parts_kernel(const float *__restric
             s.w += __shfl_xor_sync(0xffffffffu, s.w, sh);
         }
         const int64_t o = (int64_t)blockIdx.x * 32 + 4 * q;
-        if (l == 0 && o < len)
-            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(out) + o) =
+        uint16_t *to = o < cut ? static_cast<uint16_t *>(out) : static_cast<uint16_t *>(out2);
+        if (l == 0 && o < len && to != nullptr)
+            *reinterpret_cast<uint2 *>(to + (o < cut ? o : o - cut)) =
                 make_uint2(OutT<DT>::pack(s.x, s.y), OutT<DT>::pack(s.z, s.w));
     }
 }

@@ -19,7 +19,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgemm_epi.so")
 
 # enums (include/gemm_epi.h)
-F16, BF16, E4M3 = 0, 1, 2
+F16, BF16, E4M3, I8 = 0, 1, 2, 4
+I8_MAX_K = 131071
 NONE, BIAS, RELU_BIAS, RELU_AUX_BIAS, GELU_BIAS = 0, 1, 2, 3, 4
 TANH_BIAS, RELU, RELU_AUX, GELU, TANH = 5, 6, 7, 8, 9
 DRELU, DRELU_BGRAD = 10, 11
@@ -30,7 +31,7 @@ KERNEL_AUTO, KERNEL_TC1, KERNEL_TC2, KERNEL_SPLITK = 0, 1, 2, 3
 OK, ERR_ARG, ERR_ALIGN, ERR_NULL, ERR_UNSUPPORTED, ERR_CUDA, ERR_TIMEOUT, ERR_NO_DEVICE = \
     0, -1, -2, -3, -4, -5, -6, -7
 
-DTYPE = {"f16": F16, "bf16": BF16, "e4m3": E4M3}
+DTYPE = {"f16": F16, "bf16": BF16, "e4m3": E4M3, "i8": I8}
 EPILOGUE = {"none": NONE, "bias": BIAS, "relu_bias": RELU_BIAS, "relu_aux_bias": RELU_AUX_BIAS,
             "gelu_bias": GELU_BIAS, "tanh_bias": TANH_BIAS, "relu": RELU, "relu_aux": RELU_AUX,
             "gelu": GELU, "tanh": TANH, "drelu": DRELU, "drelu_bgrad": DRELU_BGRAD}
@@ -41,8 +42,9 @@ AXIS = {"row": BIAS_ROW, "col": BIAS_COL}
 LAYOUT = {"kn": B_KN, "nk": B_NK}
 KERNEL = {"auto": KERNEL_AUTO, "tc1": KERNEL_TC1, "tc2": KERNEL_TC2, "splitk": KERNEL_SPLITK}
 STREAM_K = {"auto": 0, "off": 1, "on": 2}
-NORM_SAME, NORM_E4M3, NORM_E4M3_ROWS = 0, 1, 2
-NORM_OUT = {"same": NORM_SAME, "e4m3": NORM_E4M3, "e4m3_rows": NORM_E4M3_ROWS}
+NORM_SAME, NORM_E4M3, NORM_E4M3_ROWS, NORM_I8_ROWS = 0, 1, 2, 4
+NORM_OUT = {"same": NORM_SAME, "e4m3": NORM_E4M3, "e4m3_rows": NORM_E4M3_ROWS, "i8_rows": NORM_I8_ROWS}
+CKPT_GROUP = 32   # columns of a checkpoint that share an exponent
 
 # every symbol include/gemm_epi.h declares
 EXPORTS = ("gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts", "gemm_epi_set_scales",
@@ -53,7 +55,9 @@ EXPORTS = ("gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts", "gemm_epi_
            "gemm_epi_mlp_check", "gemm_epi_mlp_query", "gemm_epi_mlp_free", "gemm_epi_mlp_unfused_run",
            "gemm_epi_plan_preview", "gemm_epi_rmsnorm", "gemm_epi_rmsnorm_workspace_bytes",
            "gemm_epi_rmsnorm_bwd", "gemm_epi_dact_workspace_bytes", "gemm_epi_dact", "gemm_epi_run_ext",
-           "gemm_epi_mlp_run_prenorm")
+           "gemm_epi_mlp_run_prenorm", "gemm_epi_run_scaled", "gemm_epi_layernorm", "gemm_epi_layernorm_workspace_bytes",
+           "gemm_epi_layernorm_bwd", "gemm_epi_quant_rows", "gemm_epi_ckpt_groups", "gemm_epi_ckpt_save", "gemm_epi_ckpt_load",
+           "gemm_epi_dact_ckpt")
 
 
 class Options(ctypes.Structure):
@@ -134,7 +138,20 @@ def lib():
             L.gemm_epi_dact_workspace_bytes.restype = i64
             L.gemm_epi_run_ext.argtypes = [vp] * 9
             L.gemm_epi_mlp_run_prenorm.argtypes = [vp, vp, vp, vp, ctypes.c_float] + [vp] * 10
-            for name in ("gemm_epi_run_ext", "gemm_epi_mlp_run_prenorm", "gemm_epi_rmsnorm", "gemm_epi_rmsnorm_bwd", "gemm_epi_dact",
+            f32 = ctypes.c_float
+            L.gemm_epi_run_scaled.argtypes = [vp] * 10
+            L.gemm_epi_layernorm.argtypes = [i64, i64, i32, i32, f32] + [vp] * 9
+            L.gemm_epi_layernorm_workspace_bytes.argtypes = [i64, i64]
+            L.gemm_epi_layernorm_workspace_bytes.restype = i64
+            L.gemm_epi_layernorm_bwd.argtypes = [i64, i64, i32, f32] + [vp] * 9
+            L.gemm_epi_quant_rows.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp]
+            L.gemm_epi_ckpt_groups.argtypes = [i64]
+            L.gemm_epi_ckpt_groups.restype = i64
+            L.gemm_epi_ckpt_save.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp, vp]
+            L.gemm_epi_ckpt_load.argtypes = [i64, i64, i32, i32, vp, vp, vp, vp]
+            L.gemm_epi_dact_ckpt.argtypes = [i64, i64, i32, i32, i32] + [vp] * 8
+            for name in ("gemm_epi_run_scaled", "gemm_epi_layernorm", "gemm_epi_layernorm_bwd", "gemm_epi_quant_rows", "gemm_epi_ckpt_save",
+                         "gemm_epi_ckpt_load", "gemm_epi_dact_ckpt", "gemm_epi_run_ext", "gemm_epi_mlp_run_prenorm", "gemm_epi_rmsnorm", "gemm_epi_rmsnorm_bwd", "gemm_epi_dact",
                          "gemm_epi_plan", "gemm_epi_plan_ex", "gemm_epi_plan_opts",
                          "gemm_epi_set_scales", "gemm_epi_run", "gemm_epi_unfused_run",
                          "gemm_epi_check", "gemm_epi_plan_query", "gemm_epi_free",
@@ -179,6 +196,10 @@ def gemm_epi_run(plan, A, B, bias, D, aux, stream) -> None:
 
 def gemm_epi_run_ext(plan, A, B, bias, R, d_scale_rows, D, aux, stream) -> None:
     _check(lib().gemm_epi_run_ext(plan, A, B, bias, R, d_scale_rows, D, aux, stream), "gemm_epi_run_ext")
+
+
+def gemm_epi_run_scaled(plan, A, B, bias, R, d_scale_rows, d_scale_cols, D, aux, stream) -> None:
+    _check(lib().gemm_epi_run_scaled(plan, A, B, bias, R, d_scale_rows, d_scale_cols, D, aux, stream), "gemm_epi_run_scaled")
 
 
 def gemm_epi_unfused_run(plan, A, B, bias, D, aux, stream) -> None:
@@ -306,6 +327,41 @@ def gemm_epi_rmsnorm_bwd(m, d, dtype, eps, dY, S, gamma, dS, dX, dgamma, workspa
            "gemm_epi_rmsnorm_bwd")
 
 
+def gemm_epi_layernorm(m, d, dtype, out_mode, eps, X, R, gamma, beta, S, Y, d_scale, d_amax, stream) -> None:
+    _check(lib().gemm_epi_layernorm(m, d, dtype, out_mode, eps, X, R, gamma, beta, S, Y, d_scale, d_amax, stream),
+           "gemm_epi_layernorm")
+
+
+def gemm_epi_layernorm_workspace_bytes(m: int, d: int) -> int:
+    return lib().gemm_epi_layernorm_workspace_bytes(m, d)
+
+
+def gemm_epi_layernorm_bwd(m, d, dtype, eps, dY, S, gamma, dS, dX, dgamma, dbeta, workspace, stream) -> None:
+    _check(lib().gemm_epi_layernorm_bwd(m, d, dtype, eps, dY, S, gamma, dS, dX, dgamma, dbeta, workspace, stream),
+           "gemm_epi_layernorm_bwd")
+
+
+def gemm_epi_quant_rows(m, d, dtype, out_mode, X, Q, d_scale, stream) -> None:
+    _check(lib().gemm_epi_quant_rows(m, d, dtype, out_mode, X, Q, d_scale, stream), "gemm_epi_quant_rows")
+
+
+def gemm_epi_ckpt_groups(n: int) -> int:
+    return lib().gemm_epi_ckpt_groups(n)
+
+
+def gemm_epi_ckpt_save(m, n, dtype, epilogue, Z, H, codes, exps, stream) -> None:
+    _check(lib().gemm_epi_ckpt_save(m, n, dtype, epilogue, Z, H, codes, exps, stream), "gemm_epi_ckpt_save")
+
+
+def gemm_epi_ckpt_load(m, n, dtype, epilogue, codes, exps, X, stream) -> None:
+    _check(lib().gemm_epi_ckpt_load(m, n, dtype, epilogue, codes, exps, X, stream), "gemm_epi_ckpt_load")
+
+
+def gemm_epi_dact_ckpt(m, n, dtype, epilogue, bias_axis, dD, codes, exps, dZ, H, dbias, workspace, stream) -> None:
+    _check(lib().gemm_epi_dact_ckpt(m, n, dtype, epilogue, bias_axis, dD, codes, exps, dZ, H, dbias, workspace, stream),
+           "gemm_epi_dact_ckpt")
+
+
 def gemm_epi_dact_workspace_bytes(m: int, n: int, bias_axis: int) -> int:
     return lib().gemm_epi_dact_workspace_bytes(m, n, bias_axis)
 
@@ -351,7 +407,7 @@ class Plan:
         self.handle = gemm_epi_plan_opts(self.m, self.n, self.k, DTYPE[dtype], EPILOGUE[epilogue],
                                          AXIS[bias_axis], layout, opts)
         self.out_e4m3 = bool(out_e4m3)
-        self._scales = self._ext = None
+        self._scales = self._ext = self._i8 = None
 
     @property
     def info(self) -> dict:
@@ -386,12 +442,29 @@ class Plan:
                          _operand(D, "Plan.run_ext: D", out, d, dev),
                          None if mask is None else _operand(aux, "Plan.run_ext: aux", i32, mask, dev), s)
 
+    def run_i8(self, A, B, bias, D, scale_rows, scale_cols, residual=None, aux=None, stream=None):
+        """dtype "i8": D = act(scale_rows_i * scale_cols_j * (A.B)_ij + bias) + residual; ``scale_rows``: m fp32 values,
+        ``scale_cols``: n of them (see gemm_epi_run_scaled in include/gemm_epi.h).  ``residual`` may be D."""
+        dev, s = _device_and_stream(stream)
+        if self._i8 is None:
+            if self.dtype != "i8":
+                raise GemmEpiError(ERR_ARG, f"Plan.run_i8: a plan of {self.dtype!r}")
+            self._i8 = self._ext_operands() + ((self.n,),)
+        t, a, b, wide, bias_of, out, d, f32, rows, i32, mask, cols = self._i8
+        gemm_epi_run_scaled(self.handle, _operand(A, "Plan.run_i8: A", t, a, dev), _operand(B, "Plan.run_i8: B", t, b, dev),
+                        None if bias_of is None else _operand(bias, "Plan.run_i8: bias", wide, bias_of, dev),
+                        None if residual is None else _operand(residual, "Plan.run_i8: residual", wide, d, dev),
+                        _operand(scale_rows, "Plan.run_i8: scale_rows", f32, rows, dev),
+                        _operand(scale_cols, "Plan.run_i8: scale_cols", f32, cols, dev),
+                        _operand(D, "Plan.run_i8: D", out, d, dev),
+                        None if mask is None else _operand(aux, "Plan.run_i8: aux", i32, mask, dev), s)
+
     def _ext_operands(self):
         """Types and shapes of run_ext's operands: of A and B, of the bias (None without one) and the residual, of D,
         of the row scales, of the mask (None without one)."""
         import torch
-        t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn}[self.dtype]
-        wide = torch.bfloat16 if self.dtype == "e4m3" else t
+        t = {"f16": torch.float16, "bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "i8": torch.int8}[self.dtype]
+        wide = torch.bfloat16 if self.dtype in ("e4m3", "i8") else t
         m, n, k = self.m, self.n, self.k
         return (t, (k, m) if self.a_layout == "km" else (m, k), (n, k) if self.b_layout == "nk" else (k, n),
                 wide, (m if self.bias_axis == "row" else n,) if self.epilogue in HAS_BIAS else None,
@@ -559,22 +632,29 @@ def _scratch(nbytes, device, stream):
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
 
 
-class RmsNorm:
-    """Root-mean-square norm of (m, d) rows with the residual's addition before it, and its backward
-    (gemm_epi_rmsnorm, gemm_epi_rmsnorm_bwd).  ``dtype``: "f16" or "bf16"; ``out``: "same", "e4m3" (a given
-    scale) or "e4m3_rows" (one scale a row, written).  The object holds sizes only."""
+class _Norm:
+    """Sizes and types of a norm's operands."""
 
     def __init__(self, m, d, dtype="bf16", out="same", eps=1e-6):
         import torch
         self.m, self.d, self.dtype, self.out, self.eps = int(m), int(d), dtype, out, float(eps)
         if dtype not in ("f16", "bf16"):
-            raise GemmEpiError(ERR_ARG, f"RmsNorm: dtype {dtype!r}")
+            raise GemmEpiError(ERR_ARG, f"{type(self).__name__}: dtype {dtype!r}")
         self._t = torch.float16 if dtype == "f16" else torch.bfloat16
         self._dt, self._mode = DTYPE[dtype], NORM_OUT[out]
-        self._out_t = self._t if out == "same" else torch.float8_e4m3fn
+        self._out_t = self._t if out == "same" else torch.int8 if out == "i8_rows" else torch.float8_e4m3fn
         self._f32 = torch.float32
         self._shape, self._row, self._one = (self.m, self.d), (self.d,), (1,)
-        self._scales = (self.m,) if out == "e4m3_rows" else (1,)
+        self._scales = (self.m,) if out in ("e4m3_rows", "i8_rows") else (1,)
+
+
+class RmsNorm(_Norm):
+    """Root-mean-square norm of (m, d) rows with the residual's addition before it, and its backward
+    (gemm_epi_rmsnorm, gemm_epi_rmsnorm_bwd).  ``dtype``: "f16" or "bf16"; ``out``: "same", "e4m3" (a given
+    scale), "e4m3_rows" or "i8_rows" (one scale a row, written).  The object holds sizes only."""
+
+    def __init__(self, m, d, dtype="bf16", out="same", eps=1e-6):
+        super().__init__(m, d, dtype, out, eps)
         self._scratch_bytes = gemm_epi_rmsnorm_workspace_bytes(self.m, self.d)
 
     def run(self, X, gamma, Y, residual=None, S=None, scale=None, amax=None, stream=None):
@@ -609,8 +689,101 @@ class RmsNorm:
                              None if workspace is None else workspace.data_ptr(), s)
 
 
+class LayerNorm(_Norm):
+    """Layer norm of (m, d) rows with the residual's addition before it, and its backward (gemm_epi_layernorm,
+    gemm_epi_layernorm_bwd).  Arguments as for :class:`RmsNorm`.  The object holds sizes only."""
+
+    def __init__(self, m, d, dtype="bf16", out="same", eps=1e-5):
+        super().__init__(m, d, dtype, out, eps)
+        self._scratch_bytes = gemm_epi_layernorm_workspace_bytes(self.m, self.d)
+
+    def run(self, X, gamma, Y, beta=None, residual=None, S=None, scale=None, amax=None, stream=None):
+        """S = X + residual (X without one), Y = (S - mean) / deviation * gamma + beta; ``scale`` and ``amax`` as in
+        include/gemm_epi.h.  S or Y may be X or residual."""
+        dev, s = _device_and_stream(stream)
+        shape, t = self._shape, self._t
+        gemm_epi_layernorm(self.m, self.d, self._dt, self._mode, self.eps, _operand(X, "LayerNorm.run: X", t, shape, dev),
+                           _operand(residual, "LayerNorm.run: residual", t, shape, dev, True),
+                           _operand(gamma, "LayerNorm.run: gamma", t, self._row, dev),
+                           _operand(beta, "LayerNorm.run: beta", t, self._row, dev, True),
+                           _operand(S, "LayerNorm.run: S", t, shape, dev, True),
+                           _operand(Y, "LayerNorm.run: Y", self._out_t, shape, dev),
+                           _operand(scale, "LayerNorm.run: scale", self._f32, self._scales, dev, True),
+                           _operand(amax, "LayerNorm.run: amax", self._f32, self._one, dev, True), s)
+
+    def run_bwd(self, dY, S, gamma, dX, dgamma=None, dbeta=None, dS=None, workspace=None, stream=None):
+        """dX (of X and of the residual alike) and, if given, dgamma and dbeta, from the sum S of the forward run (X
+        without a residual); dS: the skip connection's gradient.  ``workspace``: a uint8 tensor of
+        gemm_epi_layernorm_workspace_bytes(m, d) bytes, taken from torch's allocator when left out."""
+        dev, s = _device_and_stream(stream)
+        shape, t = self._shape, self._t
+        if (dgamma is None and dbeta is None) or not self._scratch_bytes:
+            workspace = None
+        else:
+            workspace = _workspace(workspace, self._scratch_bytes, "LayerNorm.run_bwd", dev, stream)
+        gemm_epi_layernorm_bwd(self.m, self.d, self._dt, self.eps, _operand(dY, "LayerNorm.run_bwd: dY", t, shape, dev),
+                               _operand(S, "LayerNorm.run_bwd: S", t, shape, dev),
+                               _operand(gamma, "LayerNorm.run_bwd: gamma", t, self._row, dev),
+                               _operand(dS, "LayerNorm.run_bwd: dS", t, shape, dev, True),
+                               _operand(dX, "LayerNorm.run_bwd: dX", t, shape, dev),
+                               _operand(dgamma, "LayerNorm.run_bwd: dgamma", t, self._row, dev, True),
+                               _operand(dbeta, "LayerNorm.run_bwd: dbeta", t, self._row, dev, True),
+                               None if workspace is None else workspace.data_ptr(), s)
+
+
+class QuantRows:
+    """(m, d) rows quantised with one scale each (gemm_epi_quant_rows): ``out`` "i8_rows" or "e4m3_rows".  The object holds
+    sizes only."""
+
+    def __init__(self, m, d, dtype="bf16", out="i8_rows"):
+        import torch
+        self.m, self.d, self.dtype, self.out = int(m), int(d), dtype, out
+        if dtype not in ("f16", "bf16") or out not in ("i8_rows", "e4m3_rows"):
+            raise GemmEpiError(ERR_ARG, f"QuantRows: dtype {dtype!r}, out {out!r}")
+        self._t, self._f32 = torch.float16 if dtype == "f16" else torch.bfloat16, torch.float32
+        self._out_t = torch.int8 if out == "i8_rows" else torch.float8_e4m3fn
+        self._dt, self._mode, self._shape, self._scales = DTYPE[dtype], NORM_OUT[out], (self.m, self.d), (self.m,)
+
+    def run(self, X, Q, scale, stream=None):
+        """Q = the codes of X / scale, scale: m fp32 values, written."""
+        dev, s = _device_and_stream(stream)
+        gemm_epi_quant_rows(self.m, self.d, self._dt, self._mode, _operand(X, "QuantRows.run: X", self._t, self._shape, dev),
+                            _operand(Q, "QuantRows.run: Q", self._out_t, self._shape, dev),
+                            _operand(scale, "QuantRows.run: scale", self._f32, self._scales, dev), s)
+
+
+class ActCheckpoint:
+    """Checkpoints of an (m, n) pre-activation in 8 bits (gemm_epi_ckpt_save, gemm_epi_ckpt_load): ``codes`` (m, n) int8 and
+    ``exps`` (m, groups) uint8, ``groups`` of 32 columns each.  ``dtype`` and ``epilogue`` are the forward plan's.  The object
+    holds sizes only."""
+
+    def __init__(self, m, n, dtype="bf16", epilogue="gelu_bias"):
+        import torch
+        self.m, self.n, self.dtype, self.epilogue = int(m), int(n), dtype, epilogue
+        self.groups = gemm_epi_ckpt_groups(self.n)
+        self._dt, self._epi = DTYPE[dtype], EPILOGUE[epilogue]
+        self._t, self._i8, self._u8 = torch.float16 if dtype == "f16" else torch.bfloat16, torch.int8, torch.uint8
+        self._shape, self._exps = (self.m, self.n), (self.m, self.groups)
+
+    def save(self, Z, codes, exps, H=None, stream=None):
+        """Z kept as codes and exps; H = act(Z), if given (H may be Z)."""
+        dev, s = _device_and_stream(stream)
+        gemm_epi_ckpt_save(self.m, self.n, self._dt, self._epi, _operand(Z, "ActCheckpoint.save: Z", self._t, self._shape, dev),
+                           _operand(H, "ActCheckpoint.save: H", self._t, self._shape, dev, True),
+                           _operand(codes, "ActCheckpoint.save: codes", self._i8, self._shape, dev),
+                           _operand(exps, "ActCheckpoint.save: exps", self._u8, self._exps, dev), s)
+
+    def load(self, codes, exps, X, act=False, stream=None):
+        """X = z as kept, or (``act``) act(z)."""
+        dev, s = _device_and_stream(stream)
+        gemm_epi_ckpt_load(self.m, self.n, self._dt, self._epi if act else NONE,
+                           _operand(codes, "ActCheckpoint.load: codes", self._i8, self._shape, dev),
+                           _operand(exps, "ActCheckpoint.load: exps", self._u8, self._exps, dev),
+                           _operand(X, "ActCheckpoint.load: X", self._t, self._shape, dev), s)
+
+
 class ActBackward:
-    """Backward of a forward plan's epilogue (gemm_epi_dact): dZ = dD * act'(z) and dbias, the names as
+    """Backward of a forward plan's epilogue (gemm_epi_dact, gemm_epi_dact_ckpt): dZ = dD * act'(z) and dbias, the names as
     for :class:`Plan`.  The object holds sizes only."""
 
     def __init__(self, m, n, dtype="bf16", epilogue="bias", bias_axis="row"):
@@ -621,6 +794,7 @@ class ActBackward:
         self._i32 = torch.int32
         self._shape, self._len = (self.m, self.n), (self.m if bias_axis == "row" else self.n,)
         self._aux_words = (self.m, aux_pitch_words(self.n))
+        self._i8, self._u8, self._exps = torch.int8, torch.uint8, (self.m, gemm_epi_ckpt_groups(self.n))
         self._scratch_bytes = gemm_epi_dact_workspace_bytes(self.m, self.n, AXIS[bias_axis])
 
     def run(self, dD, dZ=None, z=None, aux=None, dbias=None, workspace=None, stream=None):
@@ -639,6 +813,23 @@ class ActBackward:
                       _operand(dZ, "ActBackward.run: dZ", t, shape, dev, True),
                       _operand(dbias, "ActBackward.run: dbias", t, self._len, dev, True),
                       None if workspace is None else workspace.data_ptr(), s)
+
+    def run_ckpt(self, dD, codes, exps, dZ, H=None, dbias=None, workspace=None, stream=None):
+        """The same from z's checkpoint (:class:`ActCheckpoint`): dZ = dD * act'(z), dbias and, if given, H = act(z), with
+        z as kept (relu, gelu and tanh epilogues without a mask)."""
+        dev, s = _device_and_stream(stream)
+        shape, t = self._shape, self._t
+        if dbias is None or not self._scratch_bytes:
+            workspace = None
+        else:
+            workspace = _workspace(workspace, self._scratch_bytes, "ActBackward.run_ckpt", dev, stream)
+        gemm_epi_dact_ckpt(self.m, self.n, *self._args, _operand(dD, "ActBackward.run_ckpt: dD", t, shape, dev),
+                           _operand(codes, "ActBackward.run_ckpt: codes", self._i8, shape, dev),
+                           _operand(exps, "ActBackward.run_ckpt: exps", self._u8, self._exps, dev),
+                           _operand(dZ, "ActBackward.run_ckpt: dZ", t, shape, dev),
+                           _operand(H, "ActBackward.run_ckpt: H", t, shape, dev, True),
+                           _operand(dbias, "ActBackward.run_ckpt: dbias", t, self._len, dev, True),
+                           None if workspace is None else workspace.data_ptr(), s)
 
 
 def _workspace(given, nbytes, what, device, stream):

@@ -24,11 +24,12 @@
  *   - Accumulation and all epilogue arithmetic are fp32; D is rounded to
  *     nearest even.  fp16 inputs give fp16 bias and D; bf16 gives bf16; e4m3
  *     inputs give bf16 bias and D ([nvmath-fusion] paragraph 5: input, weight
- *     and bias types agree; FP8 keeps a 16-bit output).
+ *     and bias types agree; FP8 keeps a 16-bit output), and so do 8-bit integers,
+ *     whose products are summed in int32.
  *   - Every pointer passed to run() is a DEVICE pointer into memory of the
  *     current CUDA device, owned by the caller, 16-byte aligned ([epilog-params]
  *     body paragraph 3).  Row pitches k*esize and n*esize must be multiples of
- *     16 bytes: k and n multiples of 8 for 16-bit types, of 16 for e4m3.
+ *     16 bytes: k and n multiples of 8 for 16-bit types, of 16 for e4m3 and 8-bit integers.
  *   - Calls are asynchronous on the given stream (a cudaStream_t passed as
  *     void*, NULL = legacy default stream) and never synchronise.
  *   - The GEMM kernels are launched with programmatic stream serialisation:
@@ -49,8 +50,17 @@ extern "C" {
 
 /* ---- enumerations -------------------------------------------------------- */
 
-/* Operand types ([nvmath-fusion] paragraph 5: FP16, BF16, FP8). */
-enum gemm_epi_dtype { GEMM_EPI_F16 = 0, GEMM_EPI_BF16 = 1, GEMM_EPI_E4M3 = 2 };
+/* Operand types ([nvmath-fusion] paragraph 5: FP16, BF16, FP8; the pages have no 8-bit integers). */
+enum gemm_epi_dtype {
+    GEMM_EPI_F16 = 0,
+    GEMM_EPI_BF16 = 1,
+    GEMM_EPI_E4M3 = 2,
+    GEMM_EPI_I8 = 4      /* signed 8-bit integers with a scale for each row of A and each column of B: plans run by
+                            gemm_epi_run_scaled (3 is no type) */
+};
+
+/* The largest k of a GEMM_EPI_I8 plan: k products of two codes of -128 ... 127 fit an int32. */
+#define GEMM_EPI_I8_MAX_K 131071
 
 /* Epilogues ([epilog-params] body paragraph 2; [bias-fusion] paragraph 2 for GELU;
  * [nvmath-fusion] paragraph 6 lists Tanh among the predefined ones).  x = alpha*A.B + bias
@@ -260,6 +270,22 @@ int gemm_epi_run(gemm_epi_plan_t plan, const void *A, const void *B, const void 
 int gemm_epi_run_ext(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, const void *R,
                      const float *d_scale_rows, void *D, uint32_t *aux, void *stream);
 
+/* The product of 8-bit integers with a scale for each token and channel, on a GEMM_EPI_I8 plan:
+ *     D = act(s_i t_j (A . B)_ij + bias) + R
+ *   A, B    int8 codes, -128 ... 127, laid out as ever.  Their products are summed in int32, exactly (k is at most
+ *           GEMM_EPI_I8_MAX_K; ERR_UNSUPPORTED beyond), and a sum becomes fp32 once, in the epilogue.
+ *   d_scale_rows  s: DEVICE pointer to m floats, 4-byte aligned: one scale a row of A, as gemm_epi_quant_rows and the
+ *           norms' GEMM_EPI_NORM_I8_ROWS write them.
+ *   d_scale_cols  t: DEVICE pointer to n floats, 16-byte aligned: one scale a column of B (an output channel; for an
+ *           nn.Linear weight, (n, k), what gemm_epi_quant_rows writes for its rows).
+ *   bias, R, D  bf16; bias and aux as for gemm_epi_run, R as for gemm_epi_run_ext (NULL: none; may be D).
+ * Plans: forward epilogues (NONE ... TANH), A stored (m, k), D in bf16, block_n 0, 128 or 256, and the kernel families of other
+ * plans (GEMM_EPI_SK_GRID is not read); ERR_UNSUPPORTED otherwise.  The other run calls, gemm_epi_set_scales and
+ * gemm_epi_run_noalloc do not take such a plan (ERR_ARG), nor is there an MLP block of them (ERR_UNSUPPORTED).  Rules and
+ * statuses as for gemm_epi_run_ext; ERR_NULL without either scale, ERR_ARG for a plan of another type. */
+int gemm_epi_run_scaled(gemm_epi_plan_t plan, const void *A, const void *B, const void *bias, const void *R,
+                    const float *d_scale_rows, const float *d_scale_cols, void *D, uint32_t *aux, void *stream);
+
 /* The library's own UNFUSED baseline on the same plan and arguments: the bare
  * GEMM (epilogue NONE) writes alpha*A.B to D in the output type, then a
  * separate elementwise kernel reads D back, adds the bias, applies the
@@ -427,14 +453,17 @@ enum gemm_epi_norm_out {
     GEMM_EPI_NORM_SAME = 0,       /* y in the type of X                                             */
     GEMM_EPI_NORM_E4M3 = 1,       /* e4m3(y / *d_scale): one scale the caller gives, as A's of a
                                      plan (gemm_epi_set_scales)                                     */
-    GEMM_EPI_NORM_E4M3_ROWS = 2   /* e4m3(y / d_scale[i]), d_scale[i] = max_j |y_ij| / 448: one scale a
+    GEMM_EPI_NORM_E4M3_ROWS = 2,  /* e4m3(y / d_scale[i]), d_scale[i] = max_j |y_ij| / 448: one scale a
                                      row, which the call writes.  A row whose largest |s_ij gamma_j|
                                      is at most 1e-35 counts as one of zeros: scale 1, codes 0      */
+    GEMM_EPI_NORM_I8_ROWS = 4     /* the same in 8-bit integers, for gemm_epi_run_scaled: round(y / d_scale[i]) to
+                                     nearest even, d_scale[i] = max_j |y_ij| / 127 (3 is no mode).  A row with a
+                                     value that is not finite has a scale that is not, or NaN        */
 };
 
 /* Root-mean-square norm of the rows of a residual stream, the residual's addition before it:
  *     s = x + r,   y_ij = s_ij * gamma_j / sqrt(mean_j s_ij^2 + eps)
- *   m, d    rows (1 ... 2^31 - 1) and row length: a multiple of 8 (of 16 for an e4m3 Y;
+ *   m, d    rows (1 ... 2^31 - 1) and row length: a multiple of 8 (of 16 for an 8-bit Y;
  *           ERR_ALIGN otherwise) up to 16384 (ERR_UNSUPPORTED beyond).
  *   dtype   GEMM_EPI_F16 or GEMM_EPI_BF16: the type of X, R, gamma, S and a 16-bit Y.
  *   eps     > 0 and finite.
@@ -442,14 +471,14 @@ enum gemm_epi_norm_out {
  *   gamma   length d.
  *   S       (m, d): s rounded to nearest even, the next residual.  May be NULL (not kept); must
  *           be NULL without R.  S may be X or R (the stream updated in place).
- *   Y       (m, d), in the 16-bit type or e4m3 (out_mode).  A 16-bit Y may be X or R, never S.
- *   d_scale E4M3: DEVICE pointer to one float > 0, read.  E4M3_ROWS: DEVICE pointer to m floats,
+ *   Y       (m, d), in the 16-bit type, e4m3 or int8 (out_mode).  A 16-bit Y may be X or R, never S.
+ *   d_scale E4M3: DEVICE pointer to one float > 0, read.  E4M3_ROWS, I8_ROWS: DEVICE pointer to m floats,
  *           written.  SAME: ignored.
  *   d_amax  E4M3, may be NULL (else ignored): DEVICE pointer to one float, set to 0 on the stream
  *           and max-reduced: max |y| before quantisation, as for gemm_epi_set_out_scale.
  * All arithmetic is fp32, and the norm is taken of the unrounded sum; y and s are rounded to
  * nearest even once, an e4m3 y saturates at +-448.  Inputs are finite, and a row's sum of squares and,
- * for an e4m3 Y, its |s_ij gamma_j| stay below the largest fp32 number.  Every pointer is 16-byte aligned (d_scale and d_amax:
+ * for an 8-bit Y, its |s_ij gamma_j| stay below the largest fp32 number.  Every pointer is 16-byte aligned (d_scale and d_amax:
  * 4-byte).  One launch (two with d_amax), nothing allocated, any stream;
  * calls may overlap as far as their buffers do.  Returns OK, ERR_ARG (a size, type, mode or eps
  * out of range; S without R; buffers that may not coincide), ERR_ALIGN, ERR_NULL,
@@ -477,6 +506,81 @@ int64_t gemm_epi_rmsnorm_workspace_bytes(int64_t m, int64_t d);
  * Rules, limits and statuses as for gemm_epi_rmsnorm; one launch, two with dgamma and scratch. */
 int gemm_epi_rmsnorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void *dY, const void *S,
                          const void *gamma, const void *dS, void *dX, void *dgamma, void *workspace, void *stream);
+
+/* Layer norm of the rows of a residual stream, the residual's addition before it:
+ *     s = x + r,   y_ij = (s_ij - mu_i) rho_i gamma_j + beta_j,
+ *     mu_i = mean_j s_ij,   rho_i = 1 / sqrt(mean_j (s_ij - mu_i)^2 + eps)
+ * Arguments, rules, limits and statuses are gemm_epi_rmsnorm's; beside them
+ *   beta    length d, in dtype; may be NULL (0).
+ *   d_amax, d_scale  of y as above, beta included; a row whose largest |y_ij| is at most 1e-35 counts as one of zeros.
+ * The mean and the squares of the differences from it are taken in fp32 from the unrounded sum, one after the other, so that a
+ * mean far above the deviation costs no digits but those of s itself. */
+int gemm_epi_layernorm(int64_t m, int64_t d, int dtype, int out_mode, float eps, const void *X, const void *R,
+                       const void *gamma, const void *beta, void *S, void *Y, float *d_scale, float *d_amax, void *stream);
+
+/* Bytes of scratch that gemm_epi_layernorm_bwd needs for dgamma or dbeta (0: none, or sizes it refuses). */
+int64_t gemm_epi_layernorm_workspace_bytes(int64_t m, int64_t d);
+
+/* Backward of gemm_epi_layernorm, from the sum S it stored (X itself without a residual); u = (s - mu) rho, a = dy * gamma:
+ *     dx_ij = ds_ij + rho_i (a_ij - mean_j a_ij - u_ij mean_j(a_ij u_ij))     the gradient of X and of R alike
+ *     dgamma_j = sum_i dy_ij u_ij,   dbeta_j = sum_i dy_ij
+ *   dgamma, dbeta  length d, in dtype, either NULL: not wanted; not the same array (ERR_ARG).
+ *   workspace  of gemm_epi_layernorm_workspace_bytes(m, d) bytes, needed with either.
+ * Everything else as for gemm_epi_rmsnorm_bwd. */
+int gemm_epi_layernorm_bwd(int64_t m, int64_t d, int dtype, float eps, const void *dY, const void *S, const void *gamma,
+                           const void *dS, void *dX, void *dgamma, void *dbeta, void *workspace, void *stream);
+
+/* Rows quantised with one scale each, for the products that read them (activations by token; an (n, k) weight by
+ * channel): what the norms' E4M3_ROWS and I8_ROWS write, without a norm.
+ *   m, d    rows and row length (1 ... 2^31 - 1 each), d a multiple of 16 (ERR_ALIGN otherwise).
+ *   dtype   GEMM_EPI_F16 or GEMM_EPI_BF16, the type of X (m, d).
+ *   out_mode  GEMM_EPI_NORM_E4M3_ROWS or GEMM_EPI_NORM_I8_ROWS.
+ *   Q       (m, d) codes, not X.    d_scale  DEVICE pointer to m floats, written: max_j |x_ij| / 448 or / 127; a row whose largest
+ *           value is at most 1e-35 counts as one of zeros (scale 1, codes 0).
+ * One launch, nothing allocated.  Alignment and statuses as for gemm_epi_rmsnorm. */
+int gemm_epi_quant_rows(int64_t m, int64_t d, int dtype, int out_mode, const void *X, void *Q, float *d_scale, void *stream);
+
+/* ---- activation checkpoints in 8 bits --------------------------------------- */
+
+/* What a training step keeps of a pre-activation z for its epilogue's backward, in a little over half of its 16 bits.  32
+ * neighbouring columns of a row share a power of two:
+ *     z ~ q 2^(e - 133),   q = round(z 2^(133 - e)) to nearest even, |q| <= 127,
+ *     e the smallest from 7 on with max |z| <= 127 * 2^(e - 133)
+ * (the blocks of the OCP Microscaling format MXINT8: int8 in units of 2^-6, a biased exponent byte).  The step is at most 1/64
+ * of the group's largest magnitude; values below 2^-127 become 0.  A group with an infinity, a NaN or a magnitude above
+ * 127 * 2^121 has e = 255 and is restored as NaN throughout.
+ *   m, n    sizes, 1 ... 2^31 - 1; n a multiple of 8 (ERR_ALIGN otherwise); m * gemm_epi_ckpt_groups(n) below 2^32 - 256
+ *           (ERR_UNSUPPORTED beyond).
+ *   dtype   the forward plan's: F16 or BF16 (E4M3: the 16-bit arrays are bf16).
+ *   codes   (m, n) int8, dense, 16-byte aligned.
+ *   exps    (m, gemm_epi_ckpt_groups(n)) bytes, dense: e of row i, columns 32 g ... 32 g + 31 (the last group of a row may be
+ *           short).
+ *   epilogue  names the activation: any from NONE to TANH (RELU_AUX: as RELU).
+ * One launch each, nothing allocated, any stream.  Statuses OK, ERR_ARG (also for codes or exps given as another
+ * array), ERR_ALIGN, ERR_NULL, ERR_UNSUPPORTED, ERR_NO_DEVICE, ERR_CUDA. */
+
+/* Exponents a row: ceil(n / 32) (0 for n < 1 or above 2^31 - 1). */
+int64_t gemm_epi_ckpt_groups(int64_t n);
+
+/* Keep Z (m, n) as codes and exps; H = act(Z) in the 16-bit type beside them (the next product's operand; NULL: not wanted; may
+ * be Z).  H is of z itself, not of what is kept. */
+int gemm_epi_ckpt_save(int64_t m, int64_t n, int dtype, int epilogue, const void *Z, void *H, int8_t *codes, uint8_t *exps,
+                       void *stream);
+
+/* X (m, n) = act(the kept z) in the 16-bit type: z itself for NONE and BIAS, the operand H again for the others (what the
+ * weight's gradient reads).  The kept z is a bf16 number, so nothing is rounded twice; in f16 a value beyond the
+ * type's largest number is that number. */
+int gemm_epi_ckpt_load(int64_t m, int64_t n, int dtype, int epilogue, const int8_t *codes, const uint8_t *exps, void *X,
+                       void *stream);
+
+/* gemm_epi_dact from a checkpoint in place of Z:
+ *     dZ = dD * act'(z),   dbias = the sum of dZ along the bias's axis,   H = act(z)      z as kept
+ *   epilogue  RELU, GELU or TANH, with or without bias (the others keep nothing of z, or the mask: ERR_ARG).  ReLU's slope is 1
+ *           where the kept z is above 0: a z that rounded to 0 counts as 0.
+ *   H       (m, n) in the 16-bit type, NULL: not wanted; may be dD, not dZ.
+ * Everything else as for gemm_epi_dact (workspace: gemm_epi_dact_workspace_bytes). */
+int gemm_epi_dact_ckpt(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, const void *dD, const int8_t *codes,
+                       const uint8_t *exps, void *dZ, void *H, void *dbias, void *workspace, void *stream);
 
 /* Bytes of scratch that gemm_epi_dact needs for dbias (0: none, or sizes or an axis it refuses). */
 int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis);
