@@ -62,45 +62,45 @@ cudaError_t quant_shape(const NormParams &p, bool pdl, cudaStream_t s) {
 // Whether a backward call has few rows: the root-mean-square norm's rule.
 bool few_rows(int64_t m, int64_t d) { return m * (d / 8) <= 148 * 1024; }
 
-// Threads a row and vectors a thread of the backward kernel.
+// The backward kernel's threads a row, vectors a thread and threads a block: one block an SM.
 struct BwdShape {
-    int tpr, vpt;
+    int tpr, vpt, t;
 };
 int64_t bwd_blocks(int64_t m, BwdShape b) {
-    const int rpb = norm_bwd_threads(b.tpr, b.vpt) / b.tpr;
+    const int rpb = b.t / b.tpr;
     return std::min<int64_t>((m + rpb - 1) / rpb, NORM_BWD_BLOCKS);
 }
 BwdShape bwd_shape(int64_t m, int64_t d) {
     const int64_t nv = d / 8;
     if (few_rows(m, d)) {
-        if (nv <= 8) return {8, 1};
-        if (nv <= 32) return {32, 1};
-        if (nv <= 128) return {128, 1};
-        if (nv <= 512) return {512, 1};
+        if (nv <= 8) return {8, 1, 128};
+        if (nv <= 32) return {32, 1, 128};
+        if (nv <= 128) return {128, 1, 128};
+        if (nv <= 512) return {512, 1, 512};
     }
-    if (nv <= 8) return {4, 2};
-    if (nv <= 16) return {8, 2};
-    if (nv <= 32) return {16, 2};
-    if (nv <= 64) return {32, 2};
-    if (nv <= 128) return {64, 2};
-    if (nv <= 256) return {128, 2};
-    if (nv <= 512) return {256, 2};
-    if (nv <= 1024) return {512, 2};
-    return {512, 4};
+    if (nv <= 8) return {4, 2, 512};
+    if (nv <= 16) return {8, 2, 512};
+    if (nv <= 32) return {16, 2, 512};
+    if (nv <= 64) return {32, 2, 512};
+    if (nv <= 128) return {64, 2, 512};
+    if (nv <= 256) return {128, 2, 512};
+    if (nv <= 512) return {256, 2, 512};
+    if (nv <= 1024) return {512, 2, 512};
+    return {512, 4, 512};
 }
 
-template <int DT, int TPR, int VPT>
+template <int DT, int TPR, int VPT, int T = 512>
 cudaError_t bwd_one(const LnBwdParams &p, int64_t grid, bool pdl, cudaStream_t s) {
-    constexpr int T = norm_bwd_threads(TPR, VPT), SMEM = ln_ring_bytes(T, VPT, false);
+    constexpr int SMEM = ln_ring_bytes(T, VPT, false);
     static std::atomic<bool> attr_done[64];
-    return launch_as(layernorm_bwd_kernel<DT, TPR, VPT>, attr_done, dim3((unsigned)grid), T, SMEM, pdl, s, p);
+    return launch_as(layernorm_bwd_kernel<DT, TPR, VPT, T>, attr_done, dim3((unsigned)grid), T, SMEM, pdl, s, p);
 }
 
 template <int DT, int TPR>
 cudaError_t bwd_cluster(const LnBwdParams &p, bool pdl, cudaStream_t s) {
     constexpr int SMEM = ln_ring_bytes(NORM_CLUSTER_T, 1, true);
     static std::atomic<bool> attr_done[64];
-    return launch_as_cluster(layernorm_bwd_kernel<DT, TPR, 1, true>, attr_done, dim3(NORM_CLUSTER), NORM_CLUSTER_T, SMEM, pdl,
+    return launch_as_cluster(layernorm_bwd_kernel<DT, TPR, 1, NORM_CLUSTER_T, true>, attr_done, dim3(NORM_CLUSTER), NORM_CLUSTER_T, SMEM, pdl,
                              NORM_CLUSTER, s, p);
 }
 
@@ -118,9 +118,9 @@ cudaError_t bwd(const LnBwdParams &p, bool pdl, cudaStream_t s) {
     const int64_t grid = bwd_blocks(p.m, b);
     if (b.vpt == 1) {
         switch (b.tpr) {
-        case 8: return bwd_one<DT, 8, 1>(p, grid, pdl, s);
-        case 32: return bwd_one<DT, 32, 1>(p, grid, pdl, s);
-        case 128: return bwd_one<DT, 128, 1>(p, grid, pdl, s);
+        case 8: return bwd_one<DT, 8, 1, 128>(p, grid, pdl, s);
+        case 32: return bwd_one<DT, 32, 1, 128>(p, grid, pdl, s);
+        case 128: return bwd_one<DT, 128, 1, 128>(p, grid, pdl, s);
         default: return bwd_one<DT, 512, 1>(p, grid, pdl, s);
         }
     }

@@ -39,32 +39,108 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// row_reduce of one value: its sum, or its maximum (NaN where there is one).
-template <int TPR, int T, bool MAX>
-__device__ __forceinline__ float row_reduce1(float a, float *red, int grp) {
+// The largest of a and the magnitudes of a pair (NaN where there is one).
+__device__ __forceinline__ float max_abs(float a, f32x2 v) {
+    const float2 f = split(v);
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(f.x), "f"(f.y));
+    return r;
+}
+__device__ __forceinline__ float4 quad(f32x2 a, f32x2 b) {
+    const float2 x = split(a), y = split(b);
+    return make_float4(x.x, x.y, y.x, y.y);
+}
+__device__ __forceinline__ float halves(f32x2 v) {
+    const float2 f = split(v);
+    return f.x + f.y;
+}
+
+// Waits for a row's threads where there are several warps of them.
+template <int TPR, int T>
+__device__ __forceinline__ void row_sync(int grp) {
+    if constexpr (TPR == T) __syncthreads();
+    else ptx::named_bar_sync(1 + grp, TPR);
+}
+
+// Sum of a over a row's TPR threads, the same bits in each; red: a float for each of its warps.
+template <int TPR, int T>
+__device__ __forceinline__ float row_sum(float a, float *red, int grp) {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
-    for (int sh = W / 2; sh >= 1; sh >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, a, sh);
-        a = MAX ? max_nan(a, o) : a + o;
-    }
+    for (int sh = W / 2; sh >= 1; sh >>= 1) a += __shfl_xor_sync(0xffffffffu, a, sh);
     if constexpr (TPR > 32) {
         constexpr int NW = TPR / 32;
         if ((threadIdx.x & 31) == 0) red[(threadIdx.x % TPR) >> 5] = a;
-        if constexpr (TPR == T) __syncthreads();
-        else ptx::named_bar_sync(1 + grp, TPR);
-        a = red[0];
+        row_sync<TPR, T>(grp);
+        const f32x2 *r = reinterpret_cast<const f32x2 *>(red);
+        f32x2 s = r[0];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) a = MAX ? max_nan(a, red[w]) : a + red[w];
+        for (int w = 1; w < NW / 2; ++w) s = add2(s, r[w]);
+        a = halves(s);
     }
     return a;
 }
 
+// The same of two values.  The warps of a long row share the work of the first exchange: their lower lanes go on with a, the
+// upper ones with b, which halves the shuffles (two sums of 256 threads cost 27 instructions, by two butterflies and a sum over
+// the warps for each 44; every thread has but 16 elements to do); red: a pair for each warp.
+template <int TPR, int T>
+__device__ __forceinline__ void row_sum2(float &a, float &b, f32x2 *red, int grp) {
+    if constexpr (TPR <= 32) {
+#pragma unroll
+        for (int sh = TPR / 2; sh >= 1; sh >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, sh);
+            b += __shfl_xor_sync(0xffffffffu, b, sh);
+        }
+    } else {
+        constexpr int NW = TPR / 32;
+        const bool upper = (threadIdx.x & 16) != 0;
+        float v = upper ? b : a;
+        v += __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+        for (int sh = 8; sh >= 1; sh >>= 1) v += __shfl_xor_sync(0xffffffffu, v, sh);
+        if ((threadIdx.x & 15) == 0) reinterpret_cast<float *>(red)[(threadIdx.x % TPR) >> 4] = v;
+        row_sync<TPR, T>(grp);
+        const ulonglong2 *r = reinterpret_cast<const ulonglong2 *>(red);
+        f32x2 s = add2(r[0].x, r[0].y);
+#pragma unroll
+        for (int w = 1; w < NW / 2; ++w) s = add2(s, add2(r[w].x, r[w].y));
+        const float2 f = split(s);
+        a = f.x;
+        b = f.y;
+    }
+}
+
+// The largest of a over a row's threads (NaN where there is one); a >= 0.
+template <int TPR, int T>
+__device__ __forceinline__ float row_max(float a, float *red, int grp) {
+    if constexpr (TPR < 32) {
+#pragma unroll
+        for (int sh = TPR / 2; sh >= 1; sh >>= 1) a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, sh));
+    } else {
+        // (the bits of numbers from 0 on order as they do, NaN's above them)
+        a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a)));
+        if constexpr (TPR > 32) {
+            constexpr int NW = TPR / 32;
+            if ((threadIdx.x & 31) == 0) red[(threadIdx.x % TPR) >> 5] = a;
+            row_sync<TPR, T>(grp);
+            a = red[0];
+#pragma unroll
+            for (int w = 1; w < NW; ++w) a = max_nan(a, red[w]);
+        }
+    }
+    return a;
+}
+
+// Blocks an SM that the forward kernel is compiled for: 24 warps at 80 registers (8192 x 4096 bf16 + residual to e4m3 by rows 39.4 us;
+// left to itself the compiler takes as many and orders them worse, 41.8; 28 and 32 warps spill, 41.2 and 65.7).
+constexpr int ln_blocks(int threads) { return threads >= 512 ? 1 : 768 / threads; }
+
 template <int DT, int OUT, int TPR, int VPT>
-__global__ void __launch_bounds__(norm_threads(TPR)) layernorm_kernel(const LnParams p) {
+__global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR))) layernorm_kernel(const LnParams p) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR, NW = TPR > 32 ? TPR / 32 : 1;
-    __shared__ float red1[RPB][NW], redm[RPB][NW];
-    __shared__ float2 red2[RPB][NW];
+    __shared__ __align__(16) float red1[RPB][NW], redm[RPB][NW];
+    __shared__ __align__(16) f32x2 red2[RPB][NW];
     const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPB + grp;
     const bool row_ok = row < p.m;
@@ -72,68 +148,72 @@ __global__ void __launch_bounds__(norm_threads(TPR)) layernorm_kernel(const LnPa
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
-    uint4 xv[VPT], rv[VPT], gv[VPT], bv[VPT];
+    uint4 xv[VPT], rv[VPT];
     const int64_t base = row * p.d;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = j * TPR + t;
-        xv[j] = rv[j] = gv[j] = bv[j] = make_uint4(0u, 0u, 0u, 0u);
+        xv[j] = rv[j] = make_uint4(0u, 0u, 0u, 0u);
         if (row_ok && v < nvec) {
             xv[j] = ptx::ld_stream(static_cast<const uint16_t *>(p.x) + base + 8 * v);
             if (p.r != nullptr) rv[j] = ptx::ld_stream(static_cast<const uint16_t *>(p.r) + base + 8 * v);
         }
     }
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        const int v = j * TPR + t;
-        if (v < nvec) {
-            gv[j] = __ldg(static_cast<const uint4 *>(p.gamma) + v);
-            if (p.beta != nullptr) bv[j] = __ldg(static_cast<const uint4 *>(p.beta) + v);
-        }
-    }
-    float s[VPT][8];
-    float sum = 0.0f;
+    f32x2 s[VPT][4];
+    f32x2 sum = both(0.0f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         unpack8<DT>(xv[j], s[j]);
         if (p.r != nullptr) {
-            float r[8];
+            f32x2 r[4];
             unpack8<DT>(rv[j], r);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) s[j][e] += r[e];
+            for (int e = 0; e < 4; ++e) s[j][e] = add2(s[j][e], r[e]);
             const int v = j * TPR + t;
             if (p.s != nullptr && row_ok && v < nvec)
                 *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.s) + base + 8 * v) = pack8<DT>(s[j]);
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += s[j][e];
+        for (int e = 0; e < 4; ++e) sum = add2(sum, s[j][e]);
     }
-    const float mu = row_reduce1<TPR, T, false>(sum, red1[grp], grp) * p.inv_d;
-    float ss = 0.0f, left = 0.0f;
+    const float mu = row_sum<TPR, T>(halves(sum), red1[grp], grp) * p.inv_d;
+    // (g and b, the same for every row, are asked for now: they take the registers that x and r had)
+    uint4 gv[VPT], bv[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int v = j * TPR + t;
+        gv[j] = bv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (v < nvec) {
+            gv[j] = __ldg(static_cast<const uint4 *>(p.gamma) + v);
+            if (p.beta != nullptr) bv[j] = __ldg(static_cast<const uint4 *>(p.beta) + v);
+        }
+    }
+    f32x2 ss2 = both(0.0f), left2 = both(0.0f);
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         if (j * TPR + t < nvec) {                         // (behind the row's end there is no difference)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                s[j][e] -= mu;
-                ss = fmaf(s[j][e], s[j][e], ss);
-                left += s[j][e];
+            for (int e = 0; e < 4; ++e) {
+                s[j][e] = add2(s[j][e], both(-mu));
+                ss2 = fma2(s[j][e], s[j][e], ss2);
+                left2 = add2(left2, s[j][e]);
             }
         }
     }
-    row_reduce<TPR, T, false>(ss, left, red2[grp], grp);
+    float ss = halves(ss2), left = halves(left2);
+    row_sum2<TPR, T>(ss, left, red2[grp], grp);
     left *= p.inv_d;
     const float rho = rsqrtf(fmaxf(fmaf(ss, p.inv_d, -left * left), 0.0f) + p.eps);
     float top = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-        float g[8], b[8];
+        f32x2 g[4], b[4];
         unpack8<DT>(gv[j], g);
         unpack8<DT>(bv[j], b);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            s[j][e] = fmaf((s[j][e] - left) * rho, g[e], b[e]);      // (0 behind the row's end: g and b are)
-            if constexpr (OUT != NORM_SAME) top = max_nan(top, fabsf(s[j][e]));
+        for (int e = 0; e < 4; ++e) {
+            s[j][e] = fma2(mul2(add2(s[j][e], both(-left)), both(rho)), g[e], b[e]);     // (0 behind the row's end: g and b are)
+            if constexpr (OUT != NORM_SAME) top = max_abs(top, s[j][e]);
         }
     }
     float mul = 1.0f;
@@ -146,9 +226,9 @@ __global__ void __launch_bounds__(norm_threads(TPR)) layernorm_kernel(const LnPa
         }
     } else if constexpr (norm_by_rows(OUT)) {
         constexpr float C = norm_top_code(OUT);
-        top = row_reduce1<TPR, T, true>(top, redm[grp], grp);
+        top = row_max<TPR, T>(top, redm[grp], grp);
         const bool zero = top <= 1e-35f;
-        mul = zero ? 0.0f : C / top;
+        mul = zero ? 0.0f : code_factor<OUT>(top);
         if (t == 0 && row_ok) p.scale[row] = zero ? 1.0f : top * (1.0f / C);
     }
     if (!row_ok) return;
@@ -184,24 +264,24 @@ __global__ void __launch_bounds__(norm_threads(TPR)) quant_rows_kernel(const Nor
     }
     float top = 0.0f;
     auto max8 = [&](const uint4 &u) {
-        float f[8];
+        f32x2 f[4];
         unpack8<DT>(u, f);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max_nan(top, fabsf(f[e]));
+        for (int e = 0; e < 4; ++e) top = max_abs(top, f[e]);
     };
 #pragma unroll
     for (int j = 0; j < VPT; ++j) max8(xv[j]);
     if constexpr (LONG)                                   // (one row a block, so the row is there)
         for (int v = VPT * TPR + t; v < nvec; v += TPR) max8(__ldg(reinterpret_cast<const uint4 *>(x + 8 * (int64_t)v)));
-    top = row_reduce1<TPR, T, true>(top, red[grp], grp);
+    top = row_max<TPR, T>(top, red[grp], grp);
     if (!row_ok) return;
     constexpr float C = norm_top_code(OUT);
     const bool zero = top <= 1e-35f;
-    const float mul = zero ? 0.0f : C / top;
+    const float mul = zero ? 0.0f : code_factor<OUT>(top);
     if (t == 0) p.scale[row] = zero ? 1.0f : top * (1.0f / C);
     uint8_t *y = static_cast<uint8_t *>(p.y) + row * p.d;
     auto put8 = [&](int v, const uint4 &u) {
-        float f[8];
+        f32x2 f[4];
         unpack8<DT>(u, f);
         *reinterpret_cast<uint2 *>(y + 8 * (int64_t)v) = codes8<OUT>(f, mul);
     };
@@ -218,14 +298,13 @@ __global__ void __launch_bounds__(norm_threads(TPR)) quant_rows_kernel(const Nor
 constexpr int ln_ring(bool cluster) { return cluster ? 4 : 2; }
 constexpr int ln_ring_bytes(int threads, int vpt, bool cluster) { return ln_ring(cluster) * 3 * threads * vpt * 16; }
 
-template <int DT, int TPR, int VPT, bool CLUSTER = false>
-__global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TPR, VPT), 1)
-    layernorm_bwd_kernel(const LnBwdParams p) {
-    constexpr int T = CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TPR, VPT), RPB = T / TPR, RING = ln_ring(CLUSTER);
+template <int DT, int TPR, int VPT, int T, bool CLUSTER = false>
+__global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p) {
+    constexpr int RPB = T / TPR, RING = ln_ring(CLUSTER);
     constexpr int ARRAY = T * VPT;                    // vectors of one array in a stage of the ring
     constexpr int NW = TPR > 32 ? TPR / 32 : 1;
     extern __shared__ uint4 ring[];                   // [RING][dy, s, ds][vector][thread]
-    __shared__ float2 red1[RPB][NW], red2[RPB][NW];     // (either is read before the other's next barrier)
+    __shared__ __align__(16) f32x2 red1[RPB][NW], red2[RPB][NW];     // (either is read before the other's next barrier)
     const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR, nvec = p.d / 8;
     const bool skip = p.ds != nullptr;
     ptx::griddep_wait();
@@ -247,13 +326,13 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
         ptx::cp_async_commit();                       // (an empty group keeps the count)
     };
     uint4 gv[VPT];
-    float accg[VPT][8], accb[VPT][8];
+    f32x2 accg[VPT][4], accb[VPT][4];
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = j * TPR + t;
         gv[j] = v < nvec ? __ldg(static_cast<const uint4 *>(p.gamma) + v) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) accg[j][e] = accb[j][e] = 0.0f;
+        for (int e = 0; e < 4; ++e) accg[j][e] = accb[j][e] = both(0.0f);
     }
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t row0 = (int64_t)blockIdx.x * RPB;
@@ -267,26 +346,26 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
         ptx::cp_async_wait<RING - 1>();
         const uint4 *cur = ring + stage * 3 * ARRAY + threadIdx.x;
         constexpr bool HOLD = VPT <= 2;
-        float a[HOLD ? VPT : 1][8], c[HOLD ? VPT : 1][8];
+        f32x2 a[HOLD ? VPT : 1][4], c[HOLD ? VPT : 1][4];
         // a and s of vector j
-        auto load = [&](int j, float (&av)[8], float (&sv)[8]) {
-            float g[8];
+        auto load = [&](int j, f32x2(&av)[4], f32x2(&sv)[4]) {
+            f32x2 g[4];
             unpack8<DT>(cur[j * T], av);
             unpack8<DT>(cur[ARRAY + j * T], sv);
             unpack8<DT>(gv[j], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) av[e] *= g[e];
+            for (int e = 0; e < 4; ++e) av[e] = mul2(av[e], g[e]);
         };
-        float mu = 0.0f, ma = 0.0f;
+        f32x2 mu2 = both(0.0f), ma2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             if (row_ok && j * TPR + t < nvec) {
-                float av[8], sv[8];
+                f32x2 av[4], sv[4];
                 load(j, av, sv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    mu += sv[e];
-                    ma += av[e];
+                for (int e = 0; e < 4; ++e) {
+                    mu2 = add2(mu2, sv[e]);
+                    ma2 = add2(ma2, av[e]);
                     if constexpr (HOLD) {
                         a[j][e] = av[e];
                         c[j][e] = sv[e];
@@ -294,25 +373,27 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
                 }
             }
         }
-        row_reduce<TPR, T, false>(mu, ma, red1[grp], grp);
+        float mu = halves(mu2), ma = halves(ma2);
+        row_sum2<TPR, T>(mu, ma, red1[grp], grp);
         mu *= p.inv_d;
         ma *= p.inv_d;
-        float ss = 0.0f, as = 0.0f;
+        f32x2 ss2 = both(0.0f), as2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             if (row_ok && j * TPR + t < nvec) {
-                float av[8], sv[8];
+                f32x2 av[4], sv[4];
                 if constexpr (!HOLD) load(j, av, sv);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float d = (HOLD ? c[HOLD ? j : 0][e] : sv[e]) - mu;
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 d = add2(HOLD ? c[HOLD ? j : 0][e] : sv[e], both(-mu));
                     if constexpr (HOLD) c[j][e] = d;
-                    ss = fmaf(d, d, ss);
-                    as = fmaf(HOLD ? a[HOLD ? j : 0][e] : av[e], d, as);
+                    ss2 = fma2(d, d, ss2);
+                    as2 = fma2(HOLD ? a[HOLD ? j : 0][e] : av[e], d, as2);
                 }
             }
         }
-        row_reduce<TPR, T, false>(ss, as, red2[grp], grp);
+        float ss = halves(ss2), as = halves(as2);
+        row_sum2<TPR, T>(ss, as, red2[grp], grp);
         const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
         const float k = rho * (rho * (as * p.inv_d));     // (rho^2 is beyond fp32 beside the smallest eps)
         uint16_t *out = static_cast<uint16_t *>(p.dx) + row * p.d;
@@ -320,17 +401,17 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
         for (int j = 0; j < VPT; ++j) {
             const int v = j * TPR + t;
             if (row_ok && v < nvec) {
-                float av[8], sv[8], y[8], o[8];
+                f32x2 av[4], sv[4], y[4], o[4];
                 if constexpr (!HOLD) load(j, av, sv);
                 unpack8<DT>(cur[j * T], y);
                 unpack8<DT>(skip ? cur[2 * ARRAY + j * T] : make_uint4(0u, 0u, 0u, 0u), o);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float d = HOLD ? c[HOLD ? j : 0][e] : sv[e] - mu;
-                    const float g = HOLD ? a[HOLD ? j : 0][e] : av[e];
-                    accb[j][e] += y[e];
-                    accg[j][e] = fmaf(y[e] * rho, d, accg[j][e]);
-                    o[e] = fmaf(rho, fmaf(-d, k, g - ma), o[e]);
+                for (int e = 0; e < 4; ++e) {
+                    const f32x2 d = HOLD ? c[HOLD ? j : 0][e] : add2(sv[e], both(-mu));
+                    const f32x2 g = HOLD ? a[HOLD ? j : 0][e] : av[e];
+                    accb[j][e] = add2(accb[j][e], y[e]);
+                    accg[j][e] = fma2(mul2(y[e], both(rho)), d, accg[j][e]);
+                    o[e] = fma2(both(rho), fma2(d, both(-k), add2(g, both(-ma))), o[e]);
                 }
                 *reinterpret_cast<uint4 *>(out + 8 * v) = pack8<DT>(o);
             }
@@ -352,9 +433,9 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
 #pragma unroll
             for (int j = 0; j < VPT; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    accg[j][e] += __shfl_xor_sync(0xffffffffu, accg[j][e], sh);
-                    accb[j][e] += __shfl_xor_sync(0xffffffffu, accb[j][e], sh);
+                for (int e = 0; e < 4; ++e) {
+                    accg[j][e] = add2(accg[j][e], __shfl_xor_sync(0xffffffffu, accg[j][e], sh));
+                    accb[j][e] = add2(accb[j][e], __shfl_xor_sync(0xffffffffu, accb[j][e], sh));
                 }
         constexpr int W = TPR < 32 ? 32 : TPR, G = T / W, V = VPT * TPR;
         float4 *sums = reinterpret_cast<float4 *>(ring);
@@ -366,8 +447,8 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     float4 *to = sums + (threadIdx.x / W * 2 + h) * V + j * TPR + t;
-                    to[0] = make_float4(accg[j][4 * h], accg[j][4 * h + 1], accg[j][4 * h + 2], accg[j][4 * h + 3]);
-                    to[2 * V * G] = make_float4(accb[j][4 * h], accb[j][4 * h + 1], accb[j][4 * h + 2], accb[j][4 * h + 3]);
+                    to[0] = quad(accg[j][2 * h], accg[j][2 * h + 1]);
+                    to[2 * V * G] = quad(accb[j][2 * h], accb[j][2 * h + 1]);
                 }
         }
         __syncthreads();
@@ -392,11 +473,11 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
             const int v = j * TPR + t;
             if (v < nvec) {
                 float4 *o = reinterpret_cast<float4 *>(part + 8 * v);
-                o[0] = make_float4(accg[j][0], accg[j][1], accg[j][2], accg[j][3]);
-                o[1] = make_float4(accg[j][4], accg[j][5], accg[j][6], accg[j][7]);
+                o[0] = quad(accg[j][0], accg[j][1]);
+                o[1] = quad(accg[j][2], accg[j][3]);
                 o = reinterpret_cast<float4 *>(part + p.d + 8 * v);
-                o[0] = make_float4(accb[j][0], accb[j][1], accb[j][2], accb[j][3]);
-                o[1] = make_float4(accb[j][4], accb[j][5], accb[j][6], accb[j][7]);
+                o[0] = quad(accb[j][0], accb[j][1]);
+                o[1] = quad(accb[j][2], accb[j][3]);
             }
         }
     }

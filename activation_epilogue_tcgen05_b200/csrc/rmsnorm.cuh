@@ -67,23 +67,57 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
     return make_uint4(O::pack(f[0], f[1]), O::pack(f[2], f[3]), O::pack(f[4], f[5]), O::pack(f[6], f[7]));
 }
 
+// Eight values in pairs, and back to the 16-bit type.
+template <int DT>
+__device__ __forceinline__ void unpack8(const uint4 &u, f32x2 (&f)[4]) {
+    float v[8];
+    unpack8<DT>(u, v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[e] = pair(v[2 * e], v[2 * e + 1]);
+}
+template <int DT>
+__device__ __forceinline__ uint4 pack8(const f32x2 (&f)[4]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float2 v = split(f[e]);
+        w[e] = OutT<DT>::pack(v.x, v.y);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
 // Eight values times mul as 8-bit codes of the output type.  Integers (|v mul| within half of 127): 1.5 * 2^23 is added, which
 // leaves the nearest integer, ties to even, in the sum's low byte; one rounding, of the product.
 template <int OUT>
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float mul) {
+__device__ __forceinline__ uint2 codes8(const f32x2 (&v)[4], float mul) {
+    const f32x2 m = both(mul);
     if constexpr (OUT == NORM_I8_ROWS) {
-        uint32_t b[8];
+        uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(fmaf(v[e], mul, 12582912.0f));
-        return make_uint2(__byte_perm(__byte_perm(b[0], b[1], 0x0040), __byte_perm(b[2], b[3], 0x0040), 0x5410),
-                          __byte_perm(__byte_perm(b[4], b[5], 0x0040), __byte_perm(b[6], b[7], 0x0040), 0x5410));
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = split(fma2(v[e], m, both(12582912.0f)));
+            w[e] = __byte_perm(__float_as_uint(f.x), __float_as_uint(f.y), 0x0040);
+        }
+        return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
     } else {
         uint32_t w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            w[e] = __nv_cvt_float2_to_fp8x2(make_float2(v[2 * e] * mul, v[2 * e + 1] * mul), __NV_SATFINITE, __NV_E4M3);
+        for (int e = 0; e < 4; ++e) w[e] = __nv_cvt_float2_to_fp8x2(split(mul2(v[e], m)), __NV_SATFINITE, __NV_E4M3);
         return make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
     }
+}
+template <int OUT>
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float mul) {
+    const f32x2 f[4] = {pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
+    return codes8<OUT>(f, mul);
+}
+
+// What the values of a row whose largest magnitude is top are multiplied by.  127 / top is rounded up: half of the largest
+// value is a tie between 63 and 64 (the only one there is unless 127 divides top's digits, and then the quotient is exact), and
+// has to go to the even 64.
+template <int OUT>
+__device__ __forceinline__ float code_factor(float top) {
+    return OUT == NORM_I8_ROWS ? __fdiv_ru(127.0f, top) : 448.0f / top;
 }
 
 // Sum of `a` and combination of `b` (maximum, or sum) over the TPR threads of a row, the same
@@ -188,7 +222,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
         // 448 / top overflows below 1.4e-36; such a row is one of zeros in 8 bits at any scale in use
         constexpr float C = norm_top_code(OUT);
         const bool zero = !(top > 1e-35f);
-        mul = zero ? (OUT == NORM_I8_ROWS ? 0.0f : rho) : C / top;
+        mul = zero ? (OUT == NORM_I8_ROWS ? 0.0f : rho) : code_factor<OUT>(top);
         if (t == 0 && row_ok) p.scale[row] = zero ? 1.0f : rho * top * (1.0f / C);
     }
     if (!row_ok) return;
