@@ -12,7 +12,7 @@
 // save: H = act(z) (the next product's operand, optional), codes and exponents in one pass over z;
 // load: z, or act(z), in the 16-bit type again.  Bound by HBM.  A thread takes eight columns, four neighbours a group, so that a
 // group's maximum is two shuffles; the groups of all rows are dealt to the threads in one line, so that narrow and
-// ragged rows leave few of them idle; CKPT_U groups a thread, all loads first.
+// ragged rows leave few of them idle; U groups a thread, all loads first.
 #pragma once
 #include <cstdint>
 
@@ -21,7 +21,6 @@
 namespace gemm_epi {
 
 constexpr int CKPT_GROUP = 32;
-constexpr int CKPT_U = 4;           // groups of a thread
 constexpr int CKPT_T = 256;
 __host__ __device__ constexpr int ckpt_groups(int64_t n) { return (int)((n + CKPT_GROUP - 1) / CKPT_GROUP); }
 
@@ -89,8 +88,8 @@ __device__ __forceinline__ void ckpt_act8(float (&f)[8]) {
 // Where a thread's groups lie: group `id` of all rows, and from it every CKPT_T / 4 further.
 struct CkptWalk {
     uint32_t id, row, g, drow, dg;
-    __device__ __forceinline__ CkptWalk(const CkptParams &p) {
-        id = blockIdx.x * (uint32_t)(CKPT_T / 4 * CKPT_U) + threadIdx.x / 4;
+    __device__ __forceinline__ CkptWalk(const CkptParams &p, int u) {
+        id = blockIdx.x * (uint32_t)(CKPT_T / 4 * u) + threadIdx.x / 4;
         row = id / p.groups;
         g = id - row * p.groups;
         drow = (CKPT_T / 4) / p.groups;
@@ -108,24 +107,24 @@ struct CkptWalk {
     }
 };
 
-template <int DT, int EPI>
+template <int DT, int EPI, int U>
 __global__ void __launch_bounds__(CKPT_T) ckpt_save_kernel(const CkptParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    uint4 zv[CKPT_U];
-    int64_t at[CKPT_U];                               // the thread's first element; negative: none
+    uint4 zv[U];
+    int64_t at[U];                               // the thread's first element; negative: none
     uint32_t id0;
     {
-        CkptWalk w(p);
+        CkptWalk w(p, U);
         id0 = w.id;
 #pragma unroll
-        for (int u = 0; u < CKPT_U; ++u, w.next(p)) {
+        for (int u = 0; u < U; ++u, w.next(p)) {
             at[u] = w.id < p.total && w.col() < p.n ? (int64_t)w.row * p.n + w.col() : -1;
             zv[u] = at[u] >= 0 ? ptx::ld_stream(static_cast<const uint16_t *>(p.z) + at[u]) : make_uint4(0u, 0u, 0u, 0u);
         }
     }
 #pragma unroll
-    for (int u = 0; u < CKPT_U; ++u) {
+    for (int u = 0; u < U; ++u) {
         float f[8];
         unpack8<DT>(zv[u], f);
         uint32_t top = 0u;
@@ -146,16 +145,16 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_save_kernel(const CkptParams p) {
 }
 
 // f16: a code's value may be above the type's largest number, to which save's z was rounded up in its step; it is drawn back.
-template <int DT, int EPI>
+template <int DT, int EPI, int U>
 __global__ void __launch_bounds__(CKPT_T) ckpt_load_kernel(const CkptParams p) {
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    uint2 q[CKPT_U];
-    uint32_t ex[CKPT_U];
-    int64_t at[CKPT_U];
-    CkptWalk w(p);
+    uint2 q[U];
+    uint32_t ex[U];
+    int64_t at[U];
+    CkptWalk w(p, U);
 #pragma unroll
-    for (int u = 0; u < CKPT_U; ++u, w.next(p)) {
+    for (int u = 0; u < U; ++u, w.next(p)) {
         at[u] = w.id < p.total && w.col() < p.n ? (int64_t)w.row * p.n + w.col() : -1;
         q[u] = make_uint2(0u, 0u);
         ex[u] = 7u;
@@ -165,7 +164,7 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_load_kernel(const CkptParams p) {
         }
     }
 #pragma unroll
-    for (int u = 0; u < CKPT_U; ++u) {
+    for (int u = 0; u < U; ++u) {
         float f[8];
         ckpt_decode8(q[u], ckpt_step(ex[u]), f);
         ckpt_act8<EPI>(f);

@@ -60,10 +60,12 @@ __device__ __forceinline__ float min_nan(float a, float b) {
     asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
-// Phi's own tail comes out on the way, and with it the value: GELU(x) = max(x, 0) - u (1 - Phi(u)) (val; for finite x).
+// Phi's own tail comes out on the way, and with it the value: GELU(x) = max(x, 0) - u (1 - Phi(u)) (val; for finite x, FINITE: which need no cut).
+template <bool FINITE = false>
 __device__ __forceinline__ f32x2 gelu_slope(float x0, float x1, f32x2 *val = nullptr) {
     constexpr float c = 0.84932180028801907f;                                 // sqrt(log2(e) / 2): e = 2^-(c u)^2
-    const f32x2 v = mul2(pair(min_nan(fabsf(x0), 16.0f), min_nan(fabsf(x1), 16.0f)), both(c));
+    const f32x2 u = pair(fabsf(x0), fabsf(x1));
+    const f32x2 v = mul2(FINITE ? u : pair(min_nan(fabsf(x0), 16.0f), min_nan(fabsf(x1), 16.0f)), both(c));
     const float2 den = split(add2(v, both(2.498f))), q = split(mul2(v, v));
     const f32x2 t = pair(rcp_approx(den.x), rcp_approx(den.y));
     f32x2 h = fma2(t, both(20.0101986f), both(-24.893486f));
@@ -75,7 +77,7 @@ __device__ __forceinline__ f32x2 gelu_slope(float x0, float x1, f32x2 *val = nul
     const f32x2 e = pair(ex2_approx(-q.x), ex2_approx(-q.y));
     const f32x2 left = mul2(e, w);
     if (val != nullptr)
-        *val = fma2(pair(0.5f * fabsf(x0), 0.5f * fabsf(x1)), mul2(e, h), pair(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
+        *val = fma2(mul2(u, both(0.5f)), mul2(e, h), pair(fmaxf(x0, 0.0f), fmaxf(x1, 0.0f)));
     const f32x2 side = pair(copysignf(0.5f, x0), copysignf(0.5f, x1));
     return fma2(left, side, add2(side, both(0.5f)));
 }
@@ -91,15 +93,15 @@ __device__ __forceinline__ f32x2 tanh_slope(float x0, float x1) {
 }
 
 // act'(z) of two neighbouring elements.
-template <int ACT>
+template <int ACT, bool FINITE>
 __device__ __forceinline__ f32x2 slope(float z0, float z1, f32x2 *val = nullptr) {
-    if constexpr (ACT == DACT_GELU) return gelu_slope(z0, z1, val);
+    if constexpr (ACT == DACT_GELU) return gelu_slope<FINITE>(z0, z1, val);
     if (val != nullptr) *val = tanh2(z0, z1);
     return tanh_slope(z0, z1);
 }
 
 // d *= act'(z) for a lane's eight elements (bits: their mask); VAL: z becomes act(z).
-template <int ACT, bool VAL = false>
+template <int ACT, bool FINITE, bool VAL>
 __device__ __forceinline__ void through_act(float (&d)[8], float (&z)[8], uint32_t bits) {
     if constexpr (ACT == DACT_RELU_MASK) {
 #pragma unroll
@@ -114,7 +116,7 @@ __device__ __forceinline__ void through_act(float (&d)[8], float (&z)[8], uint32
 #pragma unroll
         for (int e = 0; e < 8; e += 2) {
             f32x2 val;
-            const float2 f = split(mul2(pair(d[e], d[e + 1]), slope<ACT>(z[e], z[e + 1], VAL ? &val : nullptr)));
+            const float2 f = split(mul2(pair(d[e], d[e + 1]), slope<ACT, FINITE>(z[e], z[e + 1], VAL ? &val : nullptr)));
             d[e] = f.x;
             d[e + 1] = f.y;
             if constexpr (VAL) {
@@ -137,26 +139,26 @@ constexpr bool dact_reads_z(int act) { return act != DACT_NONE && act != DACT_RE
 // fit the 80 registers that three blocks an SM leave (8192 x 14336 GELU 120 us, two at a time 112).
 constexpr bool dact_computes(int act) { return act == DACT_GELU || act == DACT_TANH; }
 constexpr int DACT_RING = 2;
-constexpr int dact_smem(bool ck) { return DACT_RING * DACT_U * 32 * DACT_WARPS * (ck ? 24 : 32); }
+constexpr int dact_smem(bool ck, int u = DACT_U) { return DACT_RING * u * 32 * DACT_WARPS * (ck ? 24 : 32); }
 
 // What a thread has of one row of a stage in the ring: [DACT_RING][U][T] of dD, then as many of z or of its codes.
-template <bool CK>
+template <bool CK, int U = DACT_U>
 struct DactRing {
     using Zv = std::conditional_t<CK, uint2, uint4>;
-    static constexpr int N = DACT_RING * DACT_U * 32 * DACT_WARPS;
+    static constexpr int N = DACT_RING * U * 32 * DACT_WARPS;
     static __device__ __forceinline__ uint4 *dd(uint4 *ring, int stage, int u) {
-        return ring + (stage * DACT_U + u) * 32 * DACT_WARPS + threadIdx.x;
+        return ring + (stage * U + u) * 32 * DACT_WARPS + threadIdx.x;
     }
     static __device__ __forceinline__ Zv *z(uint4 *ring, int stage, int u) {
-        return reinterpret_cast<Zv *>(ring + N) + (stage * DACT_U + u) * 32 * DACT_WARPS + threadIdx.x;
+        return reinterpret_cast<Zv *>(ring + N) + (stage * U + u) * 32 * DACT_WARPS + threadIdx.x;
     }
 };
 
 // A lane's eight values of z in the ring (ok: whether they are there); ex: CK, their exponent.
-template <int DT, bool CK>
+template <int DT, bool CK, int U = DACT_U>
 __device__ __forceinline__ void dact_z(uint4 *ring, int stage, int u, bool ok, uint32_t ex, float (&z)[8]) {
-    if constexpr (CK) ckpt_decode8(ok ? *DactRing<CK>::z(ring, stage, u) : make_uint2(0u, 0u), ckpt_step(ok ? ex : 7u), z);
-    else unpack8<DT>(ok ? *DactRing<CK>::z(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), z);
+    if constexpr (CK) ckpt_decode8(ok ? *DactRing<CK, U>::z(ring, stage, u) : make_uint2(0u, 0u), ckpt_step(ok ? ex : 7u), z);
+    else unpack8<DT>(ok ? *DactRing<CK, U>::z(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), z);
 }
 
 template <int DT, int ACT, int AXIS, bool CK = false, bool VAL = false>
@@ -237,7 +239,7 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
             } else {
                 unpack8<DT>(dv[u], d);
             }
-            through_act<ACT, VAL>(d, z, bits[u]);
+            through_act<ACT, CK, VAL>(d, z, bits[u]);
             if constexpr (ACT != DACT_NONE) {
                 if (ok) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + i * p.n + col) = pack8<DT>(d);
             }
@@ -293,10 +295,11 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
 // time, so that a row's sum ends in the block and dbias is written at once: one launch, no scratch, and one
 // butterfly a row instead of one every 256 columns (8192 x 14336 ReLU 106 us against 115, 1023 x 4104 from the
 // mask 6.7 us a call from Python against 11.0).  The same ring, along the columns.
-template <int DT, int ACT, bool CK = false, bool VAL = false>
+template <int DT, int ACT, bool CK = false, bool VAL = false, int U = DACT_U>
 __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_rows_kernel(const DactParams p) {
-    constexpr int U = DACT_U, PASS = DACT_WARPS * DACT_COLS;
+    constexpr int PASS = DACT_WARPS * DACT_COLS;
     constexpr bool Z = dact_reads_z(ACT), SLOPE = dact_computes(ACT);
+    static_assert(U % 2 == 0 && U <= 4, "rows are worked out two at a time; their exponents share a word");
     static_assert(Z || !CK, "a checkpoint is one of z");
     extern __shared__ uint4 ring[];                   // Z: DactRing
     __shared__ float sums[DACT_WARPS][U];
@@ -315,9 +318,9 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if (u < rows) {
-                    ptx::cp_async_16(DactRing<CK>::dd(ring, stage, u), dd + (int64_t)u * p.n + col);
-                    if constexpr (CK) ptx::cp_async_8(DactRing<CK>::z(ring, stage, u), codes + (int64_t)u * p.n + col);
-                    else ptx::cp_async_16(DactRing<CK>::z(ring, stage, u), zz + (int64_t)u * p.n + col);
+                    ptx::cp_async_16(DactRing<CK, U>::dd(ring, stage, u), dd + (int64_t)u * p.n + col);
+                    if constexpr (CK) ptx::cp_async_8(DactRing<CK, U>::z(ring, stage, u), codes + (int64_t)u * p.n + col);
+                    else ptx::cp_async_16(DactRing<CK, U>::z(ring, stage, u), zz + (int64_t)u * p.n + col);
                 }
             }
         }
@@ -345,7 +348,9 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
         uint32_t bits[U], ex = 0u;                    // the mask's; CK: the rows' exponents, a byte each
         if constexpr (Z) {
             if constexpr (CK) {
-                ex = next[0] | next[1] << 8 | next[2] << 16 | next[3] << 24;
+                ex = 0u;
+#pragma unroll
+                for (int u = 0; u < U; ++u) ex |= next[u] << 8 * u;
                 exponents(col + PASS);
             }
             ptx::cp_async_wait<DACT_RING - 1>();
@@ -369,12 +374,12 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
                 const int u = u0 + k;
                 float d[8], z[8];
                 if constexpr (Z) {
-                    unpack8<DT>(u < rows ? *DactRing<CK>::dd(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), d);
-                    dact_z<DT, CK>(ring, stage, u, u < rows, ex >> 8 * u & 255u, z);
+                    unpack8<DT>(u < rows ? *DactRing<CK, U>::dd(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), d);
+                    dact_z<DT, CK, U>(ring, stage, u, u < rows, ex >> 8 * u & 255u, z);
                 } else {
                     unpack8<DT>(dv[u], d);
                 }
-                through_act<ACT, VAL>(d, z, bits[u]);
+                through_act<ACT, CK, VAL>(d, z, bits[u]);
                 if constexpr (ACT != DACT_NONE) {
                     if (u < rows) *reinterpret_cast<uint4 *>(dz + (int64_t)u * p.n + col) = pack8<DT>(d);
                 }

@@ -6,12 +6,16 @@
 namespace gemm_epi {
 
 namespace {
-template <int DT, int EPI>
+template <int DT, int EPI, int U>
 cudaError_t ckpt(bool save, const CkptParams &p, bool pdl, cudaStream_t s) {
     static std::atomic<bool> attr_done[64];
-    const dim3 grid((p.total + CKPT_T / 4 * CKPT_U - 1) / (CKPT_T / 4 * CKPT_U));
-    return save ? launch_as(ckpt_save_kernel<DT, EPI>, attr_done, grid, CKPT_T, 0, pdl, s, p)
-                : launch_as(ckpt_load_kernel<DT, EPI>, attr_done, grid, CKPT_T, 0, pdl, s, p);
+    const dim3 grid((p.total + CKPT_T / 4 * U - 1) / (CKPT_T / 4 * U));
+    return save ? launch_as(ckpt_save_kernel<DT, EPI, U>, attr_done, grid, CKPT_T, 0, pdl, s, p)
+                : launch_as(ckpt_load_kernel<DT, EPI, U>, attr_done, grid, CKPT_T, 0, pdl, s, p);
+}
+template <int DT, int EPI>
+cudaError_t ckpt(bool save, const CkptParams &p, bool pdl, cudaStream_t s) {
+    return p.total <= 148 * 8 * 2 * (CKPT_T / 4) ? ckpt<DT, EPI, 1>(save, p, pdl, s) : ckpt<DT, EPI, 4>(save, p, pdl, s);
 }
 template <int DT>
 cudaError_t ckpt_of(bool save, int epi, const CkptParams &p, bool pdl, cudaStream_t s) {
@@ -28,7 +32,10 @@ cudaError_t dact_ckpt(int axis, const DactParams &p, bool pdl, cudaStream_t s) {
     constexpr int SMEM = dact_smem(true), T = 32 * DACT_WARPS;
     const dim3 grid((unsigned)((p.n + DACT_COLS - 1) / DACT_COLS), (unsigned)((p.m + p.rows - 1) / p.rows), 1);
     if (axis == AXIS_ROW && p.dbias != nullptr) {
-        static std::atomic<bool> attr_done[64];
+        static std::atomic<bool> attr_done[64], attr_done2[64];
+        if (p.m < 148 * 3 * DACT_U)
+            return launch_as(dact_rows_kernel<DT, ACT, true, VAL, 2>, attr_done2, dim3((unsigned)((p.m + 1) / 2)), T, dact_smem(true, 2),
+                             pdl, s, p);
         return launch_as(dact_rows_kernel<DT, ACT, true, VAL>, attr_done, dim3((unsigned)((p.m + DACT_U - 1) / DACT_U)), T, SMEM, pdl,
                          s, p);
     }
