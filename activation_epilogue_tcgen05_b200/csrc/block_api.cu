@@ -141,20 +141,21 @@ int run_ckpt(bool save, int64_t m, int64_t n, int dtype, int epilogue, const voi
 
 // Whether dbias's sums go through the workspace.  They do not where they end in a block each: rows whole in a block, or all
 // rows in one run.
-bool dact_needs_workspace(int64_t m, int64_t n, int act, int bias_axis) {
-    return !(bias_axis == GEMM_EPI_BIAS_ROW ? dact_by_rows(m, n) : dact_rows(m, n, dact_reads_z(act)) >= m);
+bool dact_needs_workspace(int64_t m, int64_t n, int blocks, int bias_axis) {
+    return !(bias_axis == GEMM_EPI_BIAS_ROW ? dact_by_rows(m, n) : dact_rows(m, n, blocks) >= m);
 }
 
 // Launches of an epilogue's backward: the strips or whole rows, then what adds their sums up.
 int run_dact(DactParams &p, int64_t m, int64_t n, int dtype, int act, int bias_axis, bool ckpt, void *dbias, void *workspace,
              void *stream) {
-    const bool at_once = dbias && !dact_needs_workspace(m, n, act, bias_axis);
+    const int blocks = dact_blocks(act, ckpt);
+    const bool at_once = dbias && !dact_needs_workspace(m, n, blocks, bias_axis);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int dt = dtype == GEMM_EPI_F16 ? DT_F16 : DT_BF16;      // e4m3 operands have bf16 outputs
     const int axis = bias_axis == GEMM_EPI_BIAS_COL ? AXIS_COL : AXIS_ROW;
     p.m = m;
     p.n = (int)n;
-    p.rows = dact_rows(m, n, dact_reads_z(act));
+    p.rows = dact_rows(m, n, blocks);
     p.partial = dbias && !at_once ? static_cast<float *>(workspace) : nullptr;
     p.dbias = at_once ? dbias : nullptr;
     const bool pdl = pdl_enabled();
@@ -320,7 +321,7 @@ int64_t gemm_epi_dact_workspace_bytes(int64_t m, int64_t n, int bias_axis) {
     if (bias_axis == GEMM_EPI_BIAS_ROW && dact_by_rows(m, n)) return 0;
     if (bias_axis == GEMM_EPI_BIAS_ROW) return (n + DACT_COLS - 1) / DACT_COLS * m * (int64_t)sizeof(float);
     if (bias_axis != GEMM_EPI_BIAS_COL) return 0;
-    const int64_t rows = std::min(dact_rows(m, n, true), dact_rows(m, n, false));      // whatever the epilogue
+    const int64_t rows = std::min(dact_rows(m, n, 3), dact_rows(m, n, 4));      // whatever the epilogue
     return rows >= m ? 0 : (m + rows - 1) / rows * n * (int64_t)sizeof(float);
 }
 
@@ -335,7 +336,7 @@ int gemm_epi_dact(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, 
     const bool mask = act == DACT_RELU_MASK;
     if (!dD || (mask && !aux) || (!mask && act != DACT_NONE && !Z)) return GEMM_EPI_ERR_NULL;
     if (act == DACT_NONE ? !dbias : !dZ) return GEMM_EPI_ERR_NULL;
-    if (dbias && !workspace && dact_needs_workspace(m, n, act, bias_axis)) return GEMM_EPI_ERR_NULL;
+    if (dbias && !workspace && dact_needs_workspace(m, n, dact_blocks(act, false), bias_axis)) return GEMM_EPI_ERR_NULL;
     if (act == DACT_NONE && dZ) return GEMM_EPI_ERR_ARG;          // dZ is dD itself
     if (!aligned(dD, 16) || (act != DACT_NONE && !mask && !aligned(Z, 16)) || (mask && !aligned(aux, 16)) ||
         !aligned(dZ, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
@@ -359,7 +360,7 @@ int gemm_epi_dact_ckpt(int64_t m, int64_t n, int dtype, int epilogue, int bias_a
     const int act = dact_of_epilogue(epilogue);
     if (act == DACT_NONE || act == DACT_RELU_MASK) return GEMM_EPI_ERR_ARG;      // nothing, or the mask, is kept of z
     if (!dD || !codes || !exps || !dZ) return GEMM_EPI_ERR_NULL;
-    if (dbias && !workspace && dact_needs_workspace(m, n, act, bias_axis)) return GEMM_EPI_ERR_NULL;
+    if (dbias && !workspace && dact_needs_workspace(m, n, dact_blocks(act, true), bias_axis)) return GEMM_EPI_ERR_NULL;
     if (H == dZ || codes == dZ || codes == H || exps == dZ || exps == H) return GEMM_EPI_ERR_ARG;
     if (!aligned(dD, 16) || !aligned(codes, 16) || !aligned(dZ, 16) || !aligned(H, 16) || !aligned(dbias, 16) || !aligned(workspace, 16))
         return GEMM_EPI_ERR_ALIGN;

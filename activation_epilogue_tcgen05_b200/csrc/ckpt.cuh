@@ -44,18 +44,15 @@ __device__ __forceinline__ float ckpt_step(uint32_t e) {
 __device__ __forceinline__ float ckpt_inverse(uint32_t e) { return __uint_as_float((260u - e) << 23); }
 
 // Eight codes -> values.  A byte with its sign flipped, in the low bits of 2^23, is 2^23 + 128 + q.
-__device__ __forceinline__ void ckpt_decode8(const uint2 &q, float step, float (&f)[8]) {
+__device__ __forceinline__ void ckpt_decode8(const uint2 &q, float step, f32x2 (&f)[4]) {
     const f32x2 off = both(-8388736.0f), s = both(step);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         const uint32_t w = (h ? q.y : q.x) ^ 0x80808080u;
-        const f32x2 a = pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)), __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)));
-        const f32x2 b = pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)), __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)));
-        const float2 x = split(mul2(add2(a, off), s)), y = split(mul2(add2(b, off), s));
-        f[4 * h] = x.x;
-        f[4 * h + 1] = x.y;
-        f[4 * h + 2] = y.x;
-        f[4 * h + 3] = y.y;
+        f[2 * h] = pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440)), __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7441)));
+        f[2 * h + 1] = pair(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7442)), __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7443)));
+        f[2 * h] = mul2(add2(f[2 * h], off), s);
+        f[2 * h + 1] = mul2(add2(f[2 * h + 1], off), s);
     }
 }
 
@@ -73,15 +70,18 @@ __device__ __forceinline__ f32x2 tanh2(float x0, float x1) {
 
 // act of a thread's eight values.
 template <int EPI>
-__device__ __forceinline__ void ckpt_act8(float (&f)[8]) {
+__device__ __forceinline__ void ckpt_act8(f32x2 (&f)[4]) {
 #pragma unroll
-    for (int e = 0; e < 8; e += 2) {
-        float2 y = make_float2(f[e], f[e + 1]);
-        if constexpr (EPI == EPI_GELU) y = gelu_erf2(f[e], f[e + 1]);
-        else if constexpr (EPI == EPI_TANH) y = split(tanh2(f[e], f[e + 1]));
-        else if constexpr (EPI == EPI_RELU) y = make_float2(f[e] < 0.0f ? 0.0f : f[e], f[e + 1] < 0.0f ? 0.0f : f[e + 1]);
-        f[e] = y.x;
-        f[e + 1] = y.y;
+    for (int e = 0; e < 4; ++e) {
+        const float2 x = split(f[e]);
+        if constexpr (EPI == EPI_GELU) {
+            const float2 y = gelu_erf2(x.x, x.y);
+            f[e] = pair(y.x, y.y);
+        } else if constexpr (EPI == EPI_TANH) {
+            f[e] = tanh2(x.x, x.y);
+        } else if constexpr (EPI == EPI_RELU) {
+            f[e] = pair(x.x < 0.0f ? 0.0f : x.x, x.y < 0.0f ? 0.0f : x.y);
+        }
     }
 }
 
@@ -125,11 +125,12 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_save_kernel(const CkptParams p) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float f[8];
+        f32x2 f[4];
         unpack8<DT>(zv[u], f);
-        uint32_t top = 0u;
+        float big = 0.0f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7FFFFFFFu);
+        for (int e = 0; e < 4; ++e) big = max_abs(big, f[e]);
+        uint32_t top = __float_as_uint(big);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         const uint32_t ex = ckpt_exponent(top), id = id0 + u * (CKPT_T / 4);
@@ -165,12 +166,16 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_load_kernel(const CkptParams p) {
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-        float f[8];
+        f32x2 f[4];
         ckpt_decode8(q[u], ckpt_step(ex[u]), f);
         ckpt_act8<EPI>(f);
         if constexpr (DT == DT_F16) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) f[e] = f[e] > 65504.0f ? 65504.0f : f[e] < -65504.0f ? -65504.0f : f[e];
+            for (int e = 0; e < 4; ++e) {
+                const float2 x = split(f[e]);
+                f[e] = pair(x.x > 65504.0f ? 65504.0f : x.x < -65504.0f ? -65504.0f : x.x,
+                            x.y > 65504.0f ? 65504.0f : x.y < -65504.0f ? -65504.0f : x.y);
+            }
         }
         if (at[u] >= 0) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.h) + at[u]) = pack8<DT>(f);
     }

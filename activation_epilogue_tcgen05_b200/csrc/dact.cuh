@@ -92,40 +92,39 @@ __device__ __forceinline__ f32x2 tanh_slope(float x0, float x1) {
     return mul2(mul2(e, both(4.0f)), mul2(r, r));
 }
 
-// act'(z) of two neighbouring elements.
+// act'(z) of two neighbouring elements; val: act(z) as well, if wanted.
 template <int ACT, bool FINITE>
-__device__ __forceinline__ f32x2 slope(float z0, float z1, f32x2 *val = nullptr) {
-    if constexpr (ACT == DACT_GELU) return gelu_slope<FINITE>(z0, z1, val);
-    if (val != nullptr) *val = tanh2(z0, z1);
-    return tanh_slope(z0, z1);
+__device__ __forceinline__ f32x2 slope(f32x2 z, f32x2 *val = nullptr) {
+    const float2 x = split(z);
+    if constexpr (ACT == DACT_GELU) return gelu_slope<FINITE>(x.x, x.y, val);
+    if (val != nullptr) *val = tanh2(x.x, x.y);
+    return tanh_slope(x.x, x.y);
 }
 
 // d *= act'(z) for a lane's eight elements (bits: their mask); VAL: z becomes act(z).
 template <int ACT, bool FINITE, bool VAL>
-__device__ __forceinline__ void through_act(float (&d)[8], float (&z)[8], uint32_t bits) {
-    if constexpr (ACT == DACT_RELU_MASK) {
+__device__ __forceinline__ void through_act(f32x2 (&d)[4], f32x2 (&z)[4], uint32_t bits) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) d[e] = ((bits >> e) & 1u) ? d[e] : 0.0f;
-    } else if constexpr (ACT == DACT_RELU) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            d[e] = z[e] > 0.0f ? d[e] : 0.0f;
-            if constexpr (VAL) z[e] = z[e] < 0.0f ? 0.0f : z[e];
-        }
-    } else if constexpr (ACT != DACT_NONE) {
-#pragma unroll
-        for (int e = 0; e < 8; e += 2) {
+    for (int e = 0; e < 4; ++e) {
+        if constexpr (ACT == DACT_RELU_MASK) {
+            const float2 f = split(d[e]);
+            d[e] = pair(((bits >> 2 * e) & 1u) ? f.x : 0.0f, ((bits >> (2 * e + 1)) & 1u) ? f.y : 0.0f);
+        } else if constexpr (ACT == DACT_RELU) {
+            const float2 f = split(d[e]), x = split(z[e]);
+            d[e] = pair(x.x > 0.0f ? f.x : 0.0f, x.y > 0.0f ? f.y : 0.0f);
+            if constexpr (VAL) z[e] = pair(x.x < 0.0f ? 0.0f : x.x, x.y < 0.0f ? 0.0f : x.y);
+        } else if constexpr (ACT != DACT_NONE) {
             f32x2 val;
-            const float2 f = split(mul2(pair(d[e], d[e + 1]), slope<ACT, FINITE>(z[e], z[e + 1], VAL ? &val : nullptr)));
-            d[e] = f.x;
-            d[e + 1] = f.y;
-            if constexpr (VAL) {
-                const float2 y = split(val);
-                z[e] = y.x;
-                z[e + 1] = y.y;
-            }
+            d[e] = mul2(d[e], slope<ACT, FINITE>(z[e], VAL ? &val : nullptr));
+            if constexpr (VAL) z[e] = val;
         }
     }
+}
+
+// Sum of a lane's eight elements.
+__device__ __forceinline__ float sum8(const f32x2 (&d)[4]) {
+    const float2 f = split(add2(add2(d[0], d[1]), add2(d[2], d[3])));
+    return f.x + f.y;
 }
 
 // With z to read, rows go through a ring of batches in shared memory, each thread copying its own vectors
@@ -138,130 +137,138 @@ constexpr bool dact_reads_z(int act) { return act != DACT_NONE && act != DACT_RE
 // Where a slope is computed, two rows of a batch are worked out at a time: with all four interleaved the constants no longer
 // fit the 80 registers that three blocks an SM leave (8192 x 14336 GELU 120 us, two at a time 112).
 constexpr bool dact_computes(int act) { return act == DACT_GELU || act == DACT_TANH; }
+// Blocks an SM.  From a checkpoint two, at up to 128 registers: a batch's four rows are worked out together (rows whole in a
+// block and act(z) as well: two by two), with the codes taken apart and act(z) on top of the slope's constants (8192 x 14336
+// GELU with act(z) 136 us; three blocks, two rows at a time 157, one at a time 140; without act(z) 107 and 109).
+constexpr int dact_blocks(int act, bool ck) { return ck ? 2 : dact_reads_z(act) ? 3 : 4; }
 constexpr int DACT_RING = 2;
 constexpr int dact_smem(bool ck, int u = DACT_U) { return DACT_RING * u * 32 * DACT_WARPS * (ck ? 24 : 32); }
 
-// What a thread has of one row of a stage in the ring: [DACT_RING][U][T] of dD, then as many of z or of its codes.
+// What a thread has of one row of a stage in the ring: [DACT_RING][U][T] of dD, then as many of z or of its codes.  Where there is
+// no row (or column) left the thread puts zeros there, so that nothing that is read has to be asked about: 0 adds nothing
+// to a sum.
 template <bool CK, int U = DACT_U>
 struct DactRing {
     using Zv = std::conditional_t<CK, uint2, uint4>;
-    static constexpr int N = DACT_RING * U * 32 * DACT_WARPS;
-    static __device__ __forceinline__ uint4 *dd(uint4 *ring, int stage, int u) {
-        return ring + (stage * U + u) * 32 * DACT_WARPS + threadIdx.x;
-    }
+    using Zg = std::conditional_t<CK, int8_t, uint16_t>;
+    static constexpr int T = 32 * DACT_WARPS, N = DACT_RING * U * T;
+    static __device__ __forceinline__ uint4 *dd(uint4 *ring, int stage, int u) { return ring + (stage * U + u) * T + threadIdx.x; }
     static __device__ __forceinline__ Zv *z(uint4 *ring, int stage, int u) {
-        return reinterpret_cast<Zv *>(ring + N) + (stage * U + u) * 32 * DACT_WARPS + threadIdx.x;
+        return reinterpret_cast<Zv *>(ring + N) + (stage * U + u) * T + threadIdx.x;
+    }
+    static __device__ __forceinline__ void fetch(uint4 *ring, int stage, int u, bool ok, const uint16_t *from, const Zg *zfrom) {
+        if (ok) {
+            ptx::cp_async_16(dd(ring, stage, u), from);
+            if constexpr (CK) ptx::cp_async_8(z(ring, stage, u), zfrom);
+            else ptx::cp_async_16(z(ring, stage, u), zfrom);
+        } else {
+            *dd(ring, stage, u) = make_uint4(0u, 0u, 0u, 0u);
+            *z(ring, stage, u) = Zv{};
+        }
+    }
+    // z as values; ex: its exponent (CK)
+    template <int DT>
+    static __device__ __forceinline__ void values(uint4 *ring, int stage, int u, uint32_t ex, f32x2 (&f)[4]) {
+        if constexpr (CK) ckpt_decode8(*z(ring, stage, u), ckpt_step(ex), f);
+        else unpack8<DT>(*z(ring, stage, u), f);
     }
 };
 
-// A lane's eight values of z in the ring (ok: whether they are there); ex: CK, their exponent.
-template <int DT, bool CK, int U = DACT_U>
-__device__ __forceinline__ void dact_z(uint4 *ring, int stage, int u, bool ok, uint32_t ex, float (&z)[8]) {
-    if constexpr (CK) ckpt_decode8(ok ? *DactRing<CK, U>::z(ring, stage, u) : make_uint2(0u, 0u), ckpt_step(ok ? ex : 7u), z);
-    else unpack8<DT>(ok ? *DactRing<CK, U>::z(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), z);
-}
-
 template <int DT, int ACT, int AXIS, bool CK = false, bool VAL = false>
-__global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_kernel(const DactParams p) {
-    constexpr int T = 32 * DACT_WARPS, U = DACT_U;
+__global__ void __launch_bounds__(32 * DACT_WARPS, dact_blocks(ACT, CK)) dact_kernel(const DactParams p) {
+    constexpr int U = DACT_U;
     constexpr bool Z = dact_reads_z(ACT), SLOPE = dact_computes(ACT);
     static_assert(Z || !CK, "a checkpoint is one of z");
-    (void)T;
-    extern __shared__ uint4 ring[];                   // Z: DactRing
+    using Ring = DactRing<CK>;
+    extern __shared__ uint4 ring[];                   // Z: Ring
     __shared__ float4 sums[AXIS == AXIS_COL ? 64 * DACT_WARPS : 1];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int col = blockIdx.x * DACT_COLS + 8 * lane;
     const bool col_ok = col < p.n;                    // n is a multiple of 8
-    const int64_t r0 = (int64_t)blockIdx.y * p.rows, r1 = min(p.m, r0 + p.rows);
+    const int64_t r0 = (int64_t)blockIdx.y * p.rows + warp;
+    // the warp's rows: every DACT_WARPS-th of the run's; `at` is where this lane's values of one lie
+    const int rows = (int)min(p.rows, p.m - (int64_t)blockIdx.y * p.rows);
+    constexpr int step = U * DACT_WARPS;
+    const int64_t pitch = (int64_t)DACT_WARPS * p.n;
+    int64_t at = r0 * p.n + col;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
-    auto fetch = [&](int64_t row, int stage) {
+    const uint16_t *dd = static_cast<const uint16_t *>(p.dd);
+    auto fetch = [&](int r, int64_t at, int stage) {
+        const typename Ring::Zg *z = reinterpret_cast<const typename Ring::Zg *>(CK ? static_cast<const void *>(p.codes) : p.z);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = row + u * DACT_WARPS;
-            if (i < r1 && col_ok) {
-                ptx::cp_async_16(DactRing<CK>::dd(ring, stage, u), static_cast<const uint16_t *>(p.dd) + i * p.n + col);
-                if constexpr (CK) ptx::cp_async_8(DactRing<CK>::z(ring, stage, u), p.codes + i * p.n + col);
-                else ptx::cp_async_16(DactRing<CK>::z(ring, stage, u), static_cast<const uint16_t *>(p.z) + i * p.n + col);
-            }
-        }
-        ptx::cp_async_commit();                       // (an empty group keeps the count)
+        for (int u = 0; u < U; ++u, at += pitch) Ring::fetch(ring, stage, u, r + u * DACT_WARPS < rows && col_ok, dd + at, z + at);
+        ptx::cp_async_commit();
     };
+    // CK: the coming batch's exponents
+    uint32_t next[U];
     const int groups = ckpt_groups(p.n);
-    uint32_t next[U] = {};                            // CK: the coming batch's exponents
-    auto exponents = [&](int64_t row) {
+    const uint8_t *ex_at = CK ? p.exps + r0 * groups + col / CKPT_GROUP : nullptr;
+    auto exponents = [&](int r) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t i = row + u * DACT_WARPS;
-            if (i < r1 && col_ok) next[u] = __ldg(p.exps + i * groups + col / CKPT_GROUP);
+            next[u] = 7u;
+            if (r + u * DACT_WARPS < rows && col_ok) next[u] = __ldg(ex_at + (int64_t)(u * DACT_WARPS) * groups);
         }
+        ex_at += (int64_t)step * groups;
     };
-    float acc[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.0f;
-    int64_t row = r0 + warp;
-    constexpr int64_t step = U * DACT_WARPS;
+    f32x2 acc[4] = {both(0.0f), both(0.0f), both(0.0f), both(0.0f)};
+    int r = warp;
     if constexpr (Z) {
 #pragma unroll
-        for (int i = 0; i < DACT_RING; ++i) fetch(row + i * step, i);
-        if constexpr (CK) exponents(row);
+        for (int i = 0; i < DACT_RING; ++i) fetch(r + i * step, at + i * U * pitch, i);
+        if constexpr (CK) exponents(r);
     }
     int stage = 0;
-    for (; row < r1; row += step) {
+    for (; r < rows; r += step, at += U * pitch) {
         uint4 dv[U];
         uint32_t bits[U], ex = 0u;                    // the mask's; CK: the rows' exponents, a byte each
         if constexpr (Z) {
             if constexpr (CK) {
                 ex = next[0] | next[1] << 8 | next[2] << 16 | next[3] << 24;
-                exponents(row + step);
+                exponents(r + step);
             }
             ptx::cp_async_wait<DACT_RING - 1>();
         } else {
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const int64_t i = row + u * DACT_WARPS;
                 dv[u] = make_uint4(0u, 0u, 0u, 0u);
                 bits[u] = 0u;
-                if (i < r1 && col_ok) {
-                    dv[u] = ptx::ld_stream(static_cast<const uint16_t *>(p.dd) + i * p.n + col);
-                    if constexpr (ACT == DACT_RELU_MASK) bits[u] = __ldg(p.aux + i * p.aux_pitch + col / 8);
+                if (r + u * DACT_WARPS < rows && col_ok) {
+                    dv[u] = ptx::ld_stream(dd + at + u * pitch);
+                    if constexpr (ACT == DACT_RELU_MASK) bits[u] = __ldg(p.aux + (r0 - warp + r + u * DACT_WARPS) * p.aux_pitch + col / 8);
                 }
             }
         }
-#pragma unroll (SLOPE ? 2 : U)
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = row + u * DACT_WARPS;
-            const bool ok = i < r1 && col_ok;
-            float d[8], z[8];
+        int64_t to = at;
+        constexpr int AT_ONCE = SLOPE && !CK ? 2 : U;
+#pragma unroll AT_ONCE
+        for (int u = 0; u < U; ++u, to += pitch) {
+            const bool row_ok = r + u * DACT_WARPS < rows;
+            f32x2 d[4], z[4];
             if constexpr (Z) {
-                unpack8<DT>(ok ? *DactRing<CK>::dd(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), d);
-                dact_z<DT, CK>(ring, stage, u, ok, ex >> 8 * u & 255u, z);
+                unpack8<DT>(*Ring::dd(ring, stage, u), d);
+                Ring::template values<DT>(ring, stage, u, ex >> 8 * u & 255u, z);
             } else {
                 unpack8<DT>(dv[u], d);
             }
             through_act<ACT, CK, VAL>(d, z, bits[u]);
-            if constexpr (ACT != DACT_NONE) {
-                if (ok) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + i * p.n + col) = pack8<DT>(d);
-            }
-            if constexpr (VAL) {
-                if (ok) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.h) + i * p.n + col) = pack8<DT>(z);
+            if (row_ok && col_ok) {
+                if constexpr (ACT != DACT_NONE) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + to) = pack8<DT>(d);
+                if constexpr (VAL) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.h) + to) = pack8<DT>(z);
             }
             if constexpr (AXIS == AXIS_COL) {
 #pragma unroll
-                for (int e = 0; e < 8; e += 2) {
-                    const float2 f = split(add2(pair(acc[e], acc[e + 1]), pair(d[e], d[e + 1])));
-                    acc[e] = f.x;
-                    acc[e + 1] = f.y;
-                }
+                for (int e = 0; e < 4; ++e) acc[e] = add2(acc[e], d[e]);
             } else if (p.partial != nullptr) {
-                float s = ((d[0] + d[1]) + (d[2] + d[3])) + ((d[4] + d[5]) + (d[6] + d[7]));
+                float s = sum8(d);
 #pragma unroll
                 for (int sh = 16; sh >= 1; sh >>= 1) s += __shfl_xor_sync(0xffffffffu, s, sh);
-                if (lane == 0 && i < r1) p.partial[(int64_t)blockIdx.x * p.m + i] = s;
+                if (lane == 0 && row_ok) p.partial[(int64_t)blockIdx.x * p.m + (r0 - warp + r + u * DACT_WARPS)] = s;
             }
         }
         if constexpr (Z) {
-            fetch(row + DACT_RING * step, stage);
+            fetch(r + DACT_RING * step, at + DACT_RING * U * pitch, stage);
             if (++stage == DACT_RING) stage = 0;
         }
     }
@@ -269,8 +276,8 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
     if constexpr (AXIS == AXIS_COL) {
         if (p.partial == nullptr && p.dbias == nullptr) return;
         // the warps' sums, in order: [warp][half of a lane's 8][lane]
-        sums[(2 * warp) * 32 + lane] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        sums[(2 * warp + 1) * 32 + lane] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        sums[(2 * warp) * 32 + lane] = quad(acc[0], acc[1]);
+        sums[(2 * warp + 1) * 32 + lane] = quad(acc[2], acc[3]);
         __syncthreads();
         if (threadIdx.x < 64 && col_ok) {             // (threads 32 to 63: the second halves)
             float4 a = sums[threadIdx.x];
@@ -291,47 +298,42 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
     }
 }
 
-// The bias along the rows: a block takes DACT_U rows whole, its warps side by side on 2048 columns at a
+// The bias along the rows: a block takes U rows whole, its warps side by side on 2048 columns at a
 // time, so that a row's sum ends in the block and dbias is written at once: one launch, no scratch, and one
 // butterfly a row instead of one every 256 columns (8192 x 14336 ReLU 106 us against 115, 1023 x 4104 from the
 // mask 6.7 us a call from Python against 11.0).  The same ring, along the columns.
 template <int DT, int ACT, bool CK = false, bool VAL = false, int U = DACT_U>
-__global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) dact_rows_kernel(const DactParams p) {
+__global__ void __launch_bounds__(32 * DACT_WARPS, U == DACT_U ? dact_blocks(ACT, CK) : 3) dact_rows_kernel(const DactParams p) {
     constexpr int PASS = DACT_WARPS * DACT_COLS;
     constexpr bool Z = dact_reads_z(ACT), SLOPE = dact_computes(ACT);
     static_assert(U % 2 == 0 && U <= 4, "rows are worked out two at a time; their exponents share a word");
     static_assert(Z || !CK, "a checkpoint is one of z");
-    extern __shared__ uint4 ring[];                   // Z: DactRing
+    using Ring = DactRing<CK, U>;
+    extern __shared__ uint4 ring[];                   // Z: Ring
     __shared__ float sums[DACT_WARPS][U];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r0 = (int64_t)blockIdx.x * U;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
     const uint16_t *dd = static_cast<const uint16_t *>(p.dd) + r0 * p.n;
-    const uint16_t *zz = Z && !CK ? static_cast<const uint16_t *>(p.z) + r0 * p.n : nullptr;
-    const int8_t *codes = CK ? p.codes + r0 * p.n : nullptr;
-    uint16_t *hh = VAL ? static_cast<uint16_t *>(p.h) + r0 * p.n : nullptr;
+    const typename Ring::Zg *zz = reinterpret_cast<const typename Ring::Zg *>(CK ? static_cast<const void *>(p.codes) : p.z) + (Z ? r0 * p.n : 0);
     uint16_t *dz = static_cast<uint16_t *>(p.dz) + r0 * p.n;
+    uint16_t *hh = VAL ? static_cast<uint16_t *>(p.h) + r0 * p.n : nullptr;
     const int rows = (int)min((int64_t)U, p.m - r0);
     auto fetch = [&](int64_t col, int stage) {
-        if (col < p.n) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                if (u < rows) {
-                    ptx::cp_async_16(DactRing<CK, U>::dd(ring, stage, u), dd + (int64_t)u * p.n + col);
-                    if constexpr (CK) ptx::cp_async_8(DactRing<CK, U>::z(ring, stage, u), codes + (int64_t)u * p.n + col);
-                    else ptx::cp_async_16(DactRing<CK, U>::z(ring, stage, u), zz + (int64_t)u * p.n + col);
-                }
-            }
-        }
+        for (int u = 0; u < U; ++u)
+            Ring::fetch(ring, stage, u, u < rows && col < p.n, dd + (int64_t)u * p.n + col, zz + (int64_t)u * p.n + col);
         ptx::cp_async_commit();
     };
     const int groups = ckpt_groups(p.n);
-    uint32_t next[U] = {};                            // CK: the coming pass's exponents
+    uint32_t next[U];                                 // CK: the coming pass's exponents
     auto exponents = [&](int64_t col) {
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            next[u] = 7u;
             if (u < rows && col < p.n) next[u] = __ldg(p.exps + (r0 + u) * groups + col / CKPT_GROUP);
+        }
     };
     float acc[U];
 #pragma unroll
@@ -348,7 +350,6 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
         uint32_t bits[U], ex = 0u;                    // the mask's; CK: the rows' exponents, a byte each
         if constexpr (Z) {
             if constexpr (CK) {
-                ex = 0u;
 #pragma unroll
                 for (int u = 0; u < U; ++u) ex |= next[u] << 8 * u;
                 exponents(col + PASS);
@@ -366,27 +367,26 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_reads_z(ACT) ? 3 : 4) da
             }
         }
         // (two rows at a time; their sums go round, so that each is in its place again after the batch)
-#pragma unroll (SLOPE ? 1 : U / 2)
+        constexpr int AT_ONCE = SLOPE && (!CK || VAL) ? 1 : U / 2;
+#pragma unroll AT_ONCE
         for (int u0 = 0; u0 < U; u0 += 2) {
             float sum[2];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int u = u0 + k;
-                float d[8], z[8];
+                f32x2 d[4], z[4];
                 if constexpr (Z) {
-                    unpack8<DT>(u < rows ? *DactRing<CK, U>::dd(ring, stage, u) : make_uint4(0u, 0u, 0u, 0u), d);
-                    dact_z<DT, CK, U>(ring, stage, u, u < rows, ex >> 8 * u & 255u, z);
+                    unpack8<DT>(*Ring::dd(ring, stage, u), d);
+                    Ring::template values<DT>(ring, stage, u, ex >> 8 * u & 255u, z);
                 } else {
                     unpack8<DT>(dv[u], d);
                 }
                 through_act<ACT, CK, VAL>(d, z, bits[u]);
-                if constexpr (ACT != DACT_NONE) {
-                    if (u < rows) *reinterpret_cast<uint4 *>(dz + (int64_t)u * p.n + col) = pack8<DT>(d);
+                if (u < rows) {
+                    if constexpr (ACT != DACT_NONE) *reinterpret_cast<uint4 *>(dz + (int64_t)u * p.n + col) = pack8<DT>(d);
+                    if constexpr (VAL) *reinterpret_cast<uint4 *>(hh + (int64_t)u * p.n + col) = pack8<DT>(z);
                 }
-                if constexpr (VAL) {
-                    if (u < rows) *reinterpret_cast<uint4 *>(hh + (int64_t)u * p.n + col) = pack8<DT>(z);
-                }
-                sum[k] = acc[k] + (((d[0] + d[1]) + (d[2] + d[3])) + ((d[4] + d[5]) + (d[6] + d[7])));
+                sum[k] = acc[k] + sum8(d);
             }
 #pragma unroll
             for (int k = 0; k < U - 2; ++k) acc[k] = acc[k + 2];

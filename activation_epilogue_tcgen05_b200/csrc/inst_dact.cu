@@ -7,15 +7,15 @@
 namespace gemm_epi {
 
 // Rows of a run: nearly whole waves of blocks -- three of three blocks an SM where z is read, two of
-// four elsewhere, on 148 SMs -- or runs of one batch of 32 rows.  With one wave some SMs have a block more
+// four elsewhere and four of two from a checkpoint, on 148 SMs -- or runs of one batch of 32 rows.  With one wave some SMs have a block more
 // than others, and nothing evens that out (8192 x 14336 GELU: 392 blocks 135 us, 1288 blocks 115); a wave
 // with few blocks costs most of one (from the mask: 1120 blocks 86 us, 1232 blocks 99).  Up to 64 rows are
 // one run, which writes dbias itself (64 x 4096 GELU: 3.6 us, 6.7 a call from Python; by two launches 4.1 and
 // 11; 128 x 4096 would take 6.1 us against 4.3).
-int64_t dact_rows(int64_t m, int64_t n, bool reads_z) {
+int64_t dact_rows(int64_t m, int64_t n, int blocks_sm) {
     const int64_t strips = (n + DACT_COLS - 1) / DACT_COLS, batches = (m + 31) / 32;
     if (batches <= 2) return batches * 32;
-    const int64_t blocks = 148 * (reads_z ? 9 : 8);
+    const int64_t blocks = 148 * (blocks_sm == 3 ? 9 : 8);
     const int64_t runs = std::max<int64_t>(1, std::min<int64_t>(blocks / strips, batches));
     return (batches + runs - 1) / runs * 32;
 }

@@ -98,8 +98,8 @@ cudaError_t launch_add_parts(int dt, const float *src, int64_t parts, int64_t le
 cudaError_t launch_add_parts2(int dt, const float *src, int64_t parts, int64_t len, void *out, void *out2, int64_t cut, bool pdl,
                               cudaStream_t s);
 cudaError_t launch_zero_word(unsigned int *w, bool pdl, cudaStream_t s);
-// rows of a block's run, from the sizes and whether z is read; the launch has ceil(m / rows) runs
-int64_t dact_rows(int64_t m, int64_t n, bool reads_z);
+// rows of a block's run, from the sizes and the kernel's blocks an SM (2, 3 or 4); the launch has ceil(m / rows) runs
+int64_t dact_rows(int64_t m, int64_t n, int blocks);
 // ROW axis: whether the launch writes dbias itself (DactParams::dbias), without partials
 bool dact_by_rows(int64_t m, int64_t n);
 cudaError_t launch_dact(int dt, int act, int axis, const DactParams &p, bool pdl, cudaStream_t s);

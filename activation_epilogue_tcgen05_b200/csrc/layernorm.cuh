@@ -39,17 +39,6 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// The largest of a and the magnitudes of a pair (NaN where there is one).
-__device__ __forceinline__ float max_abs(float a, f32x2 v) {
-    const float2 f = split(v);
-    float r;
-    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(f.x), "f"(f.y));
-    return r;
-}
-__device__ __forceinline__ float4 quad(f32x2 a, f32x2 b) {
-    const float2 x = split(a), y = split(b);
-    return make_float4(x.x, x.y, y.x, y.y);
-}
 __device__ __forceinline__ float halves(f32x2 v) {
     const float2 f = split(v);
     return f.x + f.y;

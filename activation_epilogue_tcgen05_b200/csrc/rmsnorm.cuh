@@ -86,6 +86,19 @@ __device__ __forceinline__ uint4 pack8(const f32x2 (&f)[4]) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+__device__ __forceinline__ float4 quad(f32x2 a, f32x2 b) {
+    const float2 x = split(a), y = split(b);
+    return make_float4(x.x, x.y, y.x, y.y);
+}
+
+// The largest of a and the magnitudes of a pair (NaN where there is one).
+__device__ __forceinline__ float max_abs(float a, f32x2 v) {
+    const float2 f = split(v);
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(f.x), "f"(f.y));
+    return r;
+}
+
 // Eight values times mul as 8-bit codes of the output type.  Integers (|v mul| within half of 127): 1.5 * 2^23 is added, which
 // leaves the nearest integer, ties to even, in the sum's low byte; one rounding, of the product.
 template <int OUT>
