@@ -11,7 +11,9 @@ template <int DT, int OUT, int TPR, int VPT>
 cudaError_t fwd(const LnParams &p, bool pdl, cudaStream_t s) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR;
     static std::atomic<bool> attr_done[64];
-    return launch_as(layernorm_kernel<DT, OUT, TPR, VPT>, attr_done, dim3((unsigned)((p.m + RPB - 1) / RPB)), T, 0, pdl, s, p);
+    const dim3 grid((unsigned)((p.m + RPB - 1) / RPB));
+    return p.d == 8 * TPR * VPT ? launch_as(layernorm_kernel<DT, OUT, TPR, VPT, true>, attr_done, grid, T, 0, pdl, s, p)
+                                : launch_as(layernorm_kernel<DT, OUT, TPR, VPT, false>, attr_done, grid, T, 0, pdl, s, p);
 }
 
 // The root-mean-square norm's shapes.
@@ -92,15 +94,18 @@ BwdShape bwd_shape(int64_t m, int64_t d) {
 template <int DT, int TPR, int VPT, int T = 512>
 cudaError_t bwd_one(const LnBwdParams &p, int64_t grid, bool pdl, cudaStream_t s) {
     constexpr int SMEM = ln_ring_bytes(T, VPT, false);
-    static std::atomic<bool> attr_done[64];
-    return launch_as(layernorm_bwd_kernel<DT, TPR, VPT, T>, attr_done, dim3((unsigned)grid), T, SMEM, pdl, s, p);
+    static std::atomic<bool> attr_done[64], attr_done_full[64];
+    if constexpr (VPT > 1)                            // (few rows: the call's latency, whatever their length)
+        if (p.d == 8 * TPR * VPT)
+            return launch_as(layernorm_bwd_kernel<DT, TPR, VPT, T, true>, attr_done_full, dim3((unsigned)grid), T, SMEM, pdl, s, p);
+    return launch_as(layernorm_bwd_kernel<DT, TPR, VPT, T, false>, attr_done, dim3((unsigned)grid), T, SMEM, pdl, s, p);
 }
 
 template <int DT, int TPR>
 cudaError_t bwd_cluster(const LnBwdParams &p, bool pdl, cudaStream_t s) {
     constexpr int SMEM = ln_ring_bytes(NORM_CLUSTER_T, 1, true);
     static std::atomic<bool> attr_done[64];
-    return launch_as_cluster(layernorm_bwd_kernel<DT, TPR, 1, NORM_CLUSTER_T, true>, attr_done, dim3(NORM_CLUSTER), NORM_CLUSTER_T, SMEM, pdl,
+    return launch_as_cluster(layernorm_bwd_kernel<DT, TPR, 1, NORM_CLUSTER_T, false, true>, attr_done, dim3(NORM_CLUSTER), NORM_CLUSTER_T, SMEM, pdl,
                              NORM_CLUSTER, s, p);
 }
 

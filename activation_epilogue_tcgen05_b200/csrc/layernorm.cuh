@@ -121,19 +121,21 @@ __device__ __forceinline__ float row_max(float a, float *red, int grp) {
     return a;
 }
 
-// Blocks an SM that the forward kernel is compiled for: 24 warps at 80 registers (8192 x 4096 bf16 + residual to e4m3 by rows 39.4 us;
+// FULL: rows of exactly 8 TPR VPT elements (the powers of two from 128 on), without a question at each vector whether it is there
+// and zeros where it is not: 8192 x 4096 bf16 + residual to e4m3 by rows 38.0 us, 39.4 with them.
+// Blocks an SM that the forward kernel is compiled for: 24 warps at 80 registers (the same case, not FULL, 39.4 us;
 // left to itself the compiler takes as many and orders them worse, 41.8; 28 and 32 warps spill, 41.2 and 65.7).
 constexpr int ln_blocks(int threads) { return threads >= 512 ? 1 : 768 / threads; }
 
-template <int DT, int OUT, int TPR, int VPT>
+template <int DT, int OUT, int TPR, int VPT, bool FULL>
 __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR))) layernorm_kernel(const LnParams p) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR, NW = TPR > 32 ? TPR / 32 : 1;
     __shared__ __align__(16) float red1[RPB][NW], redm[RPB][NW];
     __shared__ __align__(16) f32x2 red2[RPB][NW];
     const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
     const int64_t row = (int64_t)blockIdx.x * RPB + grp;
-    const bool row_ok = row < p.m;
-    const int nvec = p.d / 8;
+    const bool row_ok = RPB == 1 || row < p.m;
+    const int nvec = FULL ? TPR * VPT : p.d / 8;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
 
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR)
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = j * TPR + t;
-        xv[j] = rv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (RPB > 1 || !FULL) xv[j] = rv[j] = make_uint4(0u, 0u, 0u, 0u);
         if (row_ok && v < nvec) {
             xv[j] = ptx::ld_stream(static_cast<const uint16_t *>(p.x) + base + 8 * v);
             if (p.r != nullptr) rv[j] = ptx::ld_stream(static_cast<const uint16_t *>(p.r) + base + 8 * v);
@@ -171,11 +173,10 @@ __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR)
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int v = j * TPR + t;
-        gv[j] = bv[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (v < nvec) {
-            gv[j] = __ldg(static_cast<const uint4 *>(p.gamma) + v);
-            if (p.beta != nullptr) bv[j] = __ldg(static_cast<const uint4 *>(p.beta) + v);
-        }
+        if (!FULL) gv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (v < nvec) gv[j] = __ldg(static_cast<const uint4 *>(p.gamma) + v);
+        bv[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (v < nvec && p.beta != nullptr) bv[j] = __ldg(static_cast<const uint4 *>(p.beta) + v);
     }
     f32x2 ss2 = both(0.0f), left2 = both(0.0f);
 #pragma unroll
@@ -287,29 +288,30 @@ __global__ void __launch_bounds__(norm_threads(TPR)) quant_rows_kernel(const Nor
 constexpr int ln_ring(bool cluster) { return cluster ? 4 : 2; }
 constexpr int ln_ring_bytes(int threads, int vpt, bool cluster) { return ln_ring(cluster) * 3 * threads * vpt * 16; }
 
-template <int DT, int TPR, int VPT, int T, bool CLUSTER = false>
+template <int DT, int TPR, int VPT, int T, bool FULL, bool CLUSTER = false>
 __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p) {
     constexpr int RPB = T / TPR, RING = ln_ring(CLUSTER);
     constexpr int ARRAY = T * VPT;                    // vectors of one array in a stage of the ring
     constexpr int NW = TPR > 32 ? TPR / 32 : 1;
     extern __shared__ uint4 ring[];                   // [RING][dy, s, ds][vector][thread]
     __shared__ __align__(16) f32x2 red1[RPB][NW], red2[RPB][NW];     // (either is read before the other's next barrier)
-    const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR, nvec = p.d / 8;
+    const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR, nvec = FULL ? TPR * VPT : p.d / 8;
     const bool skip = p.ds != nullptr;
     ptx::griddep_wait();
     ptx::griddep_launch_dependents();
+    // (zeros behind a row's end and in the place of rows behind the last: they add nothing to a sum)
     auto fetch = [&](int64_t row, int stage) {
-        if (row < p.m) {
-            const int64_t base = row * p.d;
+        const int64_t base = row * p.d;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                const int v = j * TPR + t;
-                if (v < nvec) {
-                    uint4 *dst = ring + stage * 3 * ARRAY + j * T + threadIdx.x;
-                    ptx::cp_async_16(dst, static_cast<const uint16_t *>(p.dy) + base + 8 * v);
-                    ptx::cp_async_16(dst + ARRAY, static_cast<const uint16_t *>(p.s) + base + 8 * v);
-                    if (skip) ptx::cp_async_16(dst + 2 * ARRAY, static_cast<const uint16_t *>(p.ds) + base + 8 * v);
-                }
+        for (int j = 0; j < VPT; ++j) {
+            const int v = j * TPR + t;
+            uint4 *dst = ring + stage * 3 * ARRAY + j * T + threadIdx.x;
+            if (row < p.m && v < nvec) {
+                ptx::cp_async_16(dst, static_cast<const uint16_t *>(p.dy) + base + 8 * v);
+                ptx::cp_async_16(dst + ARRAY, static_cast<const uint16_t *>(p.s) + base + 8 * v);
+                if (skip) ptx::cp_async_16(dst + 2 * ARRAY, static_cast<const uint16_t *>(p.ds) + base + 8 * v);
+            } else {
+                dst[0] = dst[ARRAY] = dst[2 * ARRAY] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         ptx::cp_async_commit();                       // (an empty group keeps the count)
@@ -348,17 +350,15 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
         f32x2 mu2 = both(0.0f), ma2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (row_ok && j * TPR + t < nvec) {
-                f32x2 av[4], sv[4];
-                load(j, av, sv);
+            f32x2 av[4], sv[4];
+            load(j, av, sv);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    mu2 = add2(mu2, sv[e]);
-                    ma2 = add2(ma2, av[e]);
-                    if constexpr (HOLD) {
-                        a[j][e] = av[e];
-                        c[j][e] = sv[e];
-                    }
+            for (int e = 0; e < 4; ++e) {
+                mu2 = add2(mu2, sv[e]);
+                ma2 = add2(ma2, av[e]);
+                if constexpr (HOLD) {
+                    a[j][e] = av[e];
+                    c[j][e] = sv[e];
                 }
             }
         }
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
         f32x2 ss2 = both(0.0f), as2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            if (row_ok && j * TPR + t < nvec) {
+            if (j * TPR + t < nvec) {                     // (behind the row's end there is no difference)
                 f32x2 av[4], sv[4];
                 if constexpr (!HOLD) load(j, av, sv);
 #pragma unroll
