@@ -123,9 +123,12 @@ __device__ __forceinline__ float row_max(float a, float *red, int grp) {
 
 // FULL: rows of exactly 8 TPR VPT elements (the powers of two from 128 on), without a question at each vector whether it is there
 // and zeros where it is not: 8192 x 4096 bf16 + residual to e4m3 by rows 38.0 us, 39.4 with them.
-// Blocks an SM that the forward kernel is compiled for: 24 warps at 80 registers (the same case, not FULL, 39.4 us;
-// left to itself the compiler takes as many and orders them worse, 41.8; 28 and 32 warps spill, 41.2 and 65.7).
-constexpr int ln_blocks(int threads) { return threads >= 512 ? 1 : 768 / threads; }
+// Blocks an SM that the forward kernel is compiled for: 24 warps at 80 registers (the same case, not FULL, 39.4 us; left to itself
+// the compiler takes as many and orders them worse, 41.8; 28 and 32 warps spilled), and two blocks of the longest rows' 512 threads
+// at 64, which take g and b only where they are used (4096 x 14336 bf16 61 us, by one block at a time 85; with residual
+// to e4m3 by rows 71 and 102).
+constexpr int ln_blocks(int threads) { return threads >= 512 ? 2 : 768 / threads; }
+constexpr bool ln_late(int threads) { return threads >= 512; }
 
 template <int DT, int OUT, int TPR, int VPT, bool FULL>
 __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR))) layernorm_kernel(const LnParams p) {
@@ -170,13 +173,17 @@ __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR)
     const float mu = row_sum<TPR, T>(halves(sum), red1[grp], grp) * p.inv_d;
     // (g and b, the same for every row, are asked for now: they take the registers that x and r had)
     uint4 gv[VPT], bv[VPT];
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
+    auto load_gb = [&](int j) {
         const int v = j * TPR + t;
         if (!FULL) gv[j] = make_uint4(0u, 0u, 0u, 0u);
         if (v < nvec) gv[j] = __ldg(static_cast<const uint4 *>(p.gamma) + v);
         bv[j] = make_uint4(0u, 0u, 0u, 0u);
         if (v < nvec && p.beta != nullptr) bv[j] = __ldg(static_cast<const uint4 *>(p.beta) + v);
+    };
+    constexpr bool LATE = ln_late(T);
+    if constexpr (!LATE) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) load_gb(j);
     }
     f32x2 ss2 = both(0.0f), left2 = both(0.0f);
 #pragma unroll
@@ -198,6 +205,7 @@ __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR)
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         f32x2 g[4], b[4];
+        if constexpr (LATE) load_gb(j);
         unpack8<DT>(gv[j], g);
         unpack8<DT>(bv[j], b);
 #pragma unroll
