@@ -292,7 +292,10 @@ __global__ void __launch_bounds__(norm_threads(TPR), (LONG ? 1024 : 1536) / norm
 
 // Backward: rows dealt and fetched as by rmsnorm_bwd_kernel.  A thread keeps the sums of both gradients of its
 // columns, so it has two vectors of a row where that kernel has four, and holds a and s - mu in registers through the two
-// reductions; with four vectors (rows beyond 8192) they are taken from the ring again.
+// reductions; with three or four vectors they are taken from the ring again.  What bounds it is the chain of a row's two
+// reductions, with two rows at a time on an SM: 8192 x 4096 with the skip gradient 44.7 us, 6.0 TB/s, and 4.5 for the second launch;
+// 4096 x 8192 (one row at a time) 59, 2340 x 14336 65 of 41 at a copy's rate.  (Three or four rows in the ring, 1024 threads of one
+// vector, four rows of 128 threads: none faster.)
 constexpr int ln_ring(bool cluster) { return cluster ? 4 : 2; }
 constexpr int ln_ring_bytes(int threads, int vpt, bool cluster) { return ln_ring(cluster) * 3 * threads * vpt * 16; }
 

@@ -563,7 +563,7 @@ int gemm_epi_quant_rows(int64_t m, int64_t d, int dtype, int out_mode, const voi
 int64_t gemm_epi_ckpt_groups(int64_t n);
 
 /* Keep Z (m, n) as codes and exps; H = act(Z) in the 16-bit type beside them (the next product's operand; NULL: not wanted; may
- * be Z).  H is of z itself, not of what is kept. */
+ * be Z).  H is of z itself, not of what is kept, and as the plans' epilogue has it: Z finite. */
 int gemm_epi_ckpt_save(int64_t m, int64_t n, int dtype, int epilogue, const void *Z, void *H, int8_t *codes, uint8_t *exps,
                        void *stream);
 

@@ -128,7 +128,7 @@ def test_offsets_beyond_32_bits():
 @pytest.mark.parametrize("recompute", [False, True])
 @pytest.mark.parametrize("axis", ["row", "col", None])
 @pytest.mark.parametrize("epilogue", ["relu_bias", "gelu_bias", "tanh_bias"])
-@pytest.mark.parametrize("m,n", SIZES + [(300, 16384), (4000, 520)])
+@pytest.mark.parametrize("m,n", SIZES + [(300, 16384), (4000, 520), (1024, 1024), (20000, 8), (1025, 264), (1024, 1032)])
 def test_backward(m, n, epilogue, axis, recompute):
     dtype = "f16" if (m + n) % 3 == 0 else "bf16"
     dd, z = randn(m, n, seed=2, dtype=dtype), pre(m, n, dtype, seed=3)

@@ -41,7 +41,7 @@ def test_layer_norm(m, d, dtype, residual, out):
     ref.check_layer_norm(out, dtype, x, r, gamma, beta, EPS, Y, S, sc, amax)
 
 
-@pytest.mark.parametrize("m,d", [(5, 8), (3, 1000), (2, 4104), (3, 16376)])
+@pytest.mark.parametrize("m,d", [(5, 8), (3, 1000), (2, 4104), (3, 6144), (2, 6152), (3, 12288), (2, 12296), (3, 16376)])
 def test_lengths_that_are_no_multiple_of_16(m, d):
     x, gamma, beta, r = randn(m, d, seed=1), randn(d, seed=2), randn(d, seed=3), randn(m, d, seed=4)
     Y, S, _ = run_norm(x, r, gamma, beta, "bf16", "same")
@@ -146,7 +146,9 @@ def run_bwd(dy, s, gamma, ds, dtype, eps=EPS, want="gb", workspace=None, stream=
 # one cluster (a row on 8, 32, 128, 512 threads; one turn and two), few rows with partial sums, and every shape of many rows
 BWD = [(1, 8), (3, 64), (1000, 64), (1024, 56), (256, 256), (37, 1000), (64, 1024), (8, 4096), (16, 4096), (16, 2056),
        (1100, 64), (300, 256), (70, 1024), (17, 4096), (37, 2048), (3, 8192), (2, 16384),
-       (40000, 64), (20011, 128), (9001, 256), (5003, 512), (2001, 1024), (1203, 2048), (601, 4096), (333, 8192), (151, 8200), (150, 16384)]
+       (26, 5000), (3, 6144),
+       (40000, 64), (20011, 128), (20011, 104), (9001, 256), (5003, 512), (2001, 1024), (1203, 2048), (601, 4096), (600, 4008), (450, 5000), (400, 6144),
+       (333, 8192), (151, 8200), (150, 12288), (150, 16384)]
 
 
 @pytest.mark.parametrize("skip", [False, True])
