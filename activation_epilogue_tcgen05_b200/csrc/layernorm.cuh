@@ -243,9 +243,9 @@ __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR)
 
 // Rows quantised with one scale each, without a norm: x -> codes and max |x| / 448 (127).  Rows of up to TPR * VPT vectors
 // are held in registers; of longer ones (LONG) the rest is read again, from L2.  Three blocks of 512 threads an SM (8192 x 14336
-// to int8 58 us, 6.1 TB/s; two 64).
+// to int8 58 us, 6.1 TB/s; two 64), two where the rest is read again (2048 x 32768 36 us, one 50).
 template <int DT, int OUT, int TPR, int VPT, bool LONG>
-__global__ void __launch_bounds__(norm_threads(TPR), TPR >= 512 && !LONG ? 3 : 1) quant_rows_kernel(const NormParams p) {
+__global__ void __launch_bounds__(norm_threads(TPR), TPR >= 512 ? (LONG ? 2 : 3) : 1) quant_rows_kernel(const NormParams p) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR, NW = TPR > 32 ? TPR / 32 : 1;
     __shared__ float red[RPB][NW];
     const int grp = threadIdx.x / TPR, t = threadIdx.x % TPR;
