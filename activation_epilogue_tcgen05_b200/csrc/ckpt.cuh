@@ -7,12 +7,14 @@
 //     e the smallest exponent from 7 on with max |z| <= 127 * 2^(e - 133);
 // e = 255 stands for a group with a value that is not finite (or above 127 * 2^121): all of it is restored as NaN.
 // With a power of two the products are exact: the codes do not depend on how the quotient is taken, and a code times its step
-// is a bf16 number.  The step is between 1/64 and 1/127 of the largest magnitude, where bf16's is 1/128 to 1/256.
+// is a bf16 number.  The step is between 1/127 and 1/63.5 of the largest magnitude, where bf16's is between 1/256 and 1/128.
 //
 // save: H = act(z) (the next product's operand, optional), codes and exponents in one pass over z;
 // load: z, or act(z), in the 16-bit type again.  Bound by HBM.  A thread takes eight columns, four neighbours a group, so that a
 // group's maximum is two shuffles; the groups of all rows are dealt to the threads in one line, so that narrow and
 // ragged rows leave few of them idle; U groups a thread, all loads first.
+// Measured (a copy moves 6.55 TB/s): 8192 x 14336 bf16 GELU saved in 99 us, 6.0 TB/s (20 instructions an element, three quarters of
+// the issue slots), loaded in 52.6, 6.8 TB/s; 32768 x 128 5.2 and 3.2.
 #pragma once
 #include <cstdint>
 

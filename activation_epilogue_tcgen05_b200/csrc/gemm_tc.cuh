@@ -457,7 +457,9 @@ struct TcCfg {
     static constexpr bool B_MN = B_MN_;             // B stored (k, n): N contiguous
     static constexpr bool A_MN = A_MN_;             // A stored (k, m): M contiguous
     // 8-bit integers: the accumulators, partial tiles among them, are int32 and exact, and become fp32 in the epilogue,
-    // where each meets its row's and its column's scale
+    // where each meets its row's and its column's scale.  The mainloop is e4m3's, byte for byte; against its extended
+    // epilogue, us: 8192 x 4096 x 14336 306 and 329 (less power, a higher clock), 8192 x 4096 x 2048 with a residual 62.8 and
+    // 62.0, 8192 x 8192 x 1024 100 and 94: what the columns' scales and the conversion cost shows where k is short.
     static constexpr bool I8 = DT == DT_I8;
     static constexpr int ESIZE = dt_size(DT);
     static constexpr int KIND = dt_kind(DT);

@@ -17,6 +17,7 @@ cudaError_t ckpt(bool save, const CkptParams &p, bool pdl, cudaStream_t s) {
 }
 template <int DT, int EPI>
 cudaError_t ckpt(bool save, const CkptParams &p, bool pdl, cudaStream_t s) {
+    // four groups a thread, or one where that leaves SMs without a block (1023 x 4104 tanh, saved and loaded, 13.3 us by fours, 9.8)
     return p.total <= 148 * 8 * 2 * (CKPT_T / 4) ? ckpt<DT, EPI, 1>(save, p, pdl, s) : ckpt<DT, EPI, 4>(save, p, pdl, s);
 }
 template <int DT>
@@ -40,6 +41,7 @@ cudaError_t dact_ckpt(int axis, const DactParams &p, bool pdl, cudaStream_t s) {
             return launch_as(dact_narrow_kernel<DT, ACT, VAL>, attr_done3,
                              dim3((unsigned)std::min<int64_t>((p.m + DACT_WARPS - 1) / DACT_WARPS, 148 * dact_blocks(ACT, true))), T, SMEM,
                              pdl, s, p);
+        // two rows a block where four leave SMs with one block or none (1023 x 4104 GELU 6.2 us, by fours 9.6)
         if (p.m < 148 * 3 * DACT_U)
             return launch_as(dact_rows_kernel<DT, ACT, true, VAL, 2>, attr_done2, dim3((unsigned)((p.m + 1) / 2)), T, dact_smem(true, 2),
                              pdl, s, p);

@@ -546,7 +546,7 @@ int gemm_epi_quant_rows(int64_t m, int64_t d, int dtype, int out_mode, const voi
  * neighbouring columns of a row share a power of two:
  *     z ~ q 2^(e - 133),   q = round(z 2^(133 - e)) to nearest even, |q| <= 127,
  *     e the smallest from 7 on with max |z| <= 127 * 2^(e - 133)
- * (the blocks of the OCP Microscaling format MXINT8: int8 in units of 2^-6, a biased exponent byte).  The step is at most 1/64
+ * (the blocks of the OCP Microscaling format MXINT8: int8 in units of 2^-6, a biased exponent byte).  The step is at most 1/63.5
  * of the group's largest magnitude; values below 2^-127 become 0.  A group with an infinity, a NaN or a magnitude above
  * 127 * 2^121 has e = 255 and is restored as NaN throughout.
  *   m, n    sizes, 1 ... 2^31 - 1; n a multiple of 8 (ERR_ALIGN otherwise); m * gemm_epi_ckpt_groups(n) below 2^32 - 256
