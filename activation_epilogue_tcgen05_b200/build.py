@@ -9,6 +9,9 @@ the library needs only the NVIDIA driver at run time.  The driver API
 (tensor-map encoding) is reached through ``cudaGetDriverEntryPoint``; nothing
 links libcuda directly, so the library also loads on machines without a GPU
 (where every entry point that needs a device returns GEMM_EPI_ERR_NO_DEVICE).
+
+Beside it, ``binding/operands.cpp`` becomes ``_operands.so`` (g++, torch's headers): the Python binding's checks of operands,
+compiled.  Where that cannot be built the binding's own Python forms are used, and the build says so.
 """
 from __future__ import annotations
 
@@ -19,6 +22,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +30,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgemm_epi.so")
+
+OPERANDS = os.path.join(PKG, "binding", "operands.cpp")
+OPERANDS_SO = os.path.join(PKG, "_operands.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-Wall",
@@ -72,11 +79,44 @@ def source_hash() -> str:
     return h.hexdigest()
 
 
+def build_operands(force: bool = False, verbose: bool = False) -> bool:
+    """Compile (if stale) the binding's operand checks; whether they are there."""
+    import hashlib
+    import importlib.metadata
+    with open(OPERANDS, "rb") as f:
+        digest = hashlib.sha1(f.read() + f"{importlib.metadata.version('torch')} {sys.version}".encode()).hexdigest()
+    stamp = OPERANDS_SO + ".sha1"
+    if not force and os.path.exists(OPERANDS_SO) and os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read().strip() == digest:
+                return True
+    tmp = OPERANDS_SO + f".tmp{os.getpid()}"
+    import torch
+    at = os.path.dirname(torch.__file__)
+    include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+               os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", OPERANDS, "-o", tmp]
+    cmd += [a for i in include for a in ("-isystem", i)]
+    cmd += ["-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print(f"{os.path.basename(OPERANDS)} was not built; the binding checks its operands in Python:\n{r.stderr[-2000:]}", file=sys.stderr)
+        return False
+    os.replace(tmp, OPERANDS_SO)
+    with open(stamp, "w") as f:
+        f.write(digest + "\n")
+    return True
+
+
 def build(force: bool = False, jobs: int | None = None, verbose: bool = False) -> str:
-    """Compile (if stale) and link libgemm_epi.so; return its path.
+    """Compile (if stale) and link libgemm_epi.so, and the binding's operand checks; return the library's path.
 
     The library is current when its stamp file holds the hash of the present
     sources (copies that do not keep file times stay current)."""
+    build_operands(force, verbose)
     stamp = LIB + ".sha1"
     digest = source_hash()
     if not force and os.path.exists(LIB) and os.path.exists(stamp):
