@@ -147,7 +147,8 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_save_kernel(const CkptParams p) {
     }
 }
 
-// f16: a code's value may be above the type's largest number, to which save's z was rounded up in its step; it is drawn back.
+// f16: a code's value may be above the type's largest number, to which save's z was rounded up in its step; it is drawn back
+// (in groups whose 127 steps reach that far, and not where act does not).
 template <int DT, int EPI, int U>
 __global__ void __launch_bounds__(CKPT_T) ckpt_load_kernel(const CkptParams p) {
     ptx::griddep_wait();
@@ -171,7 +172,7 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_load_kernel(const CkptParams p) {
         f32x2 f[4];
         ckpt_decode8(q[u], ckpt_step(ex[u]), f);
         ckpt_act8<EPI>(f);
-        if constexpr (DT == DT_F16) {
+        if (DT == DT_F16 && EPI != EPI_TANH && ex[u] >= 143u) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float2 x = split(f[e]);
