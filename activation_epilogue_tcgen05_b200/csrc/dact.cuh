@@ -121,10 +121,10 @@ __device__ __forceinline__ void through_act(f32x2 (&d)[4], f32x2 (&z)[4], uint32
     }
 }
 
-// Sum of a lane's eight elements.
+// Sum of a lane's eight elements, neighbours first.
 __device__ __forceinline__ float sum8(const f32x2 (&d)[4]) {
-    const float2 f = split(add2(add2(d[0], d[1]), add2(d[2], d[3])));
-    return f.x + f.y;
+    const float2 a = split(d[0]), b = split(d[1]), c = split(d[2]), e = split(d[3]);
+    return ((a.x + a.y) + (b.x + b.y)) + ((c.x + c.y) + (e.x + e.y));
 }
 
 // With z to read, rows go through a ring of batches in shared memory, each thread copying its own vectors

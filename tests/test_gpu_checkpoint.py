@@ -197,3 +197,27 @@ def test_operands_are_checked():
         with pytest.raises(g.GemmEpiError) as e:
             plan.save(**{**dict(Z=z, codes=codes, exps=exps), **bad})
         assert e.value.status in (g.ERR_ARG, g.ERR_NULL)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("m", [1, 37, 5000])
+def test_order_of_a_rows_sum(m, dtype):
+    """dbias along rows adds eight neighbours as ((0+1)+(2+3)) + ((4+5)+(6+7)) in fp32, from a checkpoint as from D: the large
+    values of a row cancel, so that another order leaves other bits."""
+    d = randn(m, 8, seed=5, dtype=dtype) * 2.0 ** -12
+    d[:, 0], d[:, 4] = randn(m, seed=6, dtype=dtype) * 1024, randn(m, seed=7, dtype=dtype) * 64
+    d[:, 2], d[:, 6] = -d[:, 0], -d[:, 4]
+    f = d.float()
+    want = (((f[:, 0] + f[:, 1]) + (f[:, 2] + f[:, 3])) + ((f[:, 4] + f[:, 5]) + (f[:, 6] + f[:, 7]))).to(T16[dtype])
+    other = (((f[:, 0] + f[:, 2]) + (f[:, 1] + f[:, 3])) + ((f[:, 4] + f[:, 6]) + (f[:, 5] + f[:, 7]))).to(T16[dtype])
+    assert not torch.equal(want, other)
+    got = Guarded(m, T16[dtype])
+    g.ActBackward(m, 8, dtype, "bias", "row").run(d, dbias=got.t)
+    torch.cuda.synchronize()
+    assert got.intact() and torch.equal(got.t, want)
+    one = torch.ones_like(d)                                     # z > 0: ReLU's slope is 1
+    codes, exps, _ = save(one, dtype, "relu_bias")
+    got, dz = Guarded(m, T16[dtype]), Guarded(m * 8, T16[dtype])
+    g.ActBackward(m, 8, dtype, "relu_bias", "row").run_ckpt(d, codes, exps, dz.t.view(m, 8), dbias=got.t)
+    torch.cuda.synchronize()
+    assert got.intact() and dz.intact() and torch.equal(got.t, want) and torch.equal(dz.t.view(m, 8), d)
