@@ -87,6 +87,20 @@ __device__ __forceinline__ void ckpt_act8(f32x2 (&f)[4]) {
     }
 }
 
+// f16: the kept z of a value near the type's largest number is above it (65536: save's z was rounded up in its step), and so is act
+// of it but for tanh's; it is drawn back, in groups whose 127 steps reach that far.  NaN stays NaN.
+template <int DT>
+__device__ __forceinline__ void ckpt_draw_back8(f32x2 (&f)[4], uint32_t ex) {
+    if (DT == DT_F16 && ex >= 143u) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 x = split(f[e]);
+            f[e] = pair(x.x > 65504.0f ? 65504.0f : x.x < -65504.0f ? -65504.0f : x.x,
+                        x.y > 65504.0f ? 65504.0f : x.y < -65504.0f ? -65504.0f : x.y);
+        }
+    }
+}
+
 // Where a thread's groups lie: group `id` of all rows, and from it every CKPT_T / 4 further.
 struct CkptWalk {
     uint32_t id, row, g, drow, dg;
@@ -147,8 +161,6 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_save_kernel(const CkptParams p) {
     }
 }
 
-// f16: a code's value may be above the type's largest number, to which save's z was rounded up in its step; it is drawn back
-// (in groups whose 127 steps reach that far, and not where act does not).
 template <int DT, int EPI, int U>
 __global__ void __launch_bounds__(CKPT_T) ckpt_load_kernel(const CkptParams p) {
     ptx::griddep_wait();
@@ -172,14 +184,7 @@ __global__ void __launch_bounds__(CKPT_T) ckpt_load_kernel(const CkptParams p) {
         f32x2 f[4];
         ckpt_decode8(q[u], ckpt_step(ex[u]), f);
         ckpt_act8<EPI>(f);
-        if (DT == DT_F16 && EPI != EPI_TANH && ex[u] >= 143u) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 x = split(f[e]);
-                f[e] = pair(x.x > 65504.0f ? 65504.0f : x.x < -65504.0f ? -65504.0f : x.x,
-                            x.y > 65504.0f ? 65504.0f : x.y < -65504.0f ? -65504.0f : x.y);
-            }
-        }
+        if constexpr (EPI != EPI_TANH) ckpt_draw_back8<DT>(f, ex[u]);
         if (at[u] >= 0) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.h) + at[u]) = pack8<DT>(f);
     }
 }

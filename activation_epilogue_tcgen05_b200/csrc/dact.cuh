@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_blocks(ACT, CK)) dact_ke
                 unpack8<DT>(dv[u], d);
             }
             through_act<ACT, CK, VAL>(d, z, bits[u]);
+            if constexpr (VAL && ACT != DACT_TANH) ckpt_draw_back8<DT>(z, ex >> 8 * u & 255u);
             if (row_ok && col_ok) {
                 if constexpr (ACT != DACT_NONE) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + to) = pack8<DT>(d);
                 if constexpr (VAL) *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.h) + to) = pack8<DT>(z);
@@ -382,6 +383,7 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, U == DACT_U ? dact_blocks(ACT
                     unpack8<DT>(dv[u], d);
                 }
                 through_act<ACT, CK, VAL>(d, z, bits[u]);
+                if constexpr (VAL && ACT != DACT_TANH) ckpt_draw_back8<DT>(z, ex >> 8 * u & 255u);
                 if (u < rows) {
                     if constexpr (ACT != DACT_NONE) *reinterpret_cast<uint4 *>(dz + (int64_t)u * p.n + col) = pack8<DT>(d);
                     if constexpr (VAL) *reinterpret_cast<uint4 *>(hh + (int64_t)u * p.n + col) = pack8<DT>(z);
@@ -469,6 +471,7 @@ __global__ void __launch_bounds__(32 * DACT_WARPS, dact_blocks(ACT, true)) dact_
             unpack8<DT>(*Ring::dd(ring, stage, u), d);
             Ring::template values<DT>(ring, stage, u, cur >> 8 * u & 255u, z);
             through_act<ACT, true, VAL>(d, z, 0u);
+            if constexpr (VAL && ACT != DACT_TANH) ckpt_draw_back8<DT>(z, cur >> 8 * u & 255u);
             if (now.row < p.m && col < p.n) {
                 const int64_t at = now.row * p.n + col;
                 *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p.dz) + at) = pack8<DT>(d);

@@ -577,7 +577,8 @@ int gemm_epi_ckpt_load(int64_t m, int64_t n, int dtype, int epilogue, const int8
  *     dZ = dD * act'(z),   dbias = the sum of dZ along the bias's axis,   H = act(z)      z as kept
  *   epilogue  RELU, GELU or TANH, with or without bias (the others keep nothing of z, or the mask: ERR_ARG).  ReLU's slope is 1
  *           where the kept z is above 0: a z that rounded to 0 counts as 0.
- *   H       (m, n) in the 16-bit type, NULL: not wanted; may be dD, not dZ.
+ *   H       (m, n) in the 16-bit type, in f16 drawn back to its largest number as by gemm_epi_ckpt_load; NULL: not wanted; may
+ *           be dD, not dZ.
  * Everything else as for gemm_epi_dact (workspace: gemm_epi_dact_workspace_bytes). */
 int gemm_epi_dact_ckpt(int64_t m, int64_t n, int dtype, int epilogue, int bias_axis, const void *dD, const int8_t *codes,
                        const uint8_t *exps, void *dZ, void *H, void *dbias, void *workspace, void *stream);

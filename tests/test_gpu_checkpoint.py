@@ -221,3 +221,30 @@ def test_order_of_a_rows_sum(m, dtype):
     g.ActBackward(m, 8, dtype, "relu_bias", "row").run_ckpt(d, codes, exps, dz.t.view(m, 8), dbias=got.t)
     torch.cuda.synchronize()
     assert got.intact() and dz.intact() and torch.equal(got.t, want) and torch.equal(dz.t.view(m, 8), d)
+
+
+# ------------------------------------------------------------------ the ends of the range
+# one for each kernel and shape of the backward: columns, no bias, rows whole in a block (two and four rows), narrow rows by
+# warps, rows by strips
+ENDS = [("col", 37, 1000), (None, 37, 1000), ("row", 37, 1000), ("row", 1800, 1032), ("row", 1024, 1024), ("row", 3000, 96), ("row", 40, 6152)]
+
+
+@pytest.mark.parametrize("epilogue", ["relu_bias", "gelu_bias"])
+@pytest.mark.parametrize("axis,m,n", ENDS)
+def test_f16_values_beside_the_gradient_up_to_the_largest(axis, m, n, epilogue):
+    """A z near f16's largest number is kept as 65536 in steps of 1024: act(z) beside dZ is drawn back to a number, as load's is."""
+    z = pre(m, n, "f16", seed=8)
+    z[0, :4] = torch.tensor([65504.0, 65056.0, 64992.0, -65504.0])
+    z[m - 1, n - 1], z[m // 2, 40], z[m // 2, 41] = 65504.0, -65504.0, 65504.0
+    z[m // 3, 64:72] = float("inf")
+    codes, exps, _ = save(z, "f16", "none", H=False)
+    dd, dZ, H, X = randn(m, n, seed=9, dtype="f16"), torch.empty_like(z), torch.empty_like(z), torch.empty_like(z)
+    db = torch.empty(m if axis == "row" else n, dtype=torch.float16, device="cuda") if axis else None
+    g.ActBackward(m, n, "f16", epilogue, axis or "col").run_ckpt(dd, codes, exps, dZ, H=H, dbias=db)
+    g.ActCheckpoint(m, n, "f16", epilogue).load(codes, exps, X, act=True)
+    lost = (exps == 255).repeat_interleave(32, dim=1)[:, :n]
+    assert lost.any() and torch.equal(H.isnan(), lost) and torch.equal(X.isnan(), lost)
+    assert not H.isinf().any() and not X.isinf().any() and H[0, 0] == 65504 and H[m - 1, n - 1] == 65504 and H[m // 2, 41] == 65504
+    # (in the large groups every kept value is 0 or beyond 16, where both activations are max(z, 0) without a rounding)
+    large = (exps >= 143).repeat_interleave(32, dim=1)[:, :n] & ~lost
+    assert large.any() and torch.equal(H[large], X[large])
