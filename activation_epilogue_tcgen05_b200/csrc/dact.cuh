@@ -101,9 +101,16 @@ __device__ __forceinline__ f32x2 slope(f32x2 z, f32x2 *val = nullptr) {
     return tanh_slope(x.x, x.y);
 }
 
-// d *= act'(z) for a lane's eight elements (bits: their mask); VAL: z becomes act(z).
-template <int ACT, bool FINITE, bool VAL>
+// d *= act'(z) for a lane's eight elements (bits: their mask); VAL: z becomes act(z).  CK: z is finite or, in a group that save found
+// not to be, NaN throughout, and d becomes NaN with it: GELU's and tanh's slopes are NaN there, and ReLU's, a comparison,
+// takes the place of its 0 from the first element.
+template <int ACT, bool CK, bool VAL>
 __device__ __forceinline__ void through_act(f32x2 (&d)[4], f32x2 (&z)[4], uint32_t bits) {
+    float none = 0.0f;
+    if constexpr (CK && ACT == DACT_RELU) {
+        const float first = split(z[0]).x;
+        if (first != first) none = first;
+    }
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         if constexpr (ACT == DACT_RELU_MASK) {
@@ -111,11 +118,11 @@ __device__ __forceinline__ void through_act(f32x2 (&d)[4], f32x2 (&z)[4], uint32
             d[e] = pair(((bits >> 2 * e) & 1u) ? f.x : 0.0f, ((bits >> (2 * e + 1)) & 1u) ? f.y : 0.0f);
         } else if constexpr (ACT == DACT_RELU) {
             const float2 f = split(d[e]), x = split(z[e]);
-            d[e] = pair(x.x > 0.0f ? f.x : 0.0f, x.y > 0.0f ? f.y : 0.0f);
+            d[e] = pair(x.x > 0.0f ? f.x : none, x.y > 0.0f ? f.y : none);
             if constexpr (VAL) z[e] = pair(x.x < 0.0f ? 0.0f : x.x, x.y < 0.0f ? 0.0f : x.y);
         } else if constexpr (ACT != DACT_NONE) {
             f32x2 val;
-            d[e] = mul2(d[e], slope<ACT, FINITE>(z[e], VAL ? &val : nullptr));
+            d[e] = mul2(d[e], slope<ACT, CK>(z[e], VAL ? &val : nullptr));
             if constexpr (VAL) z[e] = val;
         }
     }

@@ -576,7 +576,8 @@ int gemm_epi_ckpt_load(int64_t m, int64_t n, int dtype, int epilogue, const int8
 /* gemm_epi_dact from a checkpoint in place of Z:
  *     dZ = dD * act'(z),   dbias = the sum of dZ along the bias's axis,   H = act(z)      z as kept
  *   epilogue  RELU, GELU or TANH, with or without bias (the others keep nothing of z, or the mask: ERR_ARG).  ReLU's slope is 1
- *           where the kept z is above 0: a z that rounded to 0 counts as 0.
+ *           where the kept z is above 0: a z that rounded to 0 counts as 0.  Where it is NaN (e = 255), dZ, H and the sums that dZ
+ *           goes into are NaN, whatever the activation.
  *   H       (m, n) in the 16-bit type, in f16 drawn back to its largest number as by gemm_epi_ckpt_load; NULL: not wanted; may
  *           be dD, not dZ.
  * Everything else as for gemm_epi_dact (workspace: gemm_epi_dact_workspace_bytes). */

@@ -248,3 +248,33 @@ def test_f16_values_beside_the_gradient_up_to_the_largest(axis, m, n, epilogue):
     # (in the large groups every kept value is 0 or beyond 16, where both activations are max(z, 0) without a rounding)
     large = (exps >= 143).repeat_interleave(32, dim=1)[:, :n] & ~lost
     assert large.any() and torch.equal(H[large], X[large])
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("epilogue", ["relu_bias", "gelu_bias", "tanh_bias"])
+@pytest.mark.parametrize("axis,m,n", ENDS)
+def test_a_group_that_is_not_finite_shows_in_the_gradient(axis, m, n, epilogue, dtype):
+    """dZ, act(z) and dbias are NaN where a group's z is lost, whatever the activation, and what they were elsewhere."""
+    z, dd = pre(m, n, dtype, seed=10), randn(m, n, seed=11, dtype=dtype)
+    plan = g.ActBackward(m, n, dtype, epilogue, axis or "col")
+
+    def run(z, recompute):
+        codes, exps, _ = save(z, dtype, "none", H=False)
+        dZ, H = torch.empty_like(z), torch.empty_like(z)
+        db = torch.empty(m if axis == "row" else n, dtype=T16[dtype], device="cuda") if axis else None
+        plan.run_ckpt(dd, codes, exps, dZ, H=H if recompute else None, dbias=db)
+        return dZ, H, db
+
+    want = run(z, True)
+    bad, lost = z.clone(), torch.zeros(m, n, dtype=torch.bool, device="cuda")
+    for i, j, v in ((0, 33, "inf"), (m // 2, n - 1, "-inf"), (m - 1, 0, "nan")) + (((m // 3, 70, "3.389e38"),) if dtype == "bf16" else ()):
+        bad[i, j] = float(v)
+        lost[i, j // 32 * 32: j // 32 * 32 + 32] = True
+    assert bad[m // 3, 70].isfinite()
+    for recompute in (True, False):
+        dZ, H, db = run(bad, recompute)
+        assert torch.equal(dZ.isnan(), lost) and torch.equal(dZ[~lost], want[0][~lost])
+        assert not recompute or (torch.equal(H.isnan(), lost) and torch.equal(H[~lost], want[1][~lost]))
+        if axis:
+            touched = lost.any(1 if axis == "row" else 0)
+            assert torch.equal(db.isnan(), touched) and torch.equal(db[~touched], want[2][~touched])
