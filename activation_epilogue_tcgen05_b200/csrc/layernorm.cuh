@@ -36,12 +36,6 @@ struct LnBwdParams : NormBwdParams {     // partial: [grid][dgamma, dbeta][d]
     void *dbeta;             // one cluster: dbeta itself, or NULL
 };
 
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
-
 __device__ __forceinline__ float halves(f32x2 v) {
     const float2 f = split(v);
     return f.x + f.y;

@@ -99,6 +99,12 @@ __device__ __forceinline__ float max_abs(float a, f32x2 v) {
     return r;
 }
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
 // Eight values times mul as 8-bit codes of the output type.  Integers (|v mul| within half of 127): 1.5 * 2^23 is added, which
 // leaves the nearest integer, ties to even, in the sum's low byte; one rounding, of the product.
 template <int OUT>
@@ -133,18 +139,24 @@ __device__ __forceinline__ float code_factor(float top) {
     return OUT == NORM_I8_ROWS ? __fdiv_ru(127.0f, top) : 448.0f / top;
 }
 
-// Sum of `a` and combination of `b` (maximum, or sum) over the TPR threads of a row, the same
+// How two parts of `b` below go together: their sum, the larger, the larger or NaN where there is one.
+enum : int { REDUCE_SUM = 0, REDUCE_MAX = 1, REDUCE_MAX_NAN = 2 };
+template <int OP>
+__device__ __forceinline__ float combine(float a, float b) {
+    return OP == REDUCE_MAX ? fmaxf(a, b) : OP == REDUCE_MAX_NAN ? max_nan(a, b) : a + b;
+}
+
+// Sum of `a` and combination of `b` over the TPR threads of a row, the same
 // bits in each of them.  Rows of up to 32 threads use an xor butterfly (every lane of the warp
 // takes part, with whatever row it has); longer ones add their warps' results in warp order, and wait
 // for their own TPR threads only (barrier 1 + grp) where a block of T threads has several rows.
-template <int TPR, int T, bool BMAX>
+template <int TPR, int T, int OP>
 __device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red, int grp) {
     constexpr int W = TPR < 32 ? TPR : 32;
 #pragma unroll
     for (int sh = W / 2; sh >= 1; sh >>= 1) {
         a += __shfl_xor_sync(0xffffffffu, a, sh);
-        const float o = __shfl_xor_sync(0xffffffffu, b, sh);
-        b = BMAX ? fmaxf(b, o) : b + o;
+        b = combine<OP>(b, __shfl_xor_sync(0xffffffffu, b, sh));
     }
     if constexpr (TPR > 32) {
         constexpr int NW = TPR / 32;
@@ -158,7 +170,7 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, float2 *red, int 
         for (int w = 1; w < NW; ++w) {
             t = red[w];
             a += t.x;
-            b = BMAX ? fmaxf(b, t.y) : b + t.y;
+            b = combine<OP>(b, t.y);
         }
     }
 }
@@ -196,6 +208,8 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
         if (v < nvec) gv[j] = __ldg(static_cast<const uint4 *>(p.gamma) + v);
     }
     float s[VPT][8];
+    // int8 codes have no NaN, so the row's scale has to show one: the maximum keeps it (e4m3 codes are NaN themselves)
+    constexpr int TOP = OUT == NORM_I8_ROWS ? REDUCE_MAX_NAN : REDUCE_MAX;
     float ss = 0.0f, top = 0.0f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
@@ -216,11 +230,11 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
             ss = fmaf(s[j][e], s[j][e], ss);
             if constexpr (OUT != NORM_SAME) {
                 s[j][e] *= g[e];
-                top = fmaxf(top, fabsf(s[j][e]));
+                top = combine<TOP>(top, fabsf(s[j][e]));
             }
         }
     }
-    row_reduce<TPR, norm_threads(TPR), true>(ss, top, red[grp], grp);
+    row_reduce<TPR, norm_threads(TPR), TOP>(ss, top, red[grp], grp);
     const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
     float mul = rho;
     if constexpr (OUT == NORM_E4M3) {
@@ -234,7 +248,7 @@ __global__ void __launch_bounds__(norm_threads(TPR)) rmsnorm_kernel(const NormPa
     } else if constexpr (norm_by_rows(OUT)) {
         // 448 / top overflows below 1.4e-36; such a row is one of zeros in 8 bits at any scale in use
         constexpr float C = norm_top_code(OUT);
-        const bool zero = !(top > 1e-35f);
+        const bool zero = OUT == NORM_I8_ROWS ? top <= 1e-35f : !(top > 1e-35f);
         mul = zero ? (OUT == NORM_I8_ROWS ? 0.0f : rho) : code_factor<OUT>(top);
         if (t == 0 && row_ok) p.scale[row] = zero ? 1.0f : rho * top * (1.0f / C);
     }
@@ -344,7 +358,7 @@ __global__ void __launch_bounds__(CLUSTER ? NORM_CLUSTER_T : norm_bwd_threads(TP
                 }
             }
         }
-        row_reduce<TPR, T, false>(ss, c, red[buf][grp], grp);
+        row_reduce<TPR, T, REDUCE_SUM>(ss, c, red[buf][grp], grp);
         const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
         const float k = rho * (rho * (c * p.inv_d));      // (rho^2 is beyond fp32 beside the smallest eps)
         uint16_t *out = static_cast<uint16_t *>(p.dx) + row * p.d;

@@ -458,7 +458,8 @@ enum gemm_epi_norm_out {
                                      is at most 1e-35 counts as one of zeros: scale 1, codes 0      */
     GEMM_EPI_NORM_I8_ROWS = 4     /* the same in 8-bit integers, for gemm_epi_run_scaled: round(y / d_scale[i]) to
                                      nearest even, d_scale[i] = max_j |y_ij| / 127 (3 is no mode).  A row with a
-                                     value that is not finite has a scale that is not, or NaN        */
+                                     value (a gain among them) that is not finite has a scale that
+                                     is not, or NaN                                                  */
 };
 
 /* Root-mean-square norm of the rows of a residual stream, the residual's addition before it:

@@ -263,3 +263,38 @@ def test_on_a_given_stream_and_captured():
     for _ in range(2):
         graph.replay()
         check()
+
+
+# ------------------------------------------------------------------ rows that are not finite, to 8-bit integers
+@pytest.mark.parametrize("norm", ["rms", "layer"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("d", [16, 64, 128, 1008, 4096, 16384])
+def test_a_row_that_is_not_finite_has_no_finite_scale(d, residual, norm):
+    """Its codes say nothing, so the scale has to: rows of NaN, a NaN among zeros, infinities, and every row beside a gain that is NaN."""
+    m = 11
+    x, gamma = randn(m, d, seed=1), randn(d, seed=2)
+    r = randn(m, d, seed=3) if residual else None
+    plan = (g.RmsNorm if norm == "rms" else g.LayerNorm)(m, d, out="i8_rows")
+
+    def run(x, gamma):
+        q, sc = torch.empty(m, d, dtype=torch.int8, device="cuda"), torch.empty(m, device="cuda")
+        plan.run(x, gamma, q, residual=r, scale=sc)
+        return q, sc
+
+    want, scales = run(x, gamma)
+    assert scales.isfinite().all()
+    bad = x.clone()
+    bad[0], bad[3] = float("nan"), 0
+    bad[3, d - 1], bad[6, d // 2], bad[8] = float("nan"), float("inf"), float("-inf")
+    if residual:
+        r[3] = 0
+    q, sc = run(bad, gamma)
+    keep = [1, 2, 4, 5, 7, 9, 10]
+    assert torch.equal(q[keep], want[keep]) and torch.equal(sc[keep], scales[keep]) and not sc[[0, 3, 6, 8]].isfinite().any()
+    odd = gamma.clone()
+    odd[d // 3] = float("nan")
+    assert not run(x, odd)[1].isfinite().any()
+    x[5] = 0
+    if residual:
+        r[5] = 0
+    assert not run(x, odd)[1].isfinite().any()
