@@ -16,6 +16,11 @@
 //     dx_j = ds_j + rho (a_j - mean a - u_j mean(a u))         (the gradient of x and of r alike)
 //     dg_j = sum_i dy_ij u_ij,  db_j = sum_i dy_ij
 // mu, rho, mean a and mean(a u) are taken in two reductions of two sums each; no statistic is kept by the forward pass.
+// A mean rounded to fp32 can be many deviations of a nearly constant row away.  The sum is not: 2^13 numbers of 11 bits and one
+// binade add up exactly in fp32's 24 (a row of more is added up as two), and if a sum is rounded, values that are far apart are
+// in it.  So mu is taken as two numbers, the nearest one, which is subtracted, and the rest of the sum over d by an fma, which joins the
+// scalars that follow and the fma that makes u.  (Putting mu right by the differences' sum, as the forward pass does, is a
+// third sum in the second reduction: 8192 x 4096 with the skip gradient 55.5 us, this 51.0, one rounded mu 49.3.)
 //
 // Both are bound by HBM and laid out as the root-mean-square norm's kernels.  Its arithmetic is near enough to show where little
 // is read: 18 instructions an element with a residual to e4m3, 13 without to 16 bits, in pairs (25 and 30 one by one).
@@ -69,9 +74,10 @@ __device__ __forceinline__ float row_sum(float a, float *red, int grp) {
 
 // The same of two values.  The warps of a long row share the work of the first exchange: their lower lanes go on with a, the
 // upper ones with b, which halves the shuffles (two sums of 256 threads cost 27 instructions, by two butterflies and a sum over
-// the warps for each 44; every thread has but 16 elements to do); red: a pair for each warp.
-template <int TPR, int T>
-__device__ __forceinline__ void row_sum2(float &a, float &b, f32x2 *red, int grp) {
+// the warps for each 44; every thread has but 16 elements to do); red: a pair for each warp.  TWO: a is the sum over the first
+// half of the warps and far that over the second.
+template <int TPR, int T, bool TWO = false>
+__device__ __forceinline__ void row_sum2(float &a, float &b, f32x2 *red, int grp, float *far = nullptr) {
     if constexpr (TPR <= 32) {
 #pragma unroll
         for (int sh = TPR / 2; sh >= 1; sh >>= 1) {
@@ -90,10 +96,18 @@ __device__ __forceinline__ void row_sum2(float &a, float &b, f32x2 *red, int grp
         const ulonglong2 *r = reinterpret_cast<const ulonglong2 *>(red);
         f32x2 s = add2(r[0].x, r[0].y);
 #pragma unroll
-        for (int w = 1; w < NW / 2; ++w) s = add2(s, add2(r[w].x, r[w].y));
+        for (int w = 1; w < (TWO ? NW / 4 : NW / 2); ++w) s = add2(s, add2(r[w].x, r[w].y));
         const float2 f = split(s);
         a = f.x;
         b = f.y;
+        if constexpr (TWO) {
+            s = add2(r[NW / 4].x, r[NW / 4].y);
+#pragma unroll
+            for (int w = NW / 4 + 1; w < NW / 2; ++w) s = add2(s, add2(r[w].x, r[w].y));
+            const float2 g = split(s);
+            *far = g.x;
+            b += g.y;
+        }
     }
 }
 
@@ -334,6 +348,12 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
 #pragma unroll
         for (int e = 0; e < 4; ++e) accg[j][e] = accb[j][e] = both(0.0f);
     }
+    // a row's values behind its sum, or behind the sums over either half of its warps
+    constexpr bool TWO = 8 * TPR * VPT > 8192;
+    int near = 0;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) near += 8 * (TWO ? min(max(nvec - j * TPR, 0), TPR / 2) : 0);
+    const float near_d = (float)(TWO ? near : 8 * nvec), far_d = (float)(8 * nvec - near);
     const int64_t step = (int64_t)gridDim.x * RPB;
     int64_t row0 = (int64_t)blockIdx.x * RPB;
 #pragma unroll
@@ -371,10 +391,11 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
                 }
             }
         }
-        float mu = halves(mu2), ma = halves(ma2);
-        row_sum2<TPR, T>(mu, ma, red1[grp], grp);
-        mu *= p.inv_d;
+        float sum = halves(mu2), far = 0.0f, ma = halves(ma2);
+        row_sum2<TPR, T, TWO>(sum, ma, red1[grp], grp, &far);
         ma *= p.inv_d;
+        const float mu = (sum + far) * p.inv_d;
+        const float rest = p.inv_d * (TWO ? fmaf(-mu, near_d, sum) + fmaf(-mu, far_d, far) : fmaf(-mu, near_d, sum));
         f32x2 ss2 = both(0.0f), as2 = both(0.0f);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -393,7 +414,8 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
         float ss = halves(ss2), as = halves(as2);
         row_sum2<TPR, T>(ss, as, red2[grp], grp);
         const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-        const float k = rho * (rho * (as * p.inv_d));     // (rho^2 is beyond fp32 beside the smallest eps)
+        const float k = rho * (rho * fmaf(as, p.inv_d, -rest * ma));     // (rho^2 is beyond fp32 beside the smallest eps)
+        const float shift = fmaf(k, rest, -ma), off = -rest * rho;
         uint16_t *out = static_cast<uint16_t *>(p.dx) + row * p.d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -408,8 +430,8 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
                     const f32x2 d = HOLD ? c[HOLD ? j : 0][e] : add2(sv[e], both(-mu));
                     const f32x2 g = HOLD ? a[HOLD ? j : 0][e] : av[e];
                     accb[j][e] = add2(accb[j][e], y[e]);
-                    accg[j][e] = fma2(mul2(y[e], both(rho)), d, accg[j][e]);
-                    o[e] = fma2(both(rho), fma2(d, both(-k), add2(g, both(-ma))), o[e]);
+                    accg[j][e] = fma2(y[e], fma2(d, both(rho), both(off)), accg[j][e]);
+                    o[e] = fma2(both(rho), fma2(d, both(-k), add2(g, both(shift))), o[e]);
                 }
                 *reinterpret_cast<uint4 *>(out + 8 * v) = pack8<DT>(o);
             }

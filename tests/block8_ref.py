@@ -136,3 +136,34 @@ def check_act(epilogue, dtype, z, H, own=None):
     y = act(epilogue, z)
     off = act_off(epilogue, z, 0.0) if own is None else own * z.abs()
     close(H, y, U[dtype] * (y.abs() + off) + TINY[dtype] + off, "H")
+
+
+def layer_norm_bwd_close(dtype, dy, s, gamma, eps):
+    """(dx, dgamma, dbeta, and what each may be off by before its rounding) from differences c = s - mean that keep their digits
+    whatever the mean.
+
+    A row's values are multiples of the smallest one's unit.  Where their magnitudes add up to at most 2^24 units their sum is exact in
+    fp32 (rows beyond 8192 are added up as two, neither more than 5/8 of the row).  Otherwise a value passes at most 32 roundings,
+    and the mean is off by D = 2^-19 mean |s|.  It is held in two numbers, the second one at most t = 2^-22 |mean| and off by 2^-22
+    of itself.  c is off by E = D + F32 |u / rho|, an eighth of it allowed for what is smaller still, and 2^-22 t; mean c^2 by F32 of
+    itself, by (D + t)^2 where t is left in it, so rho by r = 2 F32 + (D + t)^2 rho^2 of itself, its own roundings among it; mean a c by
+    A = F32 (mean |a c| + t mean |a|) + mean |a| E."""
+    dy, s, g = dy.double(), s.double(), gamma.double()
+    mean = lambda v: v.mean(1, keepdim=True)  # noqa: E731
+    unit = torch.where(s == 0, torch.inf, torch.exp2(torch.frexp(s)[1].double() - {"f16": 11, "bf16": 8}[dtype])).amin(1, keepdim=True)
+    exact = s.abs().sum(1, keepdim=True) * (0.625 if s.shape[1] > 8192 else 1.0) <= 2.0 ** 24 * unit
+    D = torch.where(exact, 0.0, 2.0 ** -19 * mean(s.abs()))
+    c = s - mean(s)
+    rho = 1 / torch.sqrt(mean(c * c) + eps)
+    u, a = c * rho, dy * g
+    ac = mean(a * c)
+    dx = rho * (a - mean(a) - rho * rho * c * ac)
+    t = 4 * E24 * mean(s).abs()
+    E = 1.125 * (D + F32 * c.abs()) + 4 * E24 * t
+    r = 2 * F32 + ((D + t) * rho) ** 2
+    A = 1.125 * F32 * mean((a * c).abs()) + F32 * t * mean(a.abs()) + mean(a.abs() * E)
+    most = (1 + r) ** 3
+    off = rho * ((r + F32) * (a.abs() + mean(a.abs())) + most * rho * rho * (E * (ac.abs() + A) + c.abs() * A)
+                 + (most - 1 + F32) * rho * rho * ((c.abs() + t) * ac.abs()))
+    og = F32 * (dy * u).abs().sum(0) + (dy.abs() * (rho * (1 + r) * E + r * u.abs() + F32 * t * rho)).sum(0)
+    return dx, (dy * u).sum(0), dy.sum(0), off, og, F32 * dy.abs().sum(0)

@@ -298,3 +298,20 @@ def test_a_row_that_is_not_finite_has_no_finite_scale(d, residual, norm):
     if residual:
         r[5] = 0
     assert not run(x, odd)[1].isfinite().any()
+
+
+# ------------------------------------------------------------------ the backward's mean
+@pytest.mark.parametrize("dtype,mean,spread", [("bf16", 1000.0, 0.0), ("f16", 30000.0, 0.0), ("f16", 1000.0, 0.5), ("bf16", 256.0, 2.0), ("f16", 0.0, 1.0)])
+@pytest.mark.parametrize("m,d", [(9, 40), (9, 200), (9, 1000), (9, 4000), (17, 4000), (1300, 56), (40000, 56), (20011, 104), (9001, 248), (5003, 504),
+                                 (2500, 1000), (1203, 2040), (601, 4040), (601, 4096), (400, 6200), (333, 8200), (180, 12400)])
+def test_bwd_means_far_from_the_deviations(m, d, dtype, mean, spread):
+    """Constant and nearly constant rows of a large mean, whose own rounding is not part of u (block8_ref.layer_norm_bwd_close).  Every
+    seventh row begins with an outlier."""
+    s = (randn(m, d, seed=5, dtype="bf16").float() * spread + mean).to(T16[dtype])
+    s[::7, 0] = mean / 2 + 3
+    dy, gamma = randn(m, d, seed=6, dtype=dtype), randn(d, seed=7, dtype=dtype)
+    dX, dg, db = run_bwd(dy, s, gamma, None, dtype)
+    dx, wg, wb, ox, og, ob = ref.layer_norm_bwd_close(dtype, dy.cpu(), s.cpu(), gamma.cpu(), EPS)
+    block_ref.close(dX, dx, block_ref.rounded(dx, dtype, ox), "dX")
+    block_ref.close(dg, wg, block_ref.rounded(wg, dtype, og), "dgamma")
+    block_ref.close(db, wb, block_ref.rounded(wb, dtype, ob), "dbeta")
