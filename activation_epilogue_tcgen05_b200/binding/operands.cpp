@@ -55,9 +55,20 @@ PyObject *device_and_stream(PyObject *, PyObject *stream) {
     return PyObject_CallOneArg(slow_stream, stream);
 }
 
+// Whether f is one of the two functions here, which would hand on to itself without end.
+bool compiled_form(PyObject *f) {
+    if (!PyCFunction_Check(f)) return false;
+    const PyCFunction c = PyCFunction_GetFunction(f);
+    return c == device_and_stream || c == reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(operand));
+}
+
 PyObject *set_python_forms(PyObject *, PyObject *args) {
     PyObject *a, *b;
     if (!PyArg_ParseTuple(args, "OO", &a, &b)) return nullptr;
+    if (!PyCallable_Check(a) || !PyCallable_Check(b) || compiled_form(a) || compiled_form(b)) {
+        PyErr_SetString(PyExc_TypeError, "set_python_forms: the Python forms of operand and device_and_stream");
+        return nullptr;
+    }
     Py_INCREF(a);
     Py_INCREF(b);
     Py_XSETREF(slow_operand, a);

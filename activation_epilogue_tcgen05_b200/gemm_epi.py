@@ -14,7 +14,6 @@ import ctypes
 import math
 import os
 import threading
-import types
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libgemm_epi.so")
@@ -621,18 +620,24 @@ def _device_and_stream(stream):
     return device, _current[1](device) if stream is None else getattr(stream, "cuda_stream", stream)
 
 
+_python_forms = _operand, _device_and_stream
+_install = threading.Lock()
+
+
 def _compiled_checks() -> bool:
     """Put the compiled forms of ``_operand`` and ``_device_and_stream`` (binding/operands.cpp) in their place, where
-    build.py has made them; they hand what is not in order to the forms here, and a call of six operands takes 2 us less."""
+    build.py has made them; they hand what is not in order to the forms here, and a call of six operands takes 2 us less.
+    Threads may make their first calls together."""
     global _operand, _device_and_stream
-    if not isinstance(_operand, types.FunctionType):
-        return True
-    try:
-        from . import _operands
-    except ImportError:
-        return False
-    _operands.set_python_forms(_operand, _device_and_stream)
-    _operand, _device_and_stream = _operands.operand, _operands.device_and_stream
+    with _install:
+        if _operand is not _python_forms[0]:
+            return True
+        try:
+            from . import _operands
+        except ImportError:
+            return False
+        _operands.set_python_forms(*_python_forms)
+        _operand, _device_and_stream = _operands.operand, _operands.device_and_stream
     return True
 
 
