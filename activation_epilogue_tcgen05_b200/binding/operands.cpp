@@ -34,8 +34,8 @@ PyObject *operand(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
     if (nargs == 6 && args[0] == Py_None && args[5] == Py_True) Py_RETURN_NONE;
     if ((nargs == 5 || nargs == 6) && args[0] != Py_None) {
         try {
-            if (fits(args[0], args[2], args[3], args[4]))
-                return PyLong_FromVoidPtr(const_cast<void *>(THPVariable_Unpack(args[0]).const_data_ptr()));
+            // (mutable: a call may write there, and a copy-on-write tensor gets memory of its own first)
+            if (fits(args[0], args[2], args[3], args[4])) return PyLong_FromVoidPtr(THPVariable_Unpack(args[0]).mutable_data_ptr());
         } catch (const std::exception &) {            // a tensor without memory of its own: the Python form's to say
         }
         PyErr_Clear();                                // (a size beyond 64 bits)
