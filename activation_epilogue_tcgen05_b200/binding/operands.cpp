@@ -14,6 +14,11 @@ namespace {
 
 PyObject *slow_operand = nullptr, *slow_stream = nullptr;
 
+bool have_python_forms() {
+    if (slow_operand == nullptr) PyErr_SetString(PyExc_RuntimeError, "_operands: set_python_forms comes first");
+    return slow_operand != nullptr;
+}
+
 // Whether obj is a tensor of this dtype, shape (a tuple) and device, contiguous.
 bool fits(PyObject *obj, PyObject *dtype, PyObject *shape, PyObject *device) {
     if (!THPVariable_Check(obj) || !THPDtype_Check(dtype) || !PyTuple_CheckExact(shape) || !PyLong_CheckExact(device)) return false;
@@ -40,7 +45,7 @@ PyObject *operand(PyObject *, PyObject *const *args, Py_ssize_t nargs) {
         }
         PyErr_Clear();                                // (a size beyond 64 bits)
     }
-    return PyObject_Vectorcall(slow_operand, args, (size_t)nargs, nullptr);
+    return have_python_forms() ? PyObject_Vectorcall(slow_operand, args, (size_t)nargs, nullptr) : nullptr;
 }
 
 // device_and_stream(stream): (current device, its current stream's handle) when stream is None.
@@ -52,7 +57,7 @@ PyObject *device_and_stream(PyObject *, PyObject *stream) {
         } catch (const std::exception &) {            // no device: as torch reports it
         }
     }
-    return PyObject_CallOneArg(slow_stream, stream);
+    return have_python_forms() ? PyObject_CallOneArg(slow_stream, stream) : nullptr;
 }
 
 // Whether f is one of the two functions here, which would hand on to itself without end.
@@ -85,4 +90,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_operands", nullptr, -1, methods, 
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__operands() { return PyModule_Create(&module); }
+// built_for: torch's version and Python's, which have to be the running ones before anything here is called (tensors are read by
+// the layout that torch's headers gave them).
+PyMODINIT_FUNC PyInit__operands() {
+    PyObject *m = PyModule_Create(&module);
+    if (m != nullptr && PyModule_AddStringConstant(m, "built_for", BUILT_FOR) != 0) Py_CLEAR(m);
+    return m;
+}

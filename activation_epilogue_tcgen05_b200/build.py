@@ -18,6 +18,7 @@ from __future__ import annotations
 import argparse
 import concurrent.futures as cf
 import glob
+import json
 import os
 import shutil
 import subprocess
@@ -96,7 +97,8 @@ def build_operands(force: bool = False, verbose: bool = False) -> bool:
     include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", OPERANDS, "-o", tmp]
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-DBUILT_FOR={json.dumps(f'{torch.__version__} {sys.version}')}",
+           OPERANDS, "-o", tmp]
     cmd += [a for i in include for a in ("-isystem", i)]
     cmd += ["-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:

@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import math
 import os
+import sys
 import threading
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -626,7 +627,7 @@ _install = threading.Lock()
 
 def _compiled_checks() -> bool:
     """Put the compiled forms of ``_operand`` and ``_device_and_stream`` (binding/operands.cpp) in their place, where
-    build.py has made them; they hand what is not in order to the forms here, and a call of six operands takes 2 us less.
+    build.py has made them for this torch and Python; they hand what is not in order to the forms here, and a call of six operands takes 2 us less.
     Threads may make their first calls together."""
     global _operand, _device_and_stream
     with _install:
@@ -635,6 +636,9 @@ def _compiled_checks() -> bool:
         try:
             from . import _operands
         except ImportError:
+            return False
+        import torch
+        if getattr(_operands, "built_for", None) != f"{torch.__version__} {sys.version}":
             return False
         _operands.set_python_forms(*_python_forms)
         _operand, _device_and_stream = _operands.operand, _operands.device_and_stream
