@@ -17,6 +17,7 @@ from __future__ import annotations
 
 import argparse
 import concurrent.futures as cf
+import contextlib
 import glob
 import json
 import os
@@ -80,36 +81,45 @@ def source_hash() -> str:
     return h.hexdigest()
 
 
-def build_operands(force: bool = False, verbose: bool = False) -> bool:
-    """Compile (if stale) the binding's operand checks; whether they are there."""
-    import hashlib
-    import importlib.metadata
-    with open(OPERANDS, "rb") as f:
-        digest = hashlib.sha1(f.read() + f"{importlib.metadata.version('torch')} {sys.version}".encode()).hexdigest()
-    stamp = OPERANDS_SO + ".sha1"
-    if not force and os.path.exists(OPERANDS_SO) and os.path.exists(stamp):
-        with open(stamp) as f:
-            if f.read().strip() == digest:
-                return True
-    tmp = OPERANDS_SO + f".tmp{os.getpid()}"
+def _compile_operands(out, verbose):
     import torch
     at = os.path.dirname(torch.__file__)
     include = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
                os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include"), sysconfig.get_paths()["include"]]
     cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", f"-DBUILT_FOR={json.dumps(f'{torch.__version__} {sys.version}')}",
-           OPERANDS, "-o", tmp]
+           OPERANDS, "-o", out]
     cmd += [a for i in include for a in ("-isystem", i)]
     cmd += ["-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
-        print(f"{os.path.basename(OPERANDS)} was not built; the binding checks its operands in Python:\n{r.stderr[-2000:]}", file=sys.stderr)
+        raise RuntimeError(r.stderr[-2000:])
+
+
+def build_operands(force: bool = False, verbose: bool = False) -> bool:
+    """Compile (if stale) the binding's operand checks; whether they are there.  Without torch, a C++ compiler or a folder to write
+    to they are not (nor is a stale module, then), which is no error."""
+    import hashlib
+    import importlib.metadata
+    stamp, tmp = OPERANDS_SO + ".sha1", OPERANDS_SO + f".tmp{os.getpid()}"
+    try:
+        with open(OPERANDS, "rb") as f:
+            digest = hashlib.sha1(f.read() + f"{importlib.metadata.version('torch')} {sys.version}".encode()).hexdigest()
+        if not force and os.path.exists(OPERANDS_SO) and os.path.exists(stamp):
+            with open(stamp) as f:
+                if f.read().strip() == digest:
+                    return True
+        _compile_operands(tmp, verbose)
+        os.replace(tmp, OPERANDS_SO)
+        with open(stamp, "w") as f:
+            f.write(digest + "\n")
+    except (ImportError, OSError, RuntimeError) as e:
+        print(f"{os.path.basename(OPERANDS)} was not built; the binding checks its operands in Python:\n{e}", file=sys.stderr)
+        with contextlib.suppress(OSError):
+            os.remove(OPERANDS_SO)
         return False
-    os.replace(tmp, OPERANDS_SO)
-    with open(stamp, "w") as f:
-        f.write(digest + "\n")
     return True
 
 
