@@ -138,7 +138,7 @@ __device__ __forceinline__ float sum8(const f32x2 (&d)[4]) {
 // (cp.async, as the norm's backward does): the next batch is on its way while the slopes of one are
 // worked out (8192 x 14336 GELU 114 us, loaded where it is used 134).  Without z there is little to work
 // out, and a batch is loaded into registers by four blocks an SM instead of three (bias alone 38.6 us,
-// through a ring 40.6; 1023 x 4104 from the mask 5.4 us against 7.0).
+// through a ring 40.6; 1023 x 4104 from the mask 5.4 us against 7.0; f16 along rows in strips from the mask spills 20 bytes a thread).
 constexpr int DACT_U = 4;                             // rows of a warp in a batch (CK: their exponents share a word)
 constexpr bool dact_reads_z(int act) { return act != DACT_NONE && act != DACT_RELU_MASK; }
 // Where a slope is computed, two rows of a batch are worked out at a time: with all four interleaved the constants no longer

@@ -17,7 +17,9 @@ cudaError_t ckpt(bool save, const CkptParams &p, bool pdl, cudaStream_t s) {
 }
 template <int DT, int EPI>
 cudaError_t ckpt(bool save, const CkptParams &p, bool pdl, cudaStream_t s) {
-    // four groups a thread, or one where that leaves SMs without a block (1023 x 4104 tanh, saved and loaded, 13.3 us by fours, 9.8)
+    // four groups a thread, or one where that leaves SMs without a block.  Saved and loaded as GELU's, bf16, by ones and by fours: 64 x 4096
+    // 3.2 and 4.4 us, 512 x 4096 5.5 and 6.1, 1023 x 4104 9.0 and 10.8 (f16 tanh 9.2 and 10.9), 32768 x 128 9.0 and 10.8, 1184 x 4096 10.3 and 11.2;
+    // beyond, 2048 x 4096 16.5 and 16.0, 1024 x 14336 27.0 and 25.3, 4096 x 4096 30.4 and 27.7, 8192 x 14336 206 and 177.
     return p.total <= 148 * 8 * 2 * (CKPT_T / 4) ? ckpt<DT, EPI, 1>(save, p, pdl, s) : ckpt<DT, EPI, 4>(save, p, pdl, s);
 }
 template <int DT>
@@ -41,7 +43,9 @@ cudaError_t dact_ckpt(int axis, const DactParams &p, bool pdl, cudaStream_t s) {
             return launch_as(dact_narrow_kernel<DT, ACT, VAL>, attr_done3,
                              dim3((unsigned)std::min<int64_t>((p.m + DACT_WARPS - 1) / DACT_WARPS, 148 * dact_blocks(ACT, true))), T, SMEM,
                              pdl, s, p);
-        // two rows a block where four leave SMs with one block or none (1023 x 4104 GELU 6.2 us, by fours 9.6)
+        // two rows a block where four leave SMs with one block or none.  GELU by twos and by fours: 64 x 4096 2.3 and 3.6 us, 300 x 4104 3.8 and
+        // 4.3, 1023 x 4104 6.4 and 6.6, 1500 x 4104 9.3 and 10.3 (1023 x 1024 3.1 and 2.9); fours are not faster beyond (2500 x 4104 14.2 and
+        // 16.1, 4096 x 4096 19.2 and 20.2): the limit is where they were thought to be.
         if (p.m < 148 * 3 * DACT_U)
             return launch_as(dact_rows_kernel<DT, ACT, true, VAL, 2>, attr_done2, dim3((unsigned)((p.m + 1) / 2)), T, dact_smem(true, 2),
                              pdl, s, p);

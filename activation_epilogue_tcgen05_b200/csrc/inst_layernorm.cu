@@ -64,7 +64,9 @@ cudaError_t quant_shape(const NormParams &p, bool pdl, cudaStream_t s) {
     return quant<DT, OUT, 512, 4, true>(p, pdl, s);
 }
 
-// Whether a backward call has few rows: the root-mean-square norm's rule.
+// Whether a backward call has few rows, one vector a thread: the root-mean-square norm's rule.  With the sums by partial rows, as few
+// and as many rows: 128 x 1024 3.9 us and 5.3, 300 x 256 3.5 and 5.0, 17 x 4096 5.3 and 5.9, 2000 x 64 3.6 and 5.4; near the rule's end
+// 1180 x 1024 7.6 and 7.9, 4700 x 256 6.6 and 7.5, but 290 x 4096 8.6 and 8.0, 600 x 1024 6.0 and 5.7.
 bool few_rows(int64_t m, int64_t d) { return m * (d / 8) <= 148 * 1024; }
 
 // The backward kernel's threads a row, vectors a thread and threads a block: one block an SM.
@@ -151,7 +153,10 @@ cudaError_t bwd(const LnBwdParams &p, bool pdl, cudaStream_t s) {
 
 int64_t ln_bwd_parts(int64_t m, int64_t d) {
     const BwdShape b = bwd_shape(m, d);
-    // one vector a thread and at most two turns of a cluster's rows: no partial rows
+    // One vector a thread and at most two turns of a cluster's rows: no partial rows, the root-mean-square norm's rule (it saves the
+    // host's second launch, and the scratch).  The cluster against partial rows in a graph, and as called from Python with
+    // scratch given: 37 x 1000 5.4 and 3.5 us, 5.8 and 7.4; 256 x 256 4.1 and 3.2, 4.7 and 7.4; 1000 x 64 3.9 and 3.3, 4.7 and 7.4;
+    // at 512 threads a row it loses both ways: 8 x 4096 7.4 and 5.1, 7.8 and 7.4; 16 x 4096 8.4 and 5.2, 8.8 and 7.3.
     if (b.vpt == 1 && m <= 2 * NORM_CLUSTER * (NORM_CLUSTER_T / b.tpr)) return 0;
     return bwd_blocks(m, b);
 }

@@ -22,10 +22,11 @@
 // scalars that follow and the fma that makes u.  (Putting mu right by the differences' sum, as the forward pass does, is a
 // third sum in the second reduction: 8192 x 4096 with the skip gradient 55.5 us, this 51.0, one rounded mu 49.3.)
 //
-// Both are bound by HBM and laid out as the root-mean-square norm's kernels.  Its arithmetic is near enough to show where little
-// is read: 18 instructions an element with a residual to e4m3, 13 without to 16 bits, in pairs (25 and 30 one by one).
-// Measured (a copy moves 6.55 TB/s): 8192 x 4096 bf16 with a residual to e4m3 by rows 37.7 us, 6.2 TB/s; 4096 x 8192 with a
-// residual to bf16 42.7 us, 6.3 TB/s; 8192 x 4096 without one to int8 26 us, 3.9 TB/s.
+// Both are laid out as the root-mean-square norm's kernels.  With a residual the forward is bound by HBM: 8192 x 4096 bf16 to e4m3 by
+// rows 37.8 us, 6.2 TB/s (a copy moves 6.55); 4096 x 8192 to bf16 42.7 us, 6.3 TB/s.  Without one neither HBM nor the
+// issue slots are full (8192 x 4096 to int8 25.4 us, 4.0 TB/s, with 63 % of the slots and 34 % of the warps; to bf16 25.6 us, 5.2 TB/s):
+// it is the chain of one row a block, load, sum, sum, maximum, store, with no next row on its way.  18 instructions an element with
+// a residual to e4m3, 13 without to 16 bits, in pairs (25 and 30 one by one).
 #pragma once
 #include <cstdint>
 
@@ -135,7 +136,8 @@ __device__ __forceinline__ float row_max(float a, float *red, int grp) {
 // FULL: rows of exactly 8 TPR VPT elements (the powers of two from 128 on), without a question at each vector whether it is there
 // and zeros where it is not: 8192 x 4096 bf16 + residual to e4m3 by rows 38.0 us, 39.4 with them.
 // Blocks an SM that the forward kernel is compiled for: 24 warps at 80 registers (the same case, not FULL, 39.4 us; left to itself
-// the compiler takes as many and orders them worse, 41.8; 28 and 32 warps spilled), and two blocks of the longest rows' 512 threads
+// the compiler takes as many and orders them worse, 41.8; 28 and 32 warps spilled in every form, 24 spill 16 to 36 bytes a thread in
+// the bf16 forms to 8 bits that are not FULL, of 64 to 256 threads a row), and two blocks of the longest rows' 512 threads
 // at 64, which take g and b only where they are used (4096 x 14336 bf16 61 us, by one block at a time 85; with residual
 // to e4m3 by rows 71 and 102).
 constexpr int ln_blocks(int threads) { return threads >= 512 ? 2 : 768 / threads; }
@@ -253,8 +255,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR)
 }
 
 // Rows quantised with one scale each, without a norm: x -> codes and max |x| / 448 (127).  Rows of up to TPR * VPT vectors
-// are held in registers; of longer ones (LONG) the rest is read again, from L2.  Three blocks of 512 threads an SM (8192 x 14336
-// to int8 58 us, 6.1 TB/s; two 64), two where the rest is read again (2048 x 32768 36 us, one 50).
+// are held in registers; of longer ones (LONG) the rest is read again, from L2.  Three blocks of 512 threads an SM (40 registers, of
+// which 24 to 28 bytes are spilled; 8192 x 14336 to int8 58 us, 6.1 TB/s; two 64), two where the rest is read again (2048 x 32768 36 us, one 50).
 template <int DT, int OUT, int TPR, int VPT, bool LONG>
 __global__ void __launch_bounds__(norm_threads(TPR), TPR >= 512 ? (LONG ? 2 : 3) : 1) quant_rows_kernel(const NormParams p) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR, NW = TPR > 32 ? TPR / 32 : 1;
@@ -303,11 +305,11 @@ __global__ void __launch_bounds__(norm_threads(TPR), TPR >= 512 ? (LONG ? 2 : 3)
 }
 
 // Backward: rows dealt and fetched as by rmsnorm_bwd_kernel.  A thread keeps the sums of both gradients of its
-// columns, so it has two vectors of a row where that kernel has four, and holds a and s - mu in registers through the two
-// reductions; with three or four vectors they are taken from the ring again.  What bounds it is the chain of a row's two
-// reductions, with two rows at a time on an SM: 8192 x 4096 with the skip gradient 44.7 us, 6.0 TB/s, and 4.5 for the second launch;
-// 4096 x 8192 (one row at a time) 59, 2340 x 14336 65 of 41 at a copy's rate.  (Three or four rows in the ring, 1024 threads of one
-// vector, four rows of 128 threads: none faster.)
+// columns, so it has two vectors of a row where that kernel has four, and holds a and s in registers through the two
+// reductions; with three or four vectors they are taken from the ring again (four vectors of 512 threads, FULL, spill 24 bytes in f16 and
+// 48 in bf16).  What bounds it is the chain of a row's two reductions, with two rows at a time on an SM: 8192 x 4096 with the
+// skip gradient 46.5 us, 5.8 TB/s, and 4.5 for the second launch; 4096 x 8192 (one row at a time) 58, 2340 x 14336 65 of 41 at a
+// copy's rate.  (Three or four rows in the ring, 1024 threads of one vector, four rows of 128 threads: none faster.)
 constexpr int ln_ring(bool cluster) { return cluster ? 4 : 2; }
 constexpr int ln_ring_bytes(int threads, int vpt, bool cluster) { return ln_ring(cluster) * 3 * threads * vpt * 16; }
 

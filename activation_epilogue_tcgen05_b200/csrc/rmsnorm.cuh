@@ -105,8 +105,8 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     return r;
 }
 
-// Eight values times mul as 8-bit codes of the output type.  Integers (|v mul| within half of 127): 1.5 * 2^23 is added, which
-// leaves the nearest integer, ties to even, in the sum's low byte; one rounding, of the product.
+// Eight values times mul as 8-bit codes of the output type.  Integers (|v mul| below 127.5): 1.5 * 2^23 is added, which
+// leaves the integer nearest to the product, ties to even, in the sum's low byte; the sum's is the only rounding.
 template <int OUT>
 __device__ __forceinline__ uint2 codes8(const f32x2 (&v)[4], float mul) {
     const f32x2 m = both(mul);
@@ -132,8 +132,10 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float mul) {
 }
 
 // What the values of a row whose largest magnitude is top are multiplied by.  127 / top is rounded up: half of the largest
-// value is a tie between 63 and 64 (the only one there is unless 127 divides top's digits, and then the quotient is exact), and
-// has to go to the even 64.
+// value is a tie between 63 and 64 and has to go to the even 64.  127 is a prime, so there are other ties only where it divides top's
+// digits: in bf16 127 / top is a power of two then, and every code of rows quantised alone is that of the exact quotient;
+// in f16 (top 3, 5 ... 15 times 127) a tie goes up, to an odd code half of the time.  A y in fp32 within 2^-16 of a tie may go to
+// either side of it.
 template <int OUT>
 __device__ __forceinline__ float code_factor(float top) {
     return OUT == NORM_I8_ROWS ? __fdiv_ru(127.0f, top) : 448.0f / top;

@@ -780,7 +780,7 @@ class QuantRows:
 
 class ActCheckpoint:
     """Checkpoints of an (m, n) pre-activation in 8 bits (gemm_epi_ckpt_save, gemm_epi_ckpt_load): ``codes`` (m, n) int8 and
-    ``exps`` (m, groups) uint8, ``groups`` of 32 columns each.  ``dtype`` and ``epilogue`` are the forward plan's.  The object
+    ``exps`` (m, groups) uint8, ``groups`` of 32 columns each.  ``dtype`` ("bf16" for an "i8" plan, whose z is) and ``epilogue`` are the forward plan's.  The object
     holds sizes only."""
 
     def __init__(self, m, n, dtype="bf16", epilogue="gelu_bias"):
@@ -810,7 +810,7 @@ class ActCheckpoint:
 
 class ActBackward:
     """Backward of a forward plan's epilogue (gemm_epi_dact, gemm_epi_dact_ckpt): dZ = dD * act'(z) and dbias, the names as
-    for :class:`Plan`.  The object holds sizes only."""
+    for :class:`Plan` (``dtype`` "bf16" for an "i8" plan, whose z is).  The object holds sizes only."""
 
     def __init__(self, m, n, dtype="bf16", epilogue="bias", bias_axis="row"):
         import torch

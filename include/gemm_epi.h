@@ -277,7 +277,8 @@ int gemm_epi_run_ext(gemm_epi_plan_t plan, const void *A, const void *B, const v
  *   d_scale_rows  s: DEVICE pointer to m floats, 4-byte aligned: one scale a row of A, as gemm_epi_quant_rows and the
  *           norms' GEMM_EPI_NORM_I8_ROWS write them.
  *   d_scale_cols  t: DEVICE pointer to n floats, 16-byte aligned: one scale a column of B (an output channel; for an
- *           nn.Linear weight, (n, k), what gemm_epi_quant_rows writes for its rows).
+ *           nn.Linear weight, (n, k), what gemm_epi_quant_rows writes for its rows).  A sum times t_j, and that times s_i, are fp32
+ *           numbers on the way and stay below the largest.
  *   bias, R, D  bf16; bias and aux as for gemm_epi_run, R as for gemm_epi_run_ext (NULL: none; may be D).
  * Plans: forward epilogues (NONE ... TANH), A stored (m, k), D in bf16, block_n 0, 128 or 256, and the kernel families of other
  * plans (GEMM_EPI_SK_GRID is not read); ERR_UNSUPPORTED otherwise.  The other run calls, gemm_epi_set_scales and
@@ -457,9 +458,10 @@ enum gemm_epi_norm_out {
                                      row, which the call writes.  A row whose largest |s_ij gamma_j|
                                      is at most 1e-35 counts as one of zeros: scale 1, codes 0      */
     GEMM_EPI_NORM_I8_ROWS = 4     /* the same in 8-bit integers, for gemm_epi_run_scaled: round(y / d_scale[i]) to
-                                     nearest even, d_scale[i] = max_j |y_ij| / 127 (3 is no mode).  A row with a
-                                     value (a gain among them) that is not finite has a scale that
-                                     is not, or NaN                                                  */
+                                     nearest even, d_scale[i] = max_j |y_ij| / 127 (3 is no mode).  The quotient is
+                                     taken in fp32: within 2^-14 of half way between two codes it may
+                                     go to either.  A row with a value (a gain among them) that is
+                                     not finite has a scale that is not, or NaN                      */
 };
 
 /* Root-mean-square norm of the rows of a residual stream, the residual's addition before it:
@@ -537,7 +539,8 @@ int gemm_epi_layernorm_bwd(int64_t m, int64_t d, int dtype, float eps, const voi
  *   dtype   GEMM_EPI_F16 or GEMM_EPI_BF16, the type of X (m, d).
  *   out_mode  GEMM_EPI_NORM_E4M3_ROWS or GEMM_EPI_NORM_I8_ROWS.
  *   Q       (m, d) codes, not X.    d_scale  DEVICE pointer to m floats, written: max_j |x_ij| / 448 or / 127; a row whose largest
- *           value is at most 1e-35 counts as one of zeros (scale 1, codes 0).
+ *           value is at most 1e-35 counts as one of zeros (scale 1, codes 0).  An int8 code is the nearest to 127 x_ij / max_j |x_ij|, ties
+ *           to even (in f16 a tie other than half of the largest value may go up).
  * One launch, nothing allocated.  Alignment and statuses as for gemm_epi_rmsnorm. */
 int gemm_epi_quant_rows(int64_t m, int64_t d, int dtype, int out_mode, const void *X, void *Q, float *d_scale, void *stream);
 
@@ -552,7 +555,7 @@ int gemm_epi_quant_rows(int64_t m, int64_t d, int dtype, int out_mode, const voi
  * 127 * 2^121 has e = 255 and is restored as NaN throughout.
  *   m, n    sizes, 1 ... 2^31 - 1; n a multiple of 8 (ERR_ALIGN otherwise); m * gemm_epi_ckpt_groups(n) below 2^32 - 256
  *           (ERR_UNSUPPORTED beyond).
- *   dtype   the forward plan's: F16 or BF16 (E4M3: the 16-bit arrays are bf16).
+ *   dtype   the forward plan's: F16 or BF16 (E4M3: the 16-bit arrays are bf16; an I8 plan's are, too: BF16).
  *   codes   (m, n) int8, dense, 16-byte aligned.
  *   exps    (m, gemm_epi_ckpt_groups(n)) bytes, dense: e of row i, columns 32 g ... 32 g + 31 (the last group of a row may be
  *           short).

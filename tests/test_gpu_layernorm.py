@@ -315,3 +315,29 @@ def test_bwd_means_far_from_the_deviations(m, d, dtype, mean, spread):
     block_ref.close(dX, dx, block_ref.rounded(dx, dtype, ox), "dX")
     block_ref.close(dg, wg, block_ref.rounded(wg, dtype, og), "dgamma")
     block_ref.close(db, wb, block_ref.rounded(wb, dtype, ob), "dbeta")
+
+
+# ------------------------------------------------------------------ codes at ties
+@pytest.mark.parametrize("dtype,bits", [("bf16", 8), ("f16", 11)])
+def test_int8_codes_are_the_nearest(dtype, bits):
+    """Every mantissa as a row's largest value, every mantissa beside it at nine sizes: the code is the one nearest to the exact quotient
+    127 v / top, and the even one at a tie but for f16's, where 127 divides top's digits (they may go up)."""
+    low = 2 ** (bits - 1)
+    digits = torch.arange(low, 2 * low, dtype=torch.int64)
+    top = digits[:, None]                                            # in units of 2^-8 below
+    v = torch.cat([digits << (8 - s) for s in range(9)])[None, :].expand(low, -1)
+    v = torch.where(v > top << 8, 0, v)                              # (256 v is what stands for a value v)
+    x = torch.cat([(top << 8), v, torch.zeros(low, 15, dtype=torch.int64)], 1).double() / 2 ** 12
+    x[1::2] *= -1
+    x16 = x.to(T16[dtype])
+    assert torch.equal(x16.double(), x)
+    q, sc = torch.empty(x.shape, dtype=torch.int8, device="cuda"), torch.empty(low, device="cuda")
+    g.QuantRows(low, x.shape[1], dtype).run(x16.cuda(), q, sc)
+    got = q.cpu().long()
+    got[1::2] *= -1
+    num, den = 127 * torch.cat([(top << 8), v, torch.zeros(low, 15, dtype=torch.int64)], 1), top << 8
+    floor, rest = num // den, num % den
+    tie = 2 * rest == den
+    want = torch.where(2 * rest < den, floor, torch.where(tie, floor + (floor & 1), floor + 1))
+    may_go_up = tie & (top % 127 == 0) & (dtype == "f16")
+    assert tie.any() and torch.equal(got[~may_go_up], want[~may_go_up]) and ((got == want) | (got == floor + 1))[may_go_up].all()
