@@ -18,9 +18,9 @@
 // mu, rho, mean a and mean(a u) are taken in two reductions of two sums each; no statistic is kept by the forward pass.
 // A mean rounded to fp32 can be many deviations of a nearly constant row away.  The sum is not: 2^13 numbers of 11 bits and one
 // binade add up exactly in fp32's 24 (a row of more is added up as two), and if a sum is rounded, values that are far apart are
-// in it.  So mu is taken as two numbers, the nearest one, which is subtracted, and the rest of the sum over d by an fma, which joins the
-// scalars that follow and the fma that makes u.  (Putting mu right by the differences' sum, as the forward pass does, is a
-// third sum in the second reduction: 8192 x 4096 with the skip gradient 55.5 us, this 51.0, one rounded mu 49.3.)
+// in it.  So mu is taken as two numbers, the nearest one, which is subtracted, and the rest of the sum over d by an fma, which joins
+// mean(a u) and the fma that makes u.  (Putting mu right by the differences' sum, as the forward pass does, is a third sum in
+// the second reduction: 8192 x 4096 with the skip gradient 55.5 us, this 50.3, one rounded mu 49.3.)
 //
 // Both are laid out as the root-mean-square norm's kernels.  With a residual the forward is bound by HBM: 8192 x 4096 bf16 to e4m3 by
 // rows 37.8 us, 6.2 TB/s (a copy moves 6.55); 4096 x 8192 to bf16 42.7 us, 6.3 TB/s.  Without one neither HBM nor the
@@ -306,10 +306,9 @@ __global__ void __launch_bounds__(norm_threads(TPR), TPR >= 512 ? (LONG ? 2 : 3)
 
 // Backward: rows dealt and fetched as by rmsnorm_bwd_kernel.  A thread keeps the sums of both gradients of its
 // columns, so it has two vectors of a row where that kernel has four, and holds a and s in registers through the two
-// reductions; with three or four vectors they are taken from the ring again (four vectors of 512 threads, FULL, spill 24 bytes in f16 and
-// 48 in bf16).  What bounds it is the chain of a row's two reductions, with two rows at a time on an SM: 8192 x 4096 with the
-// skip gradient 46.5 us, 5.8 TB/s, and 4.5 for the second launch; 4096 x 8192 (one row at a time) 58, 2340 x 14336 65 of 41 at a
-// copy's rate.  (Three or four rows in the ring, 1024 threads of one vector, four rows of 128 threads: none faster.)
+// reductions; with three or four vectors they are taken from the ring again.  What bounds it is the chain of a row's two
+// reductions, with two rows at a time on an SM: 8192 x 4096 with the skip gradient 45.8 us, 5.9 TB/s, and 4.5 for the second launch;
+// 4096 x 8192 (one row at a time) 57, 2340 x 14336 64 of 41 at a copy's rate.  (Three or four rows in the ring, 1024 threads of one vector, four rows of 128 threads: none faster.)
 constexpr int ln_ring(bool cluster) { return cluster ? 4 : 2; }
 constexpr int ln_ring_bytes(int threads, int vpt, bool cluster) { return ln_ring(cluster) * 3 * threads * vpt * 16; }
 
@@ -416,8 +415,7 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
         float ss = halves(ss2), as = halves(as2);
         row_sum2<TPR, T>(ss, as, red2[grp], grp);
         const float rho = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-        const float k = rho * (rho * fmaf(as, p.inv_d, -rest * ma));     // (rho^2 is beyond fp32 beside the smallest eps)
-        const float shift = fmaf(k, rest, -ma), off = -rest * rho;
+        const float ku = rho * fmaf(as, p.inv_d, -rest * ma), off = -rest * rho;      // mean(a u)
         uint16_t *out = static_cast<uint16_t *>(p.dx) + row * p.d;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
@@ -432,8 +430,9 @@ __global__ void __launch_bounds__(T, 1) layernorm_bwd_kernel(const LnBwdParams p
                     const f32x2 d = HOLD ? c[HOLD ? j : 0][e] : add2(sv[e], both(-mu));
                     const f32x2 g = HOLD ? a[HOLD ? j : 0][e] : av[e];
                     accb[j][e] = add2(accb[j][e], y[e]);
-                    accg[j][e] = fma2(y[e], fma2(d, both(rho), both(off)), accg[j][e]);
-                    o[e] = fma2(both(rho), fma2(d, both(-k), add2(g, both(shift))), o[e]);
+                    const f32x2 u = fma2(d, both(rho), both(off));
+                    accg[j][e] = fma2(y[e], u, accg[j][e]);
+                    o[e] = fma2(both(rho), fma2(u, both(-ku), add2(g, both(-ma))), o[e]);
                 }
                 *reinterpret_cast<uint4 *>(out + 8 * v) = pack8<DT>(o);
             }
