@@ -208,8 +208,8 @@ int choose(Plan *P) {
         // k = 14336, 28.3 vs 29.1 us at n = 14336, k = 4096; e4m3 7.5 vs 14.2 us); above, its
         // ring holds too few stages (m = 96: 17.5 vs 16.7 us).  Operands of 8 bits, bias and residual, split-K vs single CTAs:
         // at 4096 x 4096 6.9 vs 13.8 us with m = 64, 12.9 vs 14.1 with 72, 13.5 vs 13.1 with 128; n = 4096, k = 14336 14.5 vs 22.0,
-        // 29.5 vs 21.9 and 32.8 vs 21.7; n = 14336, k = 4096 22.1 vs 17.9 with 48 already, 24.7 vs 18.3 with 64 (int8; e4m3 within 4 %).  (The split-K kernel has no
-        // backward epilogue.)
+        // 29.5 vs 21.9 and 32.8 vs 21.7; n = 14336, k = 4096 22.1 vs 17.9 with 48 already, 24.7 vs 18.3 with 64 (int8; e4m3
+        // within 8 %).  (The split-K kernel has no backward epilogue.)
         const int64_t pair_tiles = ((m + 255) / 256) * ((n + 255) / 256);
         const int sms_auto = P->opts.max_ctas > 0 ? std::min(P->opts.max_ctas, P->num_sms) : P->num_sms;
         if (m <= 64 && P->kepi != EPI_DRELU && !P->a_km) kernel = GEMM_EPI_KERNEL_SPLITK;

@@ -256,7 +256,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), ln_blocks(norm_threads(TPR)
 
 // Rows quantised with one scale each, without a norm: x -> codes and max |x| / 448 (127).  Rows of up to TPR * VPT vectors
 // are held in registers; of longer ones (LONG) the rest is read again, from L2.  Three blocks of 512 threads an SM (40 registers, of
-// which 24 to 28 bytes are spilled; 8192 x 14336 to int8 58 us, 6.1 TB/s; two 64), two where the rest is read again (2048 x 32768 36 us, one 50).
+// which 24 to 28 bytes are spilled; 8192 x 14336 to int8 58 us, 6.1 TB/s; two 64), two where the rest is read again (2048 x 32768
+// 36 us, one 50).
 template <int DT, int OUT, int TPR, int VPT, bool LONG>
 __global__ void __launch_bounds__(norm_threads(TPR), TPR >= 512 ? (LONG ? 2 : 3) : 1) quant_rows_kernel(const NormParams p) {
     constexpr int T = norm_threads(TPR), RPB = T / TPR, NW = TPR > 32 ? TPR / 32 : 1;
@@ -308,7 +309,8 @@ __global__ void __launch_bounds__(norm_threads(TPR), TPR >= 512 ? (LONG ? 2 : 3)
 // columns, so it has two vectors of a row where that kernel has four, and holds a and s in registers through the two
 // reductions; with three or four vectors they are taken from the ring again.  What bounds it is the chain of a row's two
 // reductions, with two rows at a time on an SM: 8192 x 4096 with the skip gradient 45.8 us, 5.9 TB/s, and 4.5 for the second launch;
-// 4096 x 8192 (one row at a time) 57, 2340 x 14336 64 of 41 at a copy's rate.  (Three or four rows in the ring, 1024 threads of one vector, four rows of 128 threads: none faster.)
+// 4096 x 8192 (one row at a time) 57, 2340 x 14336 64 of 41 at a copy's rate.  (Three or four rows in the ring, 1024 threads of one
+// vector, four rows of 128 threads: none faster.)
 constexpr int ln_ring(bool cluster) { return cluster ? 4 : 2; }
 constexpr int ln_ring_bytes(int threads, int vpt, bool cluster) { return ln_ring(cluster) * 3 * threads * vpt * 16; }
 

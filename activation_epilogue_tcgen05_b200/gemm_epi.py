@@ -627,8 +627,8 @@ _install = threading.Lock()
 
 def _compiled_checks() -> bool:
     """Put the compiled forms of ``_operand`` and ``_device_and_stream`` (binding/operands.cpp) in their place, where
-    build.py has made them for this torch and Python; they hand what is not in order to the forms here, and a call of six operands takes 2 us less.
-    Threads may make their first calls together."""
+    build.py has made them for this torch and Python; they hand what is not in order to the forms here, and a call of six
+    operands takes 2 us less.  Threads may make their first calls together."""
     global _operand, _device_and_stream
     with _install:
         if _operand is not _python_forms[0]:
@@ -780,8 +780,8 @@ class QuantRows:
 
 class ActCheckpoint:
     """Checkpoints of an (m, n) pre-activation in 8 bits (gemm_epi_ckpt_save, gemm_epi_ckpt_load): ``codes`` (m, n) int8 and
-    ``exps`` (m, groups) uint8, ``groups`` of 32 columns each.  ``dtype`` ("bf16" for an "i8" plan, whose z is) and ``epilogue`` are the forward plan's.  The object
-    holds sizes only."""
+    ``exps`` (m, groups) uint8, ``groups`` of 32 columns each.  ``dtype`` ("bf16" for an "i8" plan, whose z is) and ``epilogue``
+    are the forward plan's.  The object holds sizes only."""
 
     def __init__(self, m, n, dtype="bf16", epilogue="gelu_bias"):
         import torch
